@@ -34,6 +34,30 @@ class PoolStats(C.Structure):
                 ("reclaimable_pages", sz), ("resident_bytes", sz), ("page_bytes", sz)]
 
 
+class Heads(C.Structure):
+    _fields_ = [("dtype", i32), ("n_heads", i32), ("n_kv_heads", i32), ("head_dim", i32)]
+
+
+class Rows(C.Structure):
+    _fields_ = [("ptr", vp), ("token_stride", C.c_longlong), ("head_stride", C.c_longlong)]
+
+
+class RotaryDesc(C.Structure):
+    _fields_ = [("cos_sin", vp), ("max_pos", i32), ("rot_dim", i32), ("interleaved", i32),
+                ("q_weight", vp), ("k_weight", vp), ("eps", C.c_float)]
+
+
+class KvDesc(C.Structure):
+    _fields_ = [("heads", Heads), ("page_tokens", i32), ("n_pages", i32),
+                ("page_stride", C.c_longlong), ("head_stride", C.c_longlong), ("token_stride", C.c_longlong)]
+
+
+class AttendDesc(C.Structure):
+    _fields_ = [("q", Rows), ("out", Rows), ("lse", vp), ("batch", i32), ("q_len", i32), ("scale", C.c_float),
+                ("table", vp), ("table_stride", i32), ("lens", vp), ("n_groups", i32), ("group_offsets", vp),
+                ("prefix_table", vp), ("prefix_stride", i32), ("prefix_lens", vp)]
+
+
 U8P3 = C.c_void_p * 3          # const uint8_t* const [3]
 U16P3 = C.c_void_p * 3         # const uint16_t* const [3]
 LUTP = (C.c_void_p * 4) * 3    # const uint16_t* const [3][4]
@@ -77,6 +101,14 @@ _SIGS = {
     "pw_debug_dequant": (i32, [vp, i32, i32, vp, vp]),
     "pw_debug_dequant_kernel": (i32, [vp, i32, i32, i32, vp, vp]),
     "pw_debug_page_address": (i32, [vp, i32, i32, i32, C.POINTER(C.c_uint64)]),
+    "pw_qk_norm_rope": (i32, [vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
+    "pw_kv_create": (i32, [vp, vp, vp, vp, C.POINTER(vp)]),
+    "pw_kv_destroy": (i32, [vp]),
+    "pw_kv_check_device": (i32, [vp, vp]),
+    "pw_kv_append": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]),
+    "pw_kv_attend_workspace_size": (i32, [vp, i32, i32, i32, C.POINTER(sz)]),
+    "pw_kv_attend": (i32, [vp, vp, vp, sz, vp]),
+    "pw_verify_draft": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
     "pw_testing_host_sim": (i32, [i32]),
     "pw_testing_complete_events": (i32, []),
     "pw_testing_wait_limit": (i32, [vp, C.c_longlong, i32]),

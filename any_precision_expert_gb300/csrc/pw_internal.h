@@ -25,6 +25,11 @@ constexpr int kErrBits = 3;          // a bitwidth word outside {3, 4, 5, 6, 16}
 constexpr int kErrOffsets = 4;       // slot offsets not monotone in [0, T*K], or a slot index out of range
 constexpr int kErrLayout = 5;        // a kernel's shared-memory window cannot hold its buffer layout
 constexpr int kErrCanary = 6;        // a workspace canary changed (a write past a scratch region)
+constexpr int kErrPosition = 7;     // a rotation position outside its table
+constexpr int kErrSlot = 8;         // a cache slot past the cache
+constexpr int kErrLength = 9;       // a sequence or prefix length, or a group offset, out of range
+constexpr int kErrPage = 10;        // a page table entry outside the cache
+constexpr int kErrToken = 11;       // a drafted token or draft count out of range
 
 #ifdef __CUDACC__
 #define PW_HD __host__ __device__
@@ -148,6 +153,11 @@ cudaError_t launch_prefill_dump(const DevLayer& L, int e, int m, __half* out, cu
 // parameters, the decode kernel classes it needs and the bytes of h scratch.
 pw_status ffn_call_args(pw_layer_t layer, const void* x_perm, const int32_t* offsets, int T, const float* y_perm,
                         DevLayer* dev, int* class_mask, size_t* h_bytes);
+// Whether the library runs in host-simulated mode (pw_testing_host_sim).
+bool host_sim();
+// A range of a hot-path call for profiling tools, when PW_NVTX=1.
+void range_push(const char* name);
+void range_pop();
 // Records a CUDA error for pw_last_cuda_error and returns PW_ERR_CUDA.
 pw_status record_cuda_error(cudaError_t e);
 

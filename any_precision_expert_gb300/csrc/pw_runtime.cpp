@@ -1572,6 +1572,16 @@ extern "C" pw_status pw_debug_page_address(pw_layer_t l, int e, int p, int vpage
 
 pw_status pw::record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+bool pw::host_sim() { return g_sim; }
+
+void pw::range_push(const char* name) {
+  if (NvtxRange::on()) nvtxRangePushA(name);
+}
+
+void pw::range_pop() {
+  if (NvtxRange::on()) nvtxRangePop();
+}
+
 pw_status pw::ffn_call_args(pw_layer_t l, const void* x_perm, const int32_t* offsets, int T, const float* y_perm,
                             DevLayer* dev, int* cmask, size_t* h_bytes) {
   PW_TRY(check_layer(l));

@@ -1,0 +1,73 @@
+// Declarations shared by the host entry points around the layer (pw_serve.cpp)
+// and their kernels: heads, the paged KV cache, attention, draft verification.
+#pragma once
+
+#include "pw_internal.h"
+
+namespace pw {
+
+constexpr int kMaxGroup = 128;       // query heads per key head
+constexpr int kMaxBatch = 4096;      // sequences, and prefix groups, of one attention call
+constexpr int kMaxQLen = 64;         // query tokens a sequence
+constexpr int kMaxDrafts = 64;       // drafted tokens a sequence
+
+// The paged cache as the kernels see it (strides in elements).
+struct KvView {
+  char* k;
+  char* v;
+  int* err;
+  int dtype, hq, hkv, d;
+  int page_shift;       // log2 of the tokens a page holds
+  int n_pages;
+  long long page_stride, head_stride, token_stride;
+};
+
+struct RopeParams {
+  const float* cos_sin;
+  const int* positions;
+  const void* qw;
+  const void* kw;
+  float eps;
+  int max_pos, rot, interleaved;
+  int T, hq, hk, hv;             // rows a token: queries, then keys, then values (0 = that side is left out)
+  pw_rows q, k, v, q_out, k_out;
+  int* err;
+  const int* slots;              // non-null: keys and values go to the cache
+  KvView kv;
+};
+
+struct AttendParams {
+  KvView kv;
+  pw_rows q, out;
+  float* lse;
+  int B, ql, G;                  // G query heads per key head
+  float scale;
+  const int* table;
+  int table_stride;
+  const int* lens;
+  int n_groups;
+  const int* group_offsets;
+  const int* prefix_table;
+  int prefix_stride;
+  const int* prefix_lens;
+};
+
+struct VerifyParams {
+  const float* p;
+  const float* q;
+  const int* tokens;
+  const int* n_draft;
+  const float* u;
+  const float* noise;
+  int B, K, V;
+  int* out;
+  int* accepted;
+  int* err;
+};
+
+cudaError_t launch_rope(const RopeParams& P, int dtype, int d, cudaStream_t s);
+size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups);
+cudaError_t launch_attend(const AttendParams& P, void* ws, cudaStream_t s);
+cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s);
+
+}  // namespace pw

@@ -527,6 +527,183 @@ pw_status pw_debug_dequant_kernel(pw_layer_t layer, int e, int m, int kernel, vo
 /* Debug: device address of virtual page `vpage` of expert e's plane p (p = 6: fp16 page), or 0. */
 pw_status pw_debug_page_address(pw_layer_t layer, int e, int p, int vpage, uint64_t* addr);
 
+/* ---------------------------------------------------------------------------
+ * Around the layer: heads, the paged KV cache, attention, draft verification
+ * ---------------------------------------------------------------------------
+ * The write-up lowers expert precision when the KV cache needs the memory
+ * ("核心洞察"); these calls are the cache's side of such a step.  The pages
+ * describe none of them: the definitions below are this library's.  A decode
+ * step of a model is then
+ *   pw_kv_append (norm and rotate q and k, write k and v into the cache)
+ *   -> pw_kv_attend -> the MoE layer (pw_moe_forward) ... -> pw_verify_draft.
+ *
+ * Heads are vectors of head_dim = 64 or 128 values of type fp16 or bf16;
+ * n_kv_heads divides n_heads, query head h reads key head
+ * h / (n_heads / n_kv_heads), and that quotient is at most 128.  Head rows
+ * come in with strides (in elements), so q, k and v may be slices of one
+ * projection: row (t, h) starts at ptr + t * token_stride + h * head_stride.
+ * Every row is contiguous and starts on a 16-byte boundary (ptr 16-byte
+ * aligned, strides multiples of 8; PW_ERR_INVALID_ARG otherwise).
+ *
+ * Device-side checks: an index out of range (a position, slot, length, page
+ * or token) is clamped or skipped as its call says, nothing outside the
+ * documented buffers is touched, and the call's device error word becomes
+ * nonzero (PW_ERR_DEVICE_CHECK at the next pw_kv_check_device).
+ */
+typedef enum { PW_F16 = 0, PW_BF16 = 1 } pw_dtype;
+
+typedef struct {
+  int dtype;        /* pw_dtype of every head row */
+  int n_heads;      /* query heads */
+  int n_kv_heads;   /* key / value heads, divides n_heads */
+  int head_dim;     /* 64 or 128 (PW_ERR_UNSUPPORTED otherwise) */
+} pw_heads;
+
+typedef struct {
+  void* ptr;                /* device; read only where the call reads */
+  long long token_stride;   /* elements */
+  long long head_stride;    /* elements */
+} pw_rows;
+
+/* Norm and rotation of query and key heads. */
+typedef struct {
+  const float* cos_sin;   /* device fp32 [max_pos][rot_dim], 16-byte aligned: rot_dim/2 cosines, then as many sines */
+  int max_pos;            /* rows of the table; a position outside [0, max_pos) is clamped and flagged */
+  int rot_dim;            /* leading values of a head that are rotated: 0..head_dim, a multiple of 16 */
+  int interleaved;        /* 0: value i turns with i + rot_dim/2; 1: value 2i with 2i + 1 */
+  const void* q_weight;   /* device [head_dim] of the heads' type, 16-byte aligned: RMS norm weight, NULL = no norm */
+  const void* k_weight;
+  float eps;              /* added to the mean of squares; >= 0 and finite */
+} pw_rotary;
+
+/*
+ * Per-head RMS norm and rotation of queries and keys in one pass.  For each
+ * head row x of token t (w = q_weight or k_weight):
+ *   n = w ? x * rsqrt(mean(x^2) + eps) * w : x           (all in fp32)
+ *   (a, b) = the pair i of n, c = cos_sin[p][i], s = cos_sin[p][rot_dim/2 + i],
+ *   out pair = (a c - b s, b c + a s),  p = positions[t],
+ * values past rot_dim keep n; one rounding to the output type at the end.
+ *   positions  device int32 [T] (ignored, may be NULL, when rot_dim is 0)
+ *   q, q_out   [T][n_heads] rows;  k, k_out  [T][n_kv_heads] rows; NULL pw_rows
+ *              pointers leave that side out.  An output may be its own input
+ *              (same pointer and strides); other overlap is not allowed.
+ *   err        device int32 or NULL: error word for clamped positions
+ * T in [0, 2^20].  No workspace.
+ */
+pw_status pw_qk_norm_rope(const pw_heads* heads, const pw_rotary* rot, const int32_t* positions, int T,
+                          const pw_rows* q, const pw_rows* k, const pw_rows* q_out, const pw_rows* k_out,
+                          int32_t* err, void* stream);
+
+/*
+ * A paged KV cache in caller memory (a torch tensor, or pages that lowered
+ * experts gave back).  The key row of token offset o in page p for head h
+ * starts at k + p * page_stride + h * head_stride + o * token_stride
+ * (elements); values likewise from v.  Both page layouts, [page][head][token]
+ * and [page][token][head], are such strides.
+ */
+typedef struct pw_kv_s* pw_kv_t;
+
+typedef struct {
+  pw_heads heads;
+  int page_tokens;          /* tokens a page holds: a power of two, 8..1024 */
+  int n_pages;              /* pages of the cache; n_pages * page_tokens < 2^31 */
+  long long page_stride, head_stride, token_stride;  /* elements, multiples of 8 */
+} pw_kv_desc;
+
+/*
+ * Handle on a cache (host memory only).  k and v: device, 16-byte aligned;
+ * err: device int32, zeroed by the caller, the handle's error word.  All three
+ * must outlive the handle.  The handle keeps no progress between calls: it may
+ * be used from several streams, one host thread at a time.
+ */
+pw_status pw_kv_create(const pw_kv_desc* desc, void* k, void* v, int32_t* err, pw_kv_t* out);
+pw_status pw_kv_destroy(pw_kv_t kv);
+/* Reads and clears the error word (synchronises the stream): PW_OK or PW_ERR_DEVICE_CHECK / PW_ERR_TIMEOUT. */
+pw_status pw_kv_check_device(pw_kv_t kv, void* stream);
+
+/*
+ * Append T tokens: keys (normed and rotated as pw_qk_norm_rope does, when rot
+ * is given) and values (copied bit for bit) go to cache slots, and the
+ * tokens' queries, when given, are normed and rotated into q_out in the same
+ * launch.
+ *   slots      device int32 [T]: page * page_tokens + offset; a negative slot
+ *              writes nothing (padding), one past the cache writes nothing
+ *              and is flagged.  Slots of one call are distinct.
+ *   positions  device int32 [T], as above; rot may be NULL (plain append)
+ *   k, v       [T][n_kv_heads] rows;  q, q_out  [T][n_heads] rows or both NULL
+ * T in [0, 2^20].
+ */
+pw_status pw_kv_append(pw_kv_t kv, const pw_rotary* rot, const int32_t* positions, const int32_t* slots, int T,
+                       const pw_rows* k, const pw_rows* v, const pw_rows* q, const pw_rows* q_out, void* stream);
+
+/*
+ * Attention of a decode batch over the cache.  The batch is cut into n_groups
+ * groups of consecutive sequences; the sequences of a group share a prefix,
+ * whose keys and values are read once for all of them.  Sequence b has q_len
+ * query tokens, rows b * q_len + j of q (j < q_len); they are its last q_len
+ * tokens, already appended: query j sees the whole prefix of its group and
+ * the positions 0 .. lens[b] - q_len + j of its own suffix.  With s = scale *
+ * (q . key) over what a query sees,
+ *   out = sum e^s value / sum e^s,   lse = ln(sum e^s)
+ * A query that sees nothing gets out = 0 and lse = -infinity.  Cache contents
+ * at and past a length are never used, whatever they hold (NaN included).
+ * Scores, the softmax and the sums are fp32; the weights e^s are rounded to
+ * the heads' type for the products with the values.
+ */
+typedef struct {
+  pw_rows q, out;                /* [batch * q_len][n_heads] rows */
+  float* lse;                    /* device fp32 [batch * q_len][n_heads], or NULL */
+  int batch;                     /* sequences, 0..4096 (PW_ERR_UNSUPPORTED above) */
+  int q_len;                     /* query tokens a sequence, 1..64 */
+  float scale;                   /* finite */
+  const int32_t* table;          /* device [batch][table_stride]: pages of each suffix, in order */
+  int table_stride;              /* >= 0 */
+  const int32_t* lens;           /* device [batch]: suffix lengths, the q_len new tokens included */
+  int n_groups;                  /* 0 (no prefix) or 1..4096 */
+  const int32_t* group_offsets;  /* device [n_groups + 1]: group g is sequences [o[g], o[g+1]); NULL when n_groups is 1 */
+  const int32_t* prefix_table;   /* device [n_groups][prefix_stride] */
+  int prefix_stride;             /* >= 0 */
+  const int32_t* prefix_lens;    /* device [n_groups] */
+} pw_attend_desc;
+
+/*
+ * Lengths are clamped to [0, stride * page_tokens], group offsets to ascending
+ * values in [0, batch], and a page outside [0, n_pages) reads as zeros; all
+ * three are flagged.  A sequence outside every group has no prefix.
+ * ws: device scratch of at least pw_kv_attend_workspace_size() bytes, 256-byte
+ * aligned, needing no initial contents (PW_ERR_OOM when ws_bytes is too
+ * small).  The result depends on the inputs alone: no atomics order it.
+ */
+pw_status pw_kv_attend_workspace_size(pw_kv_t kv, int batch, int q_len, int n_groups, size_t* bytes);
+pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling).  For sequence b with
+ * n = n_draft[b] drafts x_0 .. x_{n-1}, uniform numbers u and noise e (draws
+ * of the unit exponential distribution, > 0):
+ *   draft i is kept while every earlier one is and  u_i * q_i(x_i) < p_i(x_i);
+ *   a = number kept;  accepted[b] = a;
+ *   r = max(p_a - q_a, 0) if a < n, else max(p_a, 0); where r has no positive
+ *   entry, max(p_a, 0);
+ *   next = the index of the largest r / e, the lowest of equal ones
+ *   out[b] = x_0 .. x_{a-1}, next, -1, ..., -1.
+ * The largest r / e falls on each index with probability r / sum(r), so next
+ * is a draw from the residual distribution.  Products, differences and
+ * quotients are single fp32 operations rounded to nearest; an r or r / e that
+ * is not a number counts as 0.
+ *   target_p  device fp32 [B][K+1][V]     draft_p  device fp32 [B][K][V]
+ *   tokens    device int32 [B][K]         n_draft  device int32 [B]
+ *   u         device fp32 [B][K]          noise    device fp32 [B][V]
+ *   out       device int32 [B][K+1]       accepted device int32 [B]
+ *   err       device int32 or NULL: set when an n_draft is outside [0, K]
+ *             (clamped) or a token outside [0, V) (not kept)
+ * B in [0, 65535], K in [0, 64], V in [1, 2^24]; with K = 0 the arrays of drafts may be
+ * NULL (plain sampling from target_p).
+ */
+pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int32_t* tokens,
+                          const int32_t* n_draft, const float* u, const float* noise, int B, int K, int V,
+                          int32_t* out, int32_t* accepted, int32_t* err, void* stream);
+
 /*
  * Testing hook: host-simulated device (call before creating any pool).  The
  * pool buffer is then host memory, uploads are memcpy, events complete only
