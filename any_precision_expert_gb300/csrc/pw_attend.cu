@@ -2,106 +2,498 @@
 //
 // One pass over the keys with the running maximum m and sum l of the softmax:
 // o = sum e^(s - m) v and l = sum e^(s - m) are rescaled when m grows, and
-// partial (m, l, o) of disjoint key sets join exactly the same way.
+// partial (m, l, o) of disjoint key sets join exactly the same way, so the
+// keys of one row may be split among CTAs (pw_attend.cuh) and joined at the
+// end.  Exponents are taken in log2 units: e^s = 2^(s log2 e).
+//
+// attend_kernel streams keys and values once for up to 64 query rows: TMA
+// boxes of whole pages land in a ring of 64-token stages, four warps multiply
+// them with mma.sync.  With R rows a key head it does R products a key byte;
+// up to 64 of them the legacy tensor path keeps up with HBM, so the loads
+// bound it.
 #include <math_constants.h>
 
+#include "pw_attend.cuh"
 #include "pw_heads.cuh"
-#include "pw_serve.h"
+#include "pw_tc.cuh"
 
 namespace pw {
 
 namespace {
 
-constexpr int kSimpleWarps = 4;
+constexpr int kTile = 64;                  // keys a stage
+constexpr int kComputeWarps = 4;
+constexpr int kThreads = (kComputeWarps + 1) * 32;
+constexpr int kSegmentCost = 1;            // a segment's fixed cost, in key tiles
+// Weights are kept as 2^(s - max + kShift): fp16 weights down to 2^-(14 + kShift) of the largest stay normal numbers.
+constexpr float kShift = 6.f;
 
-// Length of a table row's sequence, clamped to what its pages can hold.
-__device__ __forceinline__ int clamp_len(int len, int stride, int page_shift, int* err) {
-  const int most = stride << page_shift;
-  if (len >= 0 && len <= most) return len;
-  atomicExch(err, kErrLength);
-  return len < 0 ? 0 : most;
+template <int D>
+struct Cfg {
+  static constexpr int HALF = kTile * 128;              // one 64-value column block of a tile, 128-byte rows
+  static constexpr int NH = D / 64;
+  static constexpr int STAGE = 2 * NH * HALF;           // keys, then values
+  static constexpr int STAGES = 98304 / STAGE;
+  static constexpr int JOIN = 2 * (D / 8) * 512;        // accumulators of two warps
+  static constexpr int JOIN_AT = STAGES * STAGE;
+  static constexpr int ML_AT = JOIN_AT + JOIN;          // (m, l) of two warps' rows
+  static constexpr int BAR_AT = ML_AT + 2 * 128;
+  static constexpr int SMEM = BAR_AT + 2 * 8 * STAGES + 16;
+};
+
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page,
+                                              uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(mbar)
+      : "memory");
 }
 
-// One CTA a (query token, head); its warps take every fourth key.
-template <typename E, int D>
-__global__ void __launch_bounds__(kSimpleWarps * 32) attend_simple_kernel(const AttendParams P) {
-  constexpr int PER = D / 32;
-  __shared__ float sm[kSimpleWarps], sl[kSimpleWarps], so[kSimpleWarps][D];
-  const int row = blockIdx.x, b = row / P.ql, j = row % P.ql, h = blockIdx.y, hk = h / P.G;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const KvView& kv = P.kv;
-  int g = -1, lo = P.group_offsets ? 0 : -1;
-  for (int i = 0; i <= P.n_groups && P.n_groups > 0; ++i) {  // bounds clamped to ascending values in [0, B]
-    const int raw = P.group_offsets ? P.group_offsets[i] : i ? P.B : 0, hi = min(max(raw, max(lo, 0)), P.B);
-    if (hi != raw) atomicExch(kv.err, kErrLength);
-    if (i > 0 && b >= lo && b < hi) g = i - 1;
-    lo = hi;
-  }
-  const int plen = g < 0 ? 0 : clamp_len(P.prefix_lens[g], P.prefix_stride, kv.page_shift, kv.err);
-  const int slen = clamp_len(P.lens[b], P.table_stride, kv.page_shift, kv.err);
-  const int vis = max(0, slen - P.ql + 1 + j);
-  float q[PER], o[PER], m = -CUDART_INF_F, l = 0.f;
-  const E* qp = static_cast<const E*>(P.q.ptr) + row * P.q.token_stride + h * P.q.head_stride;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    q[i] = (float)qp[lane * PER + i];
-    o[i] = 0.f;
-  }
-  for (int n = warp; n < plen + vis; n += kSimpleWarps) {
-    const int at = n < plen ? n : n - plen;
-    const int* tab = n < plen ? P.prefix_table + (size_t)g * P.prefix_stride : P.table + (size_t)b * P.table_stride;
-    const int page = tab[at >> kv.page_shift];
-    const bool in = page >= 0 && page < kv.n_pages;
-    if (!in && lane == 0) atomicExch(kv.err, kErrPage);
-    const size_t off = in ? page * kv.page_stride + hk * kv.head_stride +
-                                (at & ((1 << kv.page_shift) - 1)) * kv.token_stride
-                          : 0;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      s += in ? q[i] * (float)reinterpret_cast<const E*>(kv.k)[off + lane * PER + i] : 0.f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= P.scale;
-    const float mn = fmaxf(m, s), keep = m == -CUDART_INF_F ? 0.f : expf(m - mn), w = expf(s - mn);
-    l = l * keep + w;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      o[i] = o[i] * keep + (in ? w * (float)reinterpret_cast<const E*>(kv.v)[off + lane * PER + i] : 0.f);
-    m = mn;
-  }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) so[warp][lane * PER + i] = o[i];
-  __syncthreads();
-  float top = -CUDART_INF_F, sum = 0.f;
-  for (int w = 0; w < kSimpleWarps; ++w) top = fmaxf(top, sm[w]);
-  for (int w = 0; w < kSimpleWarps; ++w) sum += sl[w] > 0.f ? sl[w] * expf(sm[w] - top) : 0.f;
-  if (threadIdx.x < D) {
-    float v = 0.f;
-    for (int w = 0; w < kSimpleWarps; ++w) v += sl[w] > 0.f ? so[w][threadIdx.x] * expf(sm[w] - top) : 0.f;
-    static_cast<E*>(P.out.ptr)[row * P.out.token_stride + h * P.out.head_stride + threadIdx.x] =
-        (E)(sum > 0.f ? v / sum : 0.f);
-  }
-  if (threadIdx.x == 0 && P.lse) P.lse[(size_t)row * kv.hq + h] = sum > 0.f ? top + logf(sum) : -CUDART_INF_F;
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 template <typename E>
-cudaError_t launch_typed(const AttendParams& P, cudaStream_t s) {
-  const dim3 grid(P.B * P.ql, P.kv.hq);
-  if (P.kv.d == 128)
-    attend_simple_kernel<E, 128><<<grid, kSimpleWarps * 32, 0, s>>>(P);
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(E) == 2 && __is_same(E, __half))
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    attend_simple_kernel<E, 64><<<grid, kSimpleWarps * 32, 0, s>>>(P);
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
+
+// Which keys of a tile each of a thread's two fragment words may hold: words
+// whose key is at or past `n` (relative to the fragment's first key) become 0.
+__device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int n) {
+  return k + 1 < n ? w : k < n ? (w & 0xffffu) : 0u;
+}
+
+// MT row tiles of 16; the warps of a row tile share the stage's keys.
+template <typename E, int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    attend_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ KvMaps maps) {
+  using C = Cfg<D>;
+  constexpr int ROWS = 16 * MT, KS = kComputeWarps / MT, KPW = kTile / KS;
+  using Walk = AttendWalk<ROWS, kTile, kSegmentCost>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (base & 1023) {
+    if (tid == 0) atomicExch(P.kv.err, kErrLayout);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kComputeWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Walk walk;
+  walk.start(P, W, reinterpret_cast<unsigned*>(smem));  // scratch: the ring, before any load
+  fence_proxy_async_smem();
+  __syncthreads();
+  typename Walk::Piece pc;
+  int stage = 0, phase = 0;
+
+  if (warp == kComputeWarps) {
+    // ---- producer: one lane a page ----
+    const int shift = P.kv.page_shift;
+    const int box = min(1 << shift, kBoxTokens);
+    while (walk.next(P, pc)) {
+      for (int t = pc.tile0; t < pc.tile1; ++t) {
+        const int keys = min(kTile, pc.it.len - t * kTile), boxes = (keys + box - 1) / box;
+        const int at = t * kTile + lane * box;
+        int page = 0;
+        if (lane < boxes) {
+          page = pc.it.table[at >> shift];
+          if (page < 0 || page >= P.kv.n_pages) atomicExch(P.kv.err, kErrPage);  // reads as zeros
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, abort_flag, P.kv.err))) goto stopped;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(boxes * box * D * 4));
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t dst = base + stage * C::STAGE + lane * box * 128;
+          const int tok = at & ((1 << shift) - 1);
+#pragma unroll
+          for (int h = 0; h < C::NH; ++h) {
+            tma_load_page(dst + h * C::HALF, &maps.k, 64 * h, tok, pc.head, page, full + 8 * stage);
+            tma_load_page(dst + (C::NH + h) * C::HALF, &maps.v, 64 * h, tok, pc.head, page, full + 8 * stage);
+          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+    }
+    return;
+  stopped:
+    // a wait gave up: let the copies in flight land before the shared memory goes away
+    for (int i = 0; i < C::STAGES; ++i)
+      for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
+      }
+    return;
+  }
+
+  // ---- compute warps ----
+  const int g = lane >> 2, t4 = lane & 3;
+  const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
+  const float scale2 = P.scale * 1.4426950408889634f;
+  // ldmatrix row addresses inside a 128-byte-row block: lane l supplies row l % 8 of matrix l / 8
+  const int mrow = lane & 7, msel = lane >> 3;
+  while (walk.next(P, pc)) {
+    const int ra = pc.row0 + mt * 16 + g;
+    uint32_t qf[D / 16][4];
+    int vis[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = ra + 8 * i;
+      const bool in = r < pc.it.nrows;
+      const int tok = in ? r / P.G : 0, hd = in ? pc.head * P.G + r - tok * P.G : 0;
+      const E* src = static_cast<const E*>(P.q.ptr) + (pc.it.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride;
+      vis[i] = pc.it.causal && in ? pc.it.len - P.ql + 1 + tok : pc.it.len;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        qf[s][i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4) : 0u;
+        qf[s][2 + i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4) : 0u;
+      }
+    }
+    const int sure = pc.it.causal ? pc.it.len - P.ql + 1 : pc.it.len;  // keys below this are seen by every row
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int t = pc.tile0; t < pc.tile1; ++t) {
+      // a wait that gives up leaves the sums as they are; the walk goes on, so that every barrier is met
+      const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
+      const int first = t * kTile + k0;  // this warp's first key
+      if (landed && first < pc.it.len) {
+        const uint32_t kb = base + stage * C::STAGE, vb = kb + C::NH * C::HALF;
+        float s[KPW / 8][4];
+#pragma unroll
+        for (int n = 0; n < KPW / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        // matrices of a load: keys 0-7 / 8-15 (msel >> 1), values 0-7 / 8-15 (msel & 1)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+#pragma unroll
+          for (int n = 0; n < KPW / 16; ++n) {
+            const int row = k0 + 16 * n + 8 * (msel >> 1) + mrow, chunk = (2 * c + (msel & 1)) & 7;
+            uint32_t b[4];
+            ldsm4(kb + (c / 4) * C::HALF + row * 128 + ((chunk ^ mrow) << 4), b);
+            mma16816<E>(s[2 * n], qf[c], b[0], b[1]);
+            mma16816<E>(s[2 * n + 1], qf[c], b[2], b[3]);
+          }
+        }
+        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        const bool edge = first + KPW > sure;
+#pragma unroll
+        for (int n = 0; n < KPW / 8; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] *= scale2;
+            if (edge && first + 8 * n + 2 * t4 + (i & 1) >= vis[i >> 1]) s[n][i] = -CUDART_INF_F;
+            top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+          }
+        }
+        float ref[2];
+        bool grew = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          top[i] = fmaxf(top[i] - kShift, m[i]);
+          ref[i] = top[i] == -CUDART_INF_F ? 0.f : top[i];
+          grew |= top[i] > m[i];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f[i] = ex2(m[i] - ref[i]);  // 0 while m is -inf
+            l[i] *= f[i];
+            m[i] = top[i];
+          }
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][0] *= f[0], o[d][1] *= f[0];
+            o[d][2] *= f[1], o[d][3] *= f[1];
+          }
+        }
+        uint32_t pf[KPW / 16][4];
+#pragma unroll
+        for (int n = 0; n < KPW / 8; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] = ex2(s[n][i] - ref[i >> 1]);
+            l[i >> 1] += s[n][i];
+          }
+          pf[n / 2][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
+          pf[n / 2][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
+        }
+        const bool tail = first + KPW > pc.it.len;  // values past the length may be anything: 0 instead
+#pragma unroll
+        for (int n = 0; n < KPW / 16; ++n) {
+          const int left = pc.it.len - first - 16 * n;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            // matrices: keys 0-7 / 8-15 (msel & 1), values 0-7 / 8-15 (msel >> 1)
+            const int row = k0 + 16 * n + 8 * (msel & 1) + mrow, chunk = (2 * d + (msel >> 1)) & 7;
+            uint32_t b[4];
+            ldsm4t(vb + (d / 4) * C::HALF + row * 128 + ((chunk ^ mrow) << 4), b);
+            if (tail) {
+              b[0] = keep_keys(b[0], 2 * t4, left), b[1] = keep_keys(b[1], 2 * t4 + 8, left);
+              b[2] = keep_keys(b[2], 2 * t4, left), b[3] = keep_keys(b[3], 2 * t4 + 8, left);
+            }
+            mma16816<E>(o[2 * d], pf[n], b[0], b[1]);
+            mma16816<E>(o[2 * d + 1], pf[n], b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    }
+
+    // ---- join the warps of a row tile: the upper half hands its sums to the lower one, in halving steps ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+#pragma unroll
+    for (int step = KS / 2; step > 0; step >>= 1) {
+      compute_sync();  // the buffer is free
+      if (ks >= step && ks < 2 * step) {
+        const int slot = (ks - step) * MT + mt;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16) =
+              make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+        if (t4 == 0)
+          *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 128 + g * 16) = make_float4(m[0], l[0], m[1], l[1]);
+      }
+      compute_sync();
+      if (ks < step) {
+        const int slot = ks * MT + mt;
+        const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 128 + g * 16);
+        const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
+        float fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mm = fmaxf(m[i], ym[i]), rr = mm == -CUDART_INF_F ? 0.f : mm;
+          fa[i] = ex2(m[i] - rr);
+          fb[i] = ex2(ym[i] - rr);
+          l[i] = l[i] * fa[i] + yl[i] * fb[i];
+          m[i] = mm;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16);
+          o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
+          o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
+          o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
+          o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
+        }
+      }
+    }
+    if (ks == 0) {
+      const AttendPieces& to = pc.prefix ? W.prefix : W.suffix;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = ra + 8 * i;
+        if (r >= pc.it.nrows) continue;
+        float* dst;
+        if (pc.first) {
+          const int tok = r / P.G;
+          const long long row = (long long)(pc.it.tok0 + tok) * P.kv.hq + pc.head * P.G + r - tok * P.G;
+          dst = to.row_o + row * D;
+          if (t4 == 0)
+            to.row_ml[row] = make_float4(m[i], l[i], __int_as_float((int)blockIdx.x), __int_as_float(pc.last_cta));
+        } else {
+          const int row = blockIdx.x * ROWS + mt * 16 + g + 8 * i;
+          dst = to.cta_o + (long long)row * D;
+          if (t4 == 0) to.cta_ml[row] = make_float2(m[i], l[i]);
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float2*>(dst + 8 * d + 2 * t4) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+      }
+    }
+  }
+}
+
+// Joins a row's pieces: one warp a (query token, head).
+template <typename E, int D>
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const AttendWork W, int prefix_rows,
+                                                   int suffix_rows) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (long long)P.B * P.ql * P.kv.hq) return;
+  const int n = (int)(row / P.kv.hq), h = (int)(row % P.kv.hq), b = n / P.ql;
+  // the group of the sequence
+  int grp = -1, tok0 = 0;
+  for (int i = 0; i < P.n_groups && grp < 0; i += 32) {
+    const int gi = i + lane;
+    int lo = 0, hi = 0;
+    if (gi < P.n_groups) {
+      lo = P.group_offsets ? min(max(P.group_offsets[gi], 0), P.B) : 0;
+      hi = P.group_offsets ? min(max(P.group_offsets[gi + 1], lo), P.B) : P.B;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, b >= lo && b < hi);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      grp = i + src;
+      tok0 = __shfl_sync(0xffffffffu, lo, src) * P.ql;
+    }
+  }
+  float m = -CUDART_INF_F, l = 0.f, o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  auto add = [&](float pm, float pl, const float* src) {
+    const float mm = fmaxf(m, pm), rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), fb = ex2(pm - rr);
+    m = mm;
+    l = l * fa + pl * fb;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = o[i] * fa + src[lane * PER + i] * fb;
+  };
+  auto pieces = [&](const AttendPieces& from, int rows, int local) {
+    const float4 a = from.row_ml[row];
+    add(a.x, a.y, from.row_o + row * D);
+    const int c1 = __float_as_int(a.w);
+    for (int c = __float_as_int(a.z) + 1; c <= c1; ++c) {
+      const long long at = (long long)c * rows + local;
+      const float2 y = from.cta_ml[at];
+      add(y.x, y.y, from.cta_o + at * D);
+    }
+  };
+  const int hl = h % P.G;
+  if (grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0)
+    pieces(W.prefix, prefix_rows, ((n - tok0) * P.G + hl) % prefix_rows);
+  if (min(P.lens[b], P.table_stride << P.kv.page_shift) > 0)
+    pieces(W.suffix, suffix_rows, ((n - b * P.ql) * P.G + hl) % suffix_rows);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + lane * PER;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2) *reinterpret_cast<uint32_t*>(out + i) = pack2<E>(o[i] * inv, o[i + 1] * inv);
+  if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int stream_ctas() { return 2 * sm_count(); }
+
+struct Layout {
+  size_t row_o[2], row_ml[2], cta_o, cta_ml, total;
+  Layout(int hq, int d, int B, int ql) {
+    const size_t rows = (size_t)B * ql * hq, most = (size_t)stream_ctas() * 64;
+    size_t at = 0;
+    for (int i = 0; i < 2; ++i) {
+      row_o[i] = at;
+      at += up256(rows * d * 4);
+      row_ml[i] = at;
+      at += up256(rows * 16);
+    }
+    cta_o = at;
+    at += up256(most * d * 4);
+    cta_ml = at;
+    at += up256(most * 8);
+    total = at;
+  }
+};
+
+template <typename E, int D, int MT>
+cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMaps& maps, cudaStream_t s) {
+  const void* fn = reinterpret_cast<const void*>(attend_kernel<E, D, MT>);
+  cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  attend_kernel<E, D, MT><<<stream_ctas(), kThreads, Cfg<D>::SMEM, s>>>(P, W, maps);
+  return cudaGetLastError();
+}
+
+template <typename E, int D>
+cudaError_t launch_typed(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
+  const Layout L(P.kv.hq, D, P.B, P.ql);
+  char* w = static_cast<char*>(ws);
+  AttendWork W = {};
+  W.first = 0;
+  W.count = P.n_groups + P.B;
+  for (int i = 0; i < 2; ++i) {
+    AttendPieces& p = i ? W.suffix : W.prefix;
+    p.row_o = reinterpret_cast<float*>(w + L.row_o[i]);
+    p.row_ml = reinterpret_cast<float4*>(w + L.row_ml[i]);
+    p.cta_o = reinterpret_cast<float*>(w + L.cta_o);
+    p.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml);
+  }
+  const int own = P.ql * P.G, shared = P.n_groups > 0 ? (int)(((long long)P.B * own + P.n_groups - 1) / P.n_groups) : 0;
+  const int rows = own > shared ? own : shared;
+  W.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  cudaError_t e = W.rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
+                  : W.rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
+                                 : launch_stream<E, D, 4>(P, W, maps, s);
+  if (e != cudaSuccess) return e;
+  const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
+  join_kernel<E, D><<<(unsigned)((out_rows + 7) / 8), 256, 0, s>>>(P, W, W.rows, W.rows);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attend_ws_bytes(const KvView&, int, int, int) { return 256; }
+cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps) {
+  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const auto enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  const int pt = 1 << kv.page_shift;
+  const cuuint64_t dim[4] = {(cuuint64_t)kv.d, (cuuint64_t)pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
+  const cuuint64_t stride[3] = {(cuuint64_t)kv.token_stride * 2, (cuuint64_t)kv.head_stride * 2,
+                                (cuuint64_t)kv.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(pt < kBoxTokens ? pt : kBoxTokens), 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const auto type = kv.dtype == PW_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  for (int i = 0; i < 2; ++i)
+    if (enc(i ? &maps->v : &maps->k, type, 4, i ? kv.v : kv.k, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
 
-cudaError_t launch_attend(const AttendParams& P, void*, cudaStream_t s) {
-  return P.kv.dtype == PW_F16 ? launch_typed<__half>(P, s) : launch_typed<__nv_bfloat16>(P, s);
+size_t attend_ws_bytes(const KvView& kv, int B, int ql, int) { return Layout(kv.hq, kv.d, B, ql).total; }
+
+cudaError_t launch_attend(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
+  if (P.kv.dtype == PW_F16)
+    return P.kv.d == 128 ? launch_typed<__half, 128>(P, maps, ws, s) : launch_typed<__half, 64>(P, maps, ws, s);
+  return P.kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, ws, s)
+                       : launch_typed<__nv_bfloat16, 64>(P, maps, ws, s);
 }
 
 }  // namespace pw

@@ -1,0 +1,172 @@
+// How an attention call is cut into pieces, shared by its kernels.
+//
+// Items are the prefix groups (all query rows of the group against the
+// prefix) and the sequences (their own rows against their suffix).  Rows of an
+// item are flat: row r is query token r / G, head r % G of the key head's
+// group.  An item is cut into segments (key head, row tile), a segment into
+// key tiles.  All key tiles of a launch, plus a fixed cost in tiles for every
+// segment, form one line that is divided evenly among the CTAs, so ragged
+// lengths and few long sequences load every SM alike, and the host never
+// needs the lengths.  A CTA's range covers at most one segment that began
+// before it (its result goes to the CTA's own slot) and any number that begin
+// in it (their results go to the rows' slots); a merge kernel joins the pieces
+// of a row in a fixed order.
+#pragma once
+
+#include <cuda.h>
+
+#include "pw_serve.h"
+
+namespace pw {
+
+// Where the pieces of a launch go.  Values are sums relative to the piece's
+// reference m: o = sum 2^(s - m) v, l = sum 2^(s - m), s in log2 units.
+struct AttendPieces {
+  float* row_o;      // [rows][D]: segments' first pieces, one row a (query token, head)
+  float4* row_ml;    // m, l, and the CTAs that hold the further pieces: (first, last] as int bits
+  float* cta_o;      // [ctas][ROWS][D]: pieces that continue a segment
+  float2* cta_ml;    // [ctas][ROWS]
+};
+
+struct AttendWork {
+  int first, count;       // items of this launch: 0 .. n_groups - 1 prefixes, then the sequences
+  int rows;               // ROWS of the launch's row tiles
+  AttendPieces prefix, suffix;
+};
+
+struct Item {
+  int tok0, nrows, len;   // first query token, rows (tokens * G), keys
+  const int* table;
+  bool causal;
+};
+
+__device__ __forceinline__ Item attend_item(const AttendParams& P, int i, bool flag) {
+  Item it;
+  bool bad;
+  if (i < P.n_groups) {
+    const int lo = P.group_offsets ? P.group_offsets[i] : 0, hi = P.group_offsets ? P.group_offsets[i + 1] : P.B;
+    const int l = min(max(lo, 0), P.B), h = min(max(hi, l), P.B);
+    const int len = P.prefix_lens[i], most = P.prefix_stride << P.kv.page_shift;
+    it.tok0 = l * P.ql;
+    it.nrows = (h - l) * P.ql * P.G;
+    it.len = min(max(len, 0), most);
+    it.table = P.prefix_table + (long long)i * P.prefix_stride;
+    it.causal = false;
+    bad = l != lo || h != hi || it.len != len;
+  } else {
+    const int b = i - P.n_groups, len = P.lens[b], most = P.table_stride << P.kv.page_shift;
+    it.tok0 = b * P.ql;
+    it.nrows = P.ql * P.G;
+    it.len = min(max(len, 0), most);
+    it.table = P.table + (long long)b * P.table_stride;
+    it.causal = true;
+    bad = it.len != len;
+  }
+  if (flag && bad) atomicExch(P.kv.err, kErrLength);
+  return it;
+}
+
+// A CTA's walk over its range of the line.
+template <int ROWS, int TILE, int COST>
+struct AttendWalk {
+  int item;             // current item
+  unsigned off;         // units of the item before the current position
+  unsigned left;        // units of the range not walked yet
+  unsigned pos;         // position on the line
+  unsigned total;       // length of the line
+  int ctas;             // CTAs that share it
+
+  static __device__ __forceinline__ unsigned units(const AttendParams& P, const Item& it) {
+    if (it.len == 0 || it.nrows == 0) return 0;
+    return (unsigned)((it.len + TILE - 1) / TILE + COST) * ((it.nrows + ROWS - 1) / ROWS) * P.kv.hkv;
+  }
+
+  // Whole CTA: finds the CTA's range.  scratch: 64 words of shared memory.
+  __device__ __forceinline__ void start(const AttendParams& P, const AttendWork& W, unsigned* scratch) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (W.count + nt - 1) / nt;
+    const int i0 = min(tid * per, W.count), i1 = min(i0 + per, W.count);
+    unsigned sum = 0;
+    for (int i = i0; i < i1; ++i) sum += units(P, attend_item(P, W.first + i, blockIdx.x == 0));
+    unsigned scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    if (lane == 31) scratch[warp] = scan;
+    if (tid == 0) scratch[32] = scratch[33] = 0;
+    __syncthreads();
+    unsigned before = scan - sum;
+    total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+      if (w < warp) before += scratch[w];
+      total += scratch[w];
+    }
+    ctas = min((unsigned)gridDim.x, total);
+    const unsigned u0 = blockIdx.x < ctas ? (unsigned)((unsigned long long)total * blockIdx.x / ctas) : total;
+    const unsigned u1 = blockIdx.x < ctas ? (unsigned)((unsigned long long)total * (blockIdx.x + 1) / ctas) : total;
+    if (u0 < u1 && u0 >= before && u0 < before + sum) {  // one thread's items hold the start
+      unsigned at = before;
+      for (int i = i0; i < i1; ++i) {
+        const unsigned n = units(P, attend_item(P, W.first + i, false));
+        if (u0 < at + n) {
+          scratch[32] = W.first + i;
+          scratch[33] = u0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    item = (int)scratch[32];
+    off = scratch[33];
+    left = u1 - u0;
+    pos = u0;
+  }
+
+  struct Piece {
+    Item it;
+    int head, row0;       // key head, first row of the row tile
+    int tile0, tile1;     // key tiles
+    bool first;           // holds the segment's first tile
+    int last_cta;         // CTA that holds its last one
+    bool prefix;
+  };
+
+  // The next piece with tiles in it; false at the end of the range.
+  __device__ __forceinline__ bool next(const AttendParams& P, Piece& p) {
+    while (left > 0) {
+      p.it = attend_item(P, item, false);
+      const unsigned n = units(P, p.it);
+      if (off >= n) {
+        ++item;
+        off = 0;
+        continue;
+      }
+      const int kt = (p.it.len + TILE - 1) / TILE, rt = (p.it.nrows + ROWS - 1) / ROWS;
+      const unsigned su = kt + COST, seg = off / su, within = off - seg * su;
+      const unsigned take = min(su - within, left), end = within + take;
+      p.head = seg / rt;
+      p.row0 = (seg - p.head * rt) * ROWS;
+      p.tile0 = within > COST ? within - COST : 0;
+      p.tile1 = end > COST ? end - COST : 0;
+      p.first = within <= COST;
+      p.prefix = item < P.n_groups;
+      const unsigned seg_end = pos - within + su;  // the segment's end on the line
+      p.last_cta = (int)(((unsigned long long)seg_end * ctas + total - 1) / total) - 1;
+      off += take;
+      pos += take;
+      left -= take;
+      if (p.tile1 > p.tile0) return true;
+    }
+    return false;
+  }
+};
+
+// The tensor-core kernel for prefix groups with many rows (pw_attend_tc.cu).
+constexpr int kTcRows = 256;
+cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const CUtensorMap& mk, const CUtensorMap& mv,
+                             int ctas, cudaStream_t s);
+
+}  // namespace pw

@@ -153,6 +153,8 @@ cudaError_t launch_prefill_dump(const DevLayer& L, int e, int m, __half* out, cu
 // parameters, the decode kernel classes it needs and the bytes of h scratch.
 pw_status ffn_call_args(pw_layer_t layer, const void* x_perm, const int32_t* offsets, int T, const float* y_perm,
                         DevLayer* dev, int* class_mask, size_t* h_bytes);
+// cuTensorMapEncodeTiled of the driver, or null.
+void* tensor_map_encoder();
 // Whether the library runs in host-simulated mode (pw_testing_host_sim).
 bool host_sim();
 // A range of a hot-path call for profiling tools, when PW_NVTX=1.

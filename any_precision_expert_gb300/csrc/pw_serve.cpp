@@ -9,6 +9,7 @@ using namespace pw;
 
 struct pw_kv_s {
   KvView view;
+  KvMaps maps;
 };
 
 namespace {
@@ -114,7 +115,12 @@ extern "C" pw_status pw_kv_create(const pw_kv_desc* desc, void* k, void* v, int3
   w.page_stride = desc->page_stride;
   w.head_stride = desc->head_stride;
   w.token_stride = desc->token_stride;
-  auto* kv = new (std::nothrow) pw_kv_s{w};
+  KvMaps maps = {};
+  if (!host_sim()) {
+    const cudaError_t e = encode_kv_maps(w, &maps);
+    if (e != cudaSuccess) return record_cuda_error(e);
+  }
+  auto* kv = new (std::nothrow) pw_kv_s{w, maps};
   if (!kv) return PW_ERR_OOM;
   *out = kv;
   return PW_OK;
@@ -204,6 +210,13 @@ extern "C" pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* a, void* ws,
     if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255))) return PW_ERR_INVALID_ARG;
     if (ws_bytes < need) return PW_ERR_OOM;
   }
+  // the kernels count key tiles in 32 bits
+  const double tiles = ((double)a->batch * ((double)((long long)a->table_stride << w.page_shift) / 64 + 3) *
+                            ((double)a->q_len * (w.hq / w.hkv) / 16 + 1) +
+                        ((double)a->n_groups + (double)a->batch * a->q_len * (w.hq / w.hkv) / 16) *
+                            ((double)((long long)a->prefix_stride << w.page_shift) / 64 + 3)) *
+                       w.hkv;
+  if (tiles > 2e9) return PW_ERR_UNSUPPORTED;
   if (host_sim()) return PW_ERR_UNSUPPORTED;
   if (a->batch == 0) return PW_OK;
   Range range("pw_kv_attend");
@@ -224,7 +237,7 @@ extern "C" pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* a, void* ws,
   P.prefix_table = a->prefix_table;
   P.prefix_stride = a->prefix_stride;
   P.prefix_lens = a->prefix_lens;
-  return launched(launch_attend(P, ws, as_stream(stream)));
+  return launched(launch_attend(P, kv->maps, ws, as_stream(stream)));
 }
 
 extern "C" pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int32_t* tokens,

@@ -2,6 +2,8 @@
 // and their kernels: heads, the paged KV cache, attention, draft verification.
 #pragma once
 
+#include <cuda.h>
+
 #include "pw_internal.h"
 
 namespace pw {
@@ -67,7 +69,13 @@ struct VerifyParams {
 
 cudaError_t launch_rope(const RopeParams& P, int dtype, int d, cudaStream_t s);
 size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups);
-cudaError_t launch_attend(const AttendParams& P, void* ws, cudaStream_t s);
+// Tensor maps of a cache's keys and values: (value, token of a page, head, page), boxes of 64 values x up to 64 tokens.
+struct KvMaps {
+  CUtensorMap k, v;
+};
+constexpr int kBoxTokens = 64;
+cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps);
+cudaError_t launch_attend(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s);
 cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s);
 
 }  // namespace pw

@@ -667,9 +667,12 @@ typedef struct {
 } pw_attend_desc;
 
 /*
- * Lengths are clamped to [0, stride * page_tokens], group offsets to ascending
- * values in [0, batch], and a page outside [0, n_pages) reads as zeros; all
- * three are flagged.  A sequence outside every group has no prefix.
+ * Lengths are clamped to [0, stride * page_tokens], a group's bounds to 0 <=
+ * o[g] <= o[g+1] <= batch, and a page outside [0, n_pages) reads as zeros; all
+ * three are flagged.  A sequence outside every group has no prefix; one that
+ * descending offsets put into two groups gets unspecified values.
+ * PW_ERR_UNSUPPORTED when the tables could hold more than 2 * 10^9 (64 tokens x
+ * 16 query rows x key head) tiles.
  * ws: device scratch of at least pw_kv_attend_workspace_size() bytes, 256-byte
  * aligned, needing no initial contents (PW_ERR_OOM when ws_bytes is too
  * small).  The result depends on the inputs alone: no atomics order it.
