@@ -12,9 +12,10 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpw.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build the CUDA library first "
-                      "(python -c 'import __graft_entry__ as g; g.build()')")
+for _so in (LIB_PATH, os.path.join(_HERE, "_pw_torch.so")):
+    if not os.path.exists(_so):
+        raise ImportError(f"{_so} is missing: build the CUDA library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
 
 lib = C.CDLL(LIB_PATH)
 
