@@ -1,13 +1,18 @@
 // RMS norm of query and key heads, the position rotation, and the append of
 // keys and values to the paged cache, in one pass.
 //
-// A head row of D values lies in D / 8 lanes of a warp, 16 bytes a lane, so a
-// row's mean of squares is a few shuffles and the partner of a half-split
-// rotation (value i turns with i + rot / 2) sits rot / 16 lanes away.  All
-// arithmetic is fp32 and an output is rounded once.
+// A head row of D values lies in D / 8 lanes of a warp, eight values a lane,
+// placed so that a lane holds both values of every pair it turns: for the
+// half-split rotation four values i .. i + 3 and their partners i + rot / 2
+// .., for the interleaved one eight consecutive values.  So a rotation needs
+// no exchange, four cosines and four sines serve a lane, and the row's mean of
+// squares is a few shuffles.  All arithmetic is fp32; an output is rounded
+// once.
 //
 // Bound: every row is read and written once and little is computed, so HBM
-// for long prompts, launch and load latency for a decode step.
+// for long prompts, launch and load latency for a decode step.  A warp takes U
+// steps of rows of one token and kind (query, key or value), so that its loads
+// are in flight together and its cosines, sines and weights are loaded once.
 #include "pw_heads.cuh"
 #include "pw_serve.h"
 
@@ -17,138 +22,138 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-template <typename E, int D, int U>
+// Row chunks of a token: queries, keys, values.
+struct Chunks {
+  int q, k, v;
+  __host__ __device__ Chunks(const RopeParams& P, int rows)
+      : q((P.hq + rows - 1) / rows), k((P.hk + rows - 1) / rows), v((P.hv + rows - 1) / rows) {}
+  __host__ __device__ int all() const { return q + k + v; }
+};
+
+template <typename E>
+__device__ __forceinline__ void load_pair(const E* p, int a0, int a1, uint4& r) {
+  const uint2 lo = *reinterpret_cast<const uint2*>(p + a0), hi = *reinterpret_cast<const uint2*>(p + a1);
+  r = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+template <typename E, int D, int U, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) {
   constexpr int LPR = D / 8;          // lanes a row
   constexpr int RPW = 32 / LPR;       // rows a warp holds side by side
   constexpr int ROWS = RPW * U;       // rows of a unit
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int nrows = P.hq + P.hk + P.hv;
-  const int per = (nrows + ROWS - 1) / ROWS;
-  const long long units = (long long)P.T * per;
-  const int half = P.rot >> 1;
-  for (long long unit = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); unit < units;
-       unit += (long long)gridDim.x * (kRopeThreads / 32)) {
-    const int t = (int)(unit / per), r0 = (int)(unit % per) * ROWS;
-    uint4 raw[U];
+  const Chunks ch(P, ROWS);
+  const unsigned per = ch.all(), unit = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const unsigned t = unit / per;
+  if (t >= (unsigned)P.T) return;
+  int c = unit - t * per;
+  const int kind = c < ch.q ? 0 : c < ch.q + ch.k ? 1 : 2;
+  c -= kind == 0 ? 0 : kind == 1 ? ch.q : ch.q + ch.k;
+  const int nrows = kind == 0 ? P.hq : kind == 1 ? P.hk : P.hv, h0 = c * ROWS + sub;
+  // this lane's values: a0 .. a0 + 3 and a1 .. a1 + 3 of the row
+  const bool turns = kind < 2 && 8 * l < P.rot;
+  int a0 = 8 * l, a1 = 8 * l + 4;
+  if (!INTER && turns) a0 = 4 * l, a1 = (P.rot >> 1) + 4 * l;
+  const pw_rows in = kind == 0 ? P.q : kind == 1 ? P.k : P.v;
+  const E* src = static_cast<const E*>(in.ptr) + t * in.token_stride;
+  uint4 raw[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int r = r0 + i * RPW + sub;
-      if (r >= nrows) continue;
-      const bool isq = r < P.hq, isk = !isq && r < P.hq + P.hk;
-      const pw_rows& in = isq ? P.q : isk ? P.k : P.v;
-      const int h = isq ? r : isk ? r - P.hq : r - P.hq - P.hk;
-      raw[i] = *reinterpret_cast<const uint4*>(static_cast<const E*>(in.ptr) + t * in.token_stride +
-                                               h * in.head_stride + 8 * l);
+  for (int i = 0; i < U; ++i) {
+    const int h = h0 + i * RPW;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (h < nrows) load_pair(src + h * in.head_stride, a0, a1, raw[i]);
+  }
+  E* dst;
+  long long dst_stride;
+  if (kind == 0 || !P.slots) {
+    const pw_rows& o = kind == 0 ? P.q_out : P.k_out;
+    dst = static_cast<E*>(o.ptr) + t * o.token_stride;
+    dst_stride = o.head_stride;
+  } else {
+    const int slot = P.slots[t];
+    if (slot < 0) return;
+    if ((slot >> P.kv.page_shift) >= P.kv.n_pages) {
+      if (lane == 0) atomicExch(P.err, kErrSlot);
+      return;
     }
-    // this lane's cosines and sines: values 8 l .. 8 l + 7 of the row
-    float c[8], s[8];
-    const bool turns = 8 * l < P.rot;
+    dst = reinterpret_cast<E*>(kind == 1 ? P.kv.k : P.kv.v) + (slot >> P.kv.page_shift) * P.kv.page_stride +
+          (slot & ((1 << P.kv.page_shift) - 1)) * P.kv.token_stride;
+    dst_stride = P.kv.head_stride;
+  }
+  if (kind < 2 && (P.rot > 0 || (kind == 0 ? P.qw : P.kw))) {  // else the bits are copied
+    float4 cs = make_float4(1, 1, 1, 1), sn = make_float4(0, 0, 0, 0);
     if (turns) {
       int pos = P.positions[t];
       if (pos < 0 || pos >= P.max_pos) {
-        if (lane == 0 && P.err) atomicExch(P.err, kErrPosition);
+        if (l == 0 && P.err) atomicExch(P.err, kErrPosition);
         pos = pos < 0 ? 0 : P.max_pos - 1;
       }
-      const float* cs = P.cos_sin + (long long)pos * P.rot;
-      if (P.interleaved) {
-        const float4 cc = *reinterpret_cast<const float4*>(cs + 4 * l);
-        const float4 ss = *reinterpret_cast<const float4*>(cs + half + 4 * l);
-        c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
-        s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
-      } else {
-        const int at = 8 * l < half ? 8 * l : 8 * l - half;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 cc = *reinterpret_cast<const float4*>(cs + at + j);
-          const float4 ss = *reinterpret_cast<const float4*>(cs + half + at + j);
-          c[j] = cc.x, c[j + 1] = cc.y, c[j + 2] = cc.z, c[j + 3] = cc.w;
-          s[j] = ss.x, s[j + 1] = ss.y, s[j + 2] = ss.z, s[j + 3] = ss.w;
-        }
-        if (8 * l < half) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[j] = -s[j];
-        }
-      }
+      const float* row = P.cos_sin + (long long)pos * P.rot + 4 * l;
+      cs = *reinterpret_cast<const float4*>(row);
+      sn = *reinterpret_cast<const float4*>(row + (P.rot >> 1));
     }
-    const int partner = P.interleaved || !turns ? lane : 8 * l < half ? lane + half / 8 : lane - half / 8;
-    int slot = -1;
-    if (P.slots) {
-      slot = P.slots[t];
-      if (slot >= 0 && (slot >> P.kv.page_shift) >= P.kv.n_pages) {
-        if (lane == 0) atomicExch(P.err, kErrSlot);
-        slot = -1;
-      }
+    const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+    const void* w = kind == 0 ? P.qw : P.kw;
+    float g[8];
+    if (w) {
+      uint4 gr;
+      load_pair(static_cast<const E*>(w), a0, a1, gr);
+      unpack8<E>(gr, g);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int r = r0 + i * RPW + sub;
-      const bool live = r < nrows;
-      const bool isq = r < P.hq, isk = !isq && r < P.hq + P.hk;
-      const int h = isq ? r : isk ? r - P.hq : r - P.hq - P.hk;
-      uint4 res = raw[i];
       float x[8];
-      unpack8<E>(live ? raw[i] : make_uint4(0, 0, 0, 0), x);
-      const void* w = isq ? P.qw : isk ? P.kw : nullptr;
-      float sq = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      unpack8<E>(raw[i], x);
       if (w) {
-        float g[8];
-        unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const E*>(w) + 8 * l), g);
+        float sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
         const float inv = rsqrtf(sq * (1.f / D) + P.eps);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
       }
-      if (P.rot > 0) {
-        if (P.interleaved) {
-          if (turns) {
+      if (turns) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = x[2 * j], b = x[2 * j + 1];
-              x[2 * j] = a * c[j] - b * s[j];
-              x[2 * j + 1] = b * c[j] + a * s[j];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = __shfl_sync(0xffffffffu, x[j], partner);
-            if (turns) x[j] = x[j] * c[j] + y * s[j];
-          }
+        for (int j = 0; j < 4; ++j) {
+          float& a = x[INTER ? 2 * j : j];
+          float& b = x[INTER ? 2 * j + 1 : 4 + j];
+          const float ta = a * cv[j] - b * sv[j];
+          b = b * cv[j] + a * sv[j];
+          a = ta;
         }
       }
-      if (!live) continue;
-      if (isq || isk) res = pack8<E>(x);  // values are copied bit for bit
-      E* dst;
-      if (isq) {
-        dst = static_cast<E*>(P.q_out.ptr) + t * P.q_out.token_stride + h * P.q_out.head_stride;
-      } else if (!P.slots) {
-        dst = static_cast<E*>(P.k_out.ptr) + t * P.k_out.token_stride + h * P.k_out.head_stride;
-      } else {
-        if (slot < 0) continue;
-        dst = reinterpret_cast<E*>(isk ? P.kv.k : P.kv.v) + (slot >> P.kv.page_shift) * P.kv.page_stride +
-              h * P.kv.head_stride + (slot & ((1 << P.kv.page_shift) - 1)) * P.kv.token_stride;
-      }
-      *reinterpret_cast<uint4*>(dst + 8 * l) = res;
+      raw[i] = pack8<E>(x);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int h = h0 + i * RPW;
+    if (h >= nrows) continue;
+    E* to = dst + h * dst_stride;
+    *reinterpret_cast<uint2*>(to + a0) = make_uint2(raw[i].x, raw[i].y);
+    *reinterpret_cast<uint2*>(to + a1) = make_uint2(raw[i].z, raw[i].w);
   }
 }
 
 template <typename E, int D, int U>
 cudaError_t launch_one(const RopeParams& P, cudaStream_t s) {
-  constexpr int ROWS = 32 / (D / 8) * U;
-  const long long units = (long long)P.T * ((P.hq + P.hk + P.hv + ROWS - 1) / ROWS);
+  const long long units = (long long)P.T * Chunks(P, 32 / (D / 8) * U).all();
   const long long blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  rope_kernel<E, D, U><<<(unsigned)(blocks < 0x7fffffffll ? blocks : 0x7fffffffll), kRopeThreads, 0, s>>>(P);
+  if (blocks > 0x7fffffffll || units > 0xffffff00ll) return cudaErrorInvalidConfiguration;
+  if (P.interleaved)
+    rope_kernel<E, D, U, true><<<(unsigned)blocks, kRopeThreads, 0, s>>>(P);
+  else
+    rope_kernel<E, D, U, false><<<(unsigned)blocks, kRopeThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 
 template <typename E>
 cudaError_t launch_typed(const RopeParams& P, int d, cudaStream_t s) {
-  return d == 128 ? launch_one<E, 128, 1>(P, s) : launch_one<E, 64, 1>(P, s);
+  const bool few = (long long)P.T * (P.hq + P.hk + P.hv) * d < (1 << 21);
+  if (d == 128) return few ? launch_one<E, 128, 1>(P, s) : launch_one<E, 128, 4>(P, s);
+  return few ? launch_one<E, 64, 1>(P, s) : launch_one<E, 64, 4>(P, s);
 }
 
 }  // namespace
