@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libpw.so")
 BINDING = os.path.join(PKG, "_pw_torch.so")
 
 SOURCES = ["pw_runtime.cpp", "pw_pack.cpp", "pw_planner.cpp", "pw_kernels.cu", "pw_ffn.cu", "pw_decode.cu",
-           "pw_prefill.cu", "pw_noalloc.cu", "pw_serve.cpp", "pw_rope.cu", "pw_attend.cu", "pw_verify.cu"]
+           "pw_prefill.cu", "pw_noalloc.cu", "pw_serve.cpp", "pw_rope.cu", "pw_attend.cu", "pw_attend_tc.cu", "pw_verify.cu"]
 # the planner compares doubles: no fused multiply-adds, so x86 and Arm hosts plan alike
 SOURCE_FLAGS = {"pw_planner.cpp": ["-Xcompiler", "-ffp-contract=off"]}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -10,7 +10,7 @@
 // boxes of whole pages land in a ring of 64-token stages, four warps multiply
 // them with mma.sync.  With R rows a key head it does R products a key byte;
 // up to 64 of them the legacy tensor path keeps up with HBM, so the loads
-// bound it.
+// bound it.  Items with more rows go to the tcgen05 kernel (pw_attend_tc.cu).
 #include <math_constants.h>
 
 #include "pw_attend.cuh"
@@ -25,9 +25,6 @@ constexpr int kTile = 64;                  // keys a stage
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kSegmentCost = 1;            // a segment's fixed cost, in key tiles
-// Weights are kept as 2^(s - max + kShift): fp16 weights down to 2^-(14 + kShift) of the largest stay normal numbers.
-constexpr float kShift = 6.f;
-
 template <int D>
 struct Cfg {
   static constexpr int HALF = kTile * 128;              // one 64-value column block of a tile, 128-byte rows
@@ -40,15 +37,6 @@ struct Cfg {
   static constexpr int BAR_AT = ML_AT + 2 * 128;
   static constexpr int SMEM = BAR_AT + 2 * 8 * STAGES + 16;
 };
-
-__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page,
-                                              uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
-          "r"(dst),
-      "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(mbar)
-      : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -75,12 +63,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
@@ -406,26 +388,41 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
   if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 int stream_ctas() { return 2 * sm_count(); }
 
+// Which kernel takes which items.  Up to 64 rows a key head the streaming
+// kernel is bound by its loads; beyond, its products are.
+struct Plan {
+  bool tc_prefix, tc_suffix;
+  int stream_rows;     // rows of the streaming kernel's tiles, 0 when it has no items
+  Plan(int G, int B, int ql, int n_groups) {
+    const long long own = (long long)ql * G, shared = n_groups > 0 ? (B * own + n_groups - 1) / n_groups : 0;
+    tc_suffix = own > 64;
+    tc_prefix = n_groups > 0 && (shared > 64 || tc_suffix);
+    const long long rows = !tc_suffix && !tc_prefix && shared > own ? shared : own;
+    stream_rows = tc_suffix ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  }
+  bool tc() const { return tc_prefix || tc_suffix; }
+};
+
 struct Layout {
-  size_t row_o[2], row_ml[2], cta_o, cta_ml, total;
-  Layout(int hq, int d, int B, int ql) {
-    const size_t rows = (size_t)B * ql * hq, most = (size_t)stream_ctas() * 64;
+  size_t row_o[2], row_ml[2], cta_o[2], cta_ml[2], total;  // [prefix, suffix], [streaming, tcgen05]
+  Layout(const Plan& plan, int hq, int d, int B, int ql) {
+    const size_t rows = (size_t)B * ql * hq;
     size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t was = at;
+      at += (n + 255) & ~(size_t)255;
+      return was;
+    };
     for (int i = 0; i < 2; ++i) {
-      row_o[i] = at;
-      at += up256(rows * d * 4);
-      row_ml[i] = at;
-      at += up256(rows * 16);
+      row_o[i] = take(rows * d * 4);
+      row_ml[i] = take(rows * 16);
+      const size_t most = i ? (plan.tc() ? (size_t)attend_tc_ctas() * kTcRows : 0) : (size_t)stream_ctas() * plan.stream_rows;
+      cta_o[i] = take(most * d * 4);
+      cta_ml[i] = take(most * 8);
     }
-    cta_o = at;
-    at += up256(most * d * 4);
-    cta_ml = at;
-    at += up256(most * 8);
-    total = at;
+    total = at + 256;
   }
 };
 
@@ -440,27 +437,38 @@ cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMa
 
 template <typename E, int D>
 cudaError_t launch_typed(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
-  const Layout L(P.kv.hq, D, P.B, P.ql);
+  const Plan plan(P.G, P.B, P.ql, P.n_groups);
+  const Layout L(plan, P.kv.hq, D, P.B, P.ql);
   char* w = static_cast<char*>(ws);
+  auto pieces = [&](bool suffix, bool tc) {
+    AttendPieces p;
+    p.row_o = reinterpret_cast<float*>(w + L.row_o[suffix]);
+    p.row_ml = reinterpret_cast<float4*>(w + L.row_ml[suffix]);
+    p.cta_o = reinterpret_cast<float*>(w + L.cta_o[tc]);
+    p.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml[tc]);
+    return p;
+  };
   AttendWork W = {};
-  W.first = 0;
-  W.count = P.n_groups + P.B;
-  for (int i = 0; i < 2; ++i) {
-    AttendPieces& p = i ? W.suffix : W.prefix;
-    p.row_o = reinterpret_cast<float*>(w + L.row_o[i]);
-    p.row_ml = reinterpret_cast<float4*>(w + L.row_ml[i]);
-    p.cta_o = reinterpret_cast<float*>(w + L.cta_o);
-    p.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml);
+  W.prefix = pieces(false, plan.tc_prefix);
+  W.suffix = pieces(true, plan.tc_suffix);
+  cudaError_t e = cudaSuccess;
+  if (plan.tc()) {
+    W.first = 0;
+    W.count = P.n_groups + (plan.tc_suffix ? P.B : 0);
+    e = launch_attend_tc(P, W, maps, s);
+    if (e != cudaSuccess) return e;
   }
-  const int own = P.ql * P.G, shared = P.n_groups > 0 ? (int)(((long long)P.B * own + P.n_groups - 1) / P.n_groups) : 0;
-  const int rows = own > shared ? own : shared;
-  W.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  cudaError_t e = W.rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
-                  : W.rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
+  if (plan.stream_rows) {
+    W.first = plan.tc_prefix ? P.n_groups : 0;
+    W.count = P.n_groups + P.B - W.first;
+    e = plan.stream_rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
+        : plan.stream_rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
                                  : launch_stream<E, D, 4>(P, W, maps, s);
-  if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
+  }
   const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
-  join_kernel<E, D><<<(unsigned)((out_rows + 7) / 8), 256, 0, s>>>(P, W, W.rows, W.rows);
+  join_kernel<E, D><<<(unsigned)((out_rows + 7) / 8), 256, 0, s>>>(P, W, plan.tc_prefix ? kTcRows : plan.stream_rows,
+                                                                   plan.tc_suffix ? kTcRows : plan.stream_rows);
   return cudaGetLastError();
 }
 
@@ -487,7 +495,9 @@ cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps) {
   return cudaSuccess;
 }
 
-size_t attend_ws_bytes(const KvView& kv, int B, int ql, int) { return Layout(kv.hq, kv.d, B, ql).total; }
+size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups) {
+  return Layout(Plan(kv.hq / kv.hkv, B, ql, n_groups), kv.hq, kv.d, B, ql).total;
+}
 
 cudaError_t launch_attend(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
   if (P.kv.dtype == PW_F16)

@@ -30,7 +30,6 @@ struct AttendPieces {
 
 struct AttendWork {
   int first, count;       // items of this launch: 0 .. n_groups - 1 prefixes, then the sequences
-  int rows;               // ROWS of the launch's row tiles
   AttendPieces prefix, suffix;
 };
 
@@ -164,9 +163,27 @@ struct AttendWalk {
   }
 };
 
+// Weights are kept as 2^(s - max + kShift): fp16 weights down to 2^-(14 + kShift) of the largest stay normal numbers.
+constexpr float kShift = 6.f;
+
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page,
+                                              uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(mbar)
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The tensor-core kernel for prefix groups with many rows (pw_attend_tc.cu).
 constexpr int kTcRows = 256;
-cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const CUtensorMap& mk, const CUtensorMap& mv,
-                             int ctas, cudaStream_t s);
+cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const KvMaps& maps, cudaStream_t s);
+int attend_tc_ctas();
 
 }  // namespace pw
