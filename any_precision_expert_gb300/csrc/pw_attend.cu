@@ -6,11 +6,14 @@
 // keys of one row may be split among CTAs (pw_attend.cuh) and joined at the
 // end.  Exponents are taken in log2 units: e^s = 2^(s log2 e).
 //
-// attend_kernel streams keys and values once for up to 64 query rows: TMA
-// boxes of whole pages land in a ring of 64-token stages, four warps multiply
-// them with mma.sync.  With R rows a key head it does R products a key byte;
-// up to 64 of them the legacy tensor path keeps up with HBM, so the loads
-// bound it.  Items with more rows go to the tcgen05 kernel (pw_attend_tc.cu).
+// attend_kernel streams keys and values once for up to 64 query rows: a
+// producer warp issues TMA boxes of whole pages into a ring of 32 KB stages,
+// four warps multiply them with mma.sync.  A stage holds 64 / HB keys of HB
+// key heads; a warp takes one head (or, with fewer heads a stage, a row tile
+// or a share of the keys), so with four heads a stage no warp ever waits for
+// another.  With R rows a key head it does R products a key byte; up to 64 of
+// them the legacy tensor path keeps up with HBM, so the loads bound it.  Items
+// with more rows go to the tcgen05 kernel (pw_attend_tc.cu).
 #include <math_constants.h>
 
 #include "pw_attend.cuh"
@@ -21,21 +24,22 @@ namespace pw {
 
 namespace {
 
-constexpr int kTile = 64;                  // keys a stage
+constexpr int kStageKeys = 64;             // keys x heads a stage
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
-constexpr int kSegmentCost = 1;            // a segment's fixed cost, in key tiles
+
 template <int D>
 struct Cfg {
-  static constexpr int HALF = kTile * 128;              // one 64-value column block of a tile, 128-byte rows
+  static constexpr int HALF = kStageKeys * 128;         // one 64-value column block of a stage, 128-byte rows
   static constexpr int NH = D / 64;
   static constexpr int STAGE = 2 * NH * HALF;           // keys, then values
   static constexpr int STAGES = 98304 / STAGE;
   static constexpr int JOIN = 2 * (D / 8) * 512;        // accumulators of two warps
   static constexpr int JOIN_AT = STAGES * STAGE;
   static constexpr int ML_AT = JOIN_AT + JOIN;          // (m, l) of two warps' rows
-  static constexpr int BAR_AT = ML_AT + 2 * 128;
-  static constexpr int SMEM = BAR_AT + 2 * 8 * STAGES + 16;
+  static constexpr int PIECE_AT = ML_AT + 2 * 128;
+  static constexpr int BAR_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
+  static constexpr int SMEM = BAR_AT + 16 * STAGES + 16 * kPieces + 16;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -73,110 +77,144 @@ __device__ __forceinline__ uint32_t keep_keys(uint32_t w, int k, int n) {
   return k + 1 < n ? w : k < n ? (w & 0xffffu) : 0u;
 }
 
-// MT row tiles of 16; the warps of a row tile share the stage's keys.
-template <typename E, int D, int MT>
+// MT row tiles of 16, HB heads a stage; KS warps share the keys of a (row tile, head).
+template <typename E, int D, int MT, int HB>
 __global__ void __launch_bounds__(kThreads, 2)
     attend_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ KvMaps maps) {
   using C = Cfg<D>;
-  constexpr int ROWS = 16 * MT, KS = kComputeWarps / MT, KPW = kTile / KS;
-  using Walk = AttendWalk<ROWS, kTile, kSegmentCost>;
+  constexpr int ROWS = 16 * MT, KS = kComputeWarps / (MT * HB), TILE = kStageKeys / HB, KPW = TILE / KS;
+  constexpr int HEAD = TILE * 128;  // bytes of one head's rows in a column block
+  // a segment's fixed cost in key tiles: about one 64-key tile's time
+  using Walk = AttendWalk<ROWS, TILE, HB, HB>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES + 16 * kPieces);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (base & 1023) {
     if (tid == 0) atomicExch(P.kv.err, kErrLayout);
     return;
   }
+  PieceRing ring;
+  ring.full = empty + 8 * C::STAGES;
+  ring.empty = ring.full + 8 * kPieces;
+  ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
+  ring.abort_flag = abort_flag;
+  ring.err = P.kv.err;
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, kComputeWarps);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(ring.full + 8 * i, 1);
+      mbar_init(ring.empty + 8 * i, kComputeWarps);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   Walk walk;
-  walk.start(P, W, reinterpret_cast<unsigned*>(smem));  // scratch: the ring, before any load
-  fence_proxy_async_smem();
-  __syncthreads();
-  typename Walk::Piece pc;
+  walk.start(P, W, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
+  Piece pc;
   int stage = 0, phase = 0;
 
   if (warp == kComputeWarps) {
     // ---- producer: one lane a page ----
     const int shift = P.kv.page_shift;
-    const int box = min(1 << shift, kBoxTokens);
-    while (walk.next(P, pc)) {
-      for (int t = pc.tile0; t < pc.tile1; ++t) {
-        const int keys = min(kTile, pc.it.len - t * kTile), boxes = (keys + box - 1) / box;
-        const int at = t * kTile + lane * box;
+    const int box = min(1 << shift, TILE);  // tokens of a box
+    const int* table;
+    bool ok = true;
+    while (ok) {
+      const bool more = walk.next(P, pc, table);
+      ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
+      if (!more) break;
+      for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
+        const int keys = min(TILE, pc.len - t * TILE), boxes = (keys + box - 1) / box;
+        const int at = t * TILE + lane * box;
         int page = 0;
         if (lane < boxes) {
-          page = pc.it.table[at >> shift];
+          page = table[at >> shift];
           if (page < 0 || page >= P.kv.n_pages) atomicExch(P.kv.err, kErrPage);  // reads as zeros
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, abort_flag, P.kv.err))) goto stopped;
-        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(boxes * box * D * 4));
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, abort_flag, P.kv.err));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(boxes * box * HB * D * 4));
         __syncwarp();
         if (lane < boxes) {
+          // HB heads of a box that is shorter than the tile: one load a head, else one load for all
           const uint32_t dst = base + stage * C::STAGE + lane * box * 128;
           const int tok = at & ((1 << shift) - 1);
 #pragma unroll
           for (int h = 0; h < C::NH; ++h) {
-            tma_load_page(dst + h * C::HALF, &maps.k, 64 * h, tok, pc.head, page, full + 8 * stage);
-            tma_load_page(dst + (C::NH + h) * C::HALF, &maps.v, 64 * h, tok, pc.head, page, full + 8 * stage);
+            if (HB == 1 || box == TILE) {
+              tma_load_page(dst + h * C::HALF, &maps.k, 64 * h, tok, pc.head, page, full + 8 * stage);
+              tma_load_page(dst + (C::NH + h) * C::HALF, &maps.v, 64 * h, tok, pc.head, page, full + 8 * stage);
+            } else {
+#pragma unroll
+              for (int g = 0; g < HB; ++g) {
+                tma_load_page(dst + h * C::HALF + g * HEAD, &maps.k, 64 * h, tok, pc.head + g, page, full + 8 * stage);
+                tma_load_page(dst + (C::NH + h) * C::HALF + g * HEAD, &maps.v, 64 * h, tok, pc.head + g, page,
+                              full + 8 * stage);
+              }
+            }
           }
         }
         __syncwarp();
         if (++stage == C::STAGES) stage = 0, phase ^= 1;
       }
     }
-    return;
-  stopped:
-    // a wait gave up: let the copies in flight land before the shared memory goes away
-    for (int i = 0; i < C::STAGES; ++i)
-      for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
-      }
+    if (!ok)  // a wait gave up: let the copies in flight land before the shared memory goes away
+      for (int i = 0; i < C::STAGES; ++i)
+        for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
+        }
+    asm volatile("griddepcontrol.launch_dependents;");  // the join may take its place beside the last pieces
+    // the tcgen05 kernel of the same call may still run: this launch ends after it
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
   // ---- compute warps ----
   const int g = lane >> 2, t4 = lane & 3;
-  const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
+  const int mt = warp % MT, hb = (warp / MT) % HB, ks = warp / (MT * HB), k0 = ks * KPW;
   const float scale2 = P.scale * 1.4426950408889634f;
   // ldmatrix row addresses inside a 128-byte-row block: lane l supplies row l % 8 of matrix l / 8
   const int mrow = lane & 7, msel = lane >> 3;
-  while (walk.next(P, pc)) {
-    const int ra = pc.row0 + mt * 16 + g;
-    uint32_t qf[D / 16][4];
-    int vis[2];
+  uint32_t qf[D / 16][4];
+  auto load_q = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = ra + 8 * i;
-      const bool in = r < pc.it.nrows;
-      const int tok = in ? r / P.G : 0, hd = in ? pc.head * P.G + r - tok * P.G : 0;
-      const E* src = static_cast<const E*>(P.q.ptr) + (pc.it.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride;
-      vis[i] = pc.it.causal && in ? pc.it.len - P.ql + 1 + tok : pc.it.len;
+      const int r = pc.row0 + mt * 16 + g + 8 * i;
+      const bool in = r < pc.nrows;
+      const int tok = in ? r / P.G : 0, hd = in ? (pc.head + hb) * P.G + r - tok * P.G : 0;
+      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         qf[s][i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4) : 0u;
         qf[s][2 + i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4) : 0u;
       }
     }
-    const int sure = pc.it.causal ? pc.it.len - P.ql + 1 : pc.it.len;  // keys below this are seen by every row
+  };
+  bool have = ring.take<true>(pc);
+  if (have) load_q();
+  while (have) {
+    const Piece cur = pc;
+    const int ra = cur.row0 + mt * 16 + g;
+    int vis[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      vis[i] = cur.causal && ra + 8 * i < cur.nrows ? cur.len - P.ql + 1 + (ra + 8 * i) / P.G : cur.len;
+    const int sure = cur.causal ? cur.len - P.ql + 1 : cur.len;  // keys below this are seen by every row
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    for (int t = pc.tile0; t < pc.tile1; ++t) {
+    for (int t = cur.tile0; t < cur.tile1; ++t) {
       // a wait that gives up leaves the sums as they are; the walk goes on, so that every barrier is met
       const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
-      const int first = t * kTile + k0;  // this warp's first key
-      if (landed && first < pc.it.len) {
-        const uint32_t kb = base + stage * C::STAGE, vb = kb + C::NH * C::HALF;
+      const int first = t * TILE + k0;  // this warp's first key
+      if (landed && first < cur.len) {
+        const uint32_t kb = base + stage * C::STAGE + hb * HEAD, vb = kb + C::NH * C::HALF;
         float s[KPW / 8][4];
 #pragma unroll
         for (int n = 0; n < KPW / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
@@ -238,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           pf[n / 2][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
           pf[n / 2][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
         }
-        const bool tail = first + KPW > pc.it.len;  // values past the length may be anything: 0 instead
+        const bool tail = first + KPW > cur.len;  // values past the length may be anything: 0 instead
 #pragma unroll
         for (int n = 0; n < KPW / 16; ++n) {
-          const int left = pc.it.len - first - 16 * n;
+          const int left = cur.len - first - 16 * n;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
             // matrices: keys 0-7 / 8-15 (msel & 1), values 0-7 / 8-15 (msel >> 1)
@@ -262,7 +300,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (++stage == C::STAGES) stage = 0, phase ^= 1;
     }
 
-    // ---- join the warps of a row tile: the upper half hands its sums to the lower one, in halving steps ----
+    have = ring.take<true>(pc);
+    if (have) load_q();  // on their way while this piece's sums are stored
+
+    // ---- join the warps that share keys: the upper half hands its sums to the lower one, in halving steps ----
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -272,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int step = KS / 2; step > 0; step >>= 1) {
       compute_sync();  // the buffer is free
       if (ks >= step && ks < 2 * step) {
-        const int slot = (ks - step) * MT + mt;
+        const int slot = ((ks - step) * HB + hb) * MT + mt;
 #pragma unroll
         for (int d = 0; d < D / 8; ++d)
           *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16) =
@@ -282,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       compute_sync();
       if (ks < step) {
-        const int slot = ks * MT + mt;
+        const int slot = (ks * HB + hb) * MT + mt;
         const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 128 + g * 16);
         const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
         float fa[2], fb[2];
@@ -306,20 +347,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (ks == 0) {
-      const AttendPieces& to = pc.prefix ? W.prefix : W.suffix;
+      const AttendPieces& to = cur.prefix ? W.prefix : W.suffix;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = ra + 8 * i;
-        if (r >= pc.it.nrows) continue;
+        if (r >= cur.nrows) continue;
         float* dst;
-        if (pc.first) {
+        if (cur.first) {
           const int tok = r / P.G;
-          const long long row = (long long)(pc.it.tok0 + tok) * P.kv.hq + pc.head * P.G + r - tok * P.G;
+          const long long row = (long long)(cur.tok0 + tok) * P.kv.hq + (cur.head + hb) * P.G + r - tok * P.G;
           dst = to.row_o + row * D;
           if (t4 == 0)
-            to.row_ml[row] = make_float4(m[i], l[i], __int_as_float((int)blockIdx.x), __int_as_float(pc.last_cta));
+            to.row_ml[row] = make_float4(m[i], l[i], __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
         } else {
-          const int row = blockIdx.x * ROWS + mt * 16 + g + 8 * i;
+          const int row = (blockIdx.x * HB + hb) * ROWS + mt * 16 + g + 8 * i;
           dst = to.cta_o + (long long)row * D;
           if (t4 == 0) to.cta_ml[row] = make_float2(m[i], l[i]);
         }
@@ -331,10 +372,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+// How the prefix and suffix kernels cut rows: rows and heads of a segment.
+struct JoinShape {
+  int rows[2], heads[2];
+};
+
 // Joins a row's pieces: one warp a (query token, head).
 template <typename E, int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const AttendWork W, int prefix_rows,
-                                                   int suffix_rows) {
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const AttendWork W, const JoinShape shape) {
   constexpr int PER = D / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -359,28 +404,64 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
   float m = -CUDART_INF_F, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  auto add = [&](float pm, float pl, const float* src) {
-    const float mm = fmaxf(m, pm), rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), fb = ex2(pm - rr);
-    m = mm;
-    l = l * fa + pl * fb;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * fa + src[lane * PER + i] * fb;
-  };
-  auto pieces = [&](const AttendPieces& from, int rows, int local) {
+  // Pieces of a segment: the first in the row's own place, the others in the slots of the CTAs after it.  Eight at a
+  // time: their (m, l) in eight lanes, then their values, all loads of a step in flight together.
+  auto pieces = [&](const AttendPieces& from, int rows, int heads, int local) {
     const float4 a = from.row_ml[row];
-    add(a.x, a.y, from.row_o + row * D);
-    const int c1 = __float_as_int(a.w);
-    for (int c = __float_as_int(a.z) + 1; c <= c1; ++c) {
-      const long long at = (long long)c * rows + local;
-      const float2 y = from.cta_ml[at];
-      add(y.x, y.y, from.cta_o + at * D);
+    const int c0 = __float_as_int(a.z), n = __float_as_int(a.w) - c0 + 1;
+    const long long slot = ((long long)c0 * heads + h / P.G % heads) * rows + local, step = (long long)heads * rows;
+    for (int p0 = 0; p0 < n; p0 += 8) {
+      const int p = p0 + (lane & 7);
+      float pm = -CUDART_INF_F, pl = 0.f;
+      if (p == 0) {
+        pm = a.x, pl = a.y;
+      } else if (p < n) {
+        const float2 y = from.cta_ml[slot + p * step];
+        pm = y.x, pl = y.y;
+      }
+      float v[8][PER];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[j][i] = 0.f;
+        if (p0 + j < n) {
+          const float* src = (p0 + j == 0 ? from.row_o + row * D : from.cta_o + (slot + (p0 + j) * step) * D) + lane * PER;
+          if constexpr (PER == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src);
+            v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            v[j][0] = y.x, v[j][1] = y.y;
+          }
+        }
+      }
+      float mm = fmaxf(m, pm);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+      const float rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), f = ex2(pm - rr);
+      m = mm;
+      float add = pl * f;
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+      l = l * fa + add;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] *= fa;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = __shfl_sync(0xffffffffu, f, j);
+        if (p0 + j < n) {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) o[i] = fmaf(v[j][i], w, o[i]);
+        }
+      }
     }
   };
   const int hl = h % P.G;
-  if (grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0)
-    pieces(W.prefix, prefix_rows, ((n - tok0) * P.G + hl) % prefix_rows);
-  if (min(P.lens[b], P.table_stride << P.kv.page_shift) > 0)
-    pieces(W.suffix, suffix_rows, ((n - b * P.ql) * P.G + hl) % suffix_rows);
+  const bool pre = grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0;
+  const bool suf = min(P.lens[b], P.table_stride << P.kv.page_shift) > 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
+  if (pre) pieces(W.prefix, shape.rows[0], shape.heads[0], ((n - tok0) * P.G + hl) % shape.rows[0]);
+  if (suf) pieces(W.suffix, shape.rows[1], shape.heads[1], ((n - b * P.ql) * P.G + hl) % shape.rows[1]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + lane * PER;
 #pragma unroll
@@ -395,12 +476,15 @@ int stream_ctas() { return 2 * sm_count(); }
 struct Plan {
   bool tc_prefix, tc_suffix;
   int stream_rows;     // rows of the streaming kernel's tiles, 0 when it has no items
-  Plan(int G, int B, int ql, int n_groups) {
+  int heads;           // key heads of its stages
+  Plan(int G, int hkv, int B, int ql, int n_groups) {
     const long long own = (long long)ql * G, shared = n_groups > 0 ? (B * own + n_groups - 1) / n_groups : 0;
     tc_suffix = own > 64;
     tc_prefix = n_groups > 0 && (shared > 64 || tc_suffix);
     const long long rows = !tc_suffix && !tc_prefix && shared > own ? shared : own;
     stream_rows = tc_suffix ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    heads = stream_rows == 16 ? 4 : stream_rows == 32 ? 2 : 1;
+    while (hkv % heads) heads /= 2;
   }
   bool tc() const { return tc_prefix || tc_suffix; }
 };
@@ -418,7 +502,7 @@ struct Layout {
     for (int i = 0; i < 2; ++i) {
       row_o[i] = take(rows * d * 4);
       row_ml[i] = take(rows * 16);
-      const size_t most = i ? (plan.tc() ? (size_t)attend_tc_ctas() * kTcRows : 0) : (size_t)stream_ctas() * plan.stream_rows;
+      const size_t most = i ? (plan.tc() ? (size_t)attend_tc_ctas() * kTcRows : 0) : (size_t)stream_ctas() * plan.stream_rows * plan.heads;
       cta_o[i] = take(most * d * 4);
       cta_ml[i] = take(most * 8);
     }
@@ -426,18 +510,38 @@ struct Layout {
   }
 };
 
-template <typename E, int D, int MT>
-cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMaps& maps, cudaStream_t s) {
-  const void* fn = reinterpret_cast<const void*>(attend_kernel<E, D, MT>);
-  cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
+// Launch attributes: `early` lets the kernel start while the one before it in the stream still runs (it waits for it
+// before it reads what that one writes, and before it ends).
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  Launch(unsigned grid, unsigned block, size_t smem, cudaStream_t s, bool early) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+  }
+};
+
+template <typename E, int D, int MT, int HB>
+cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMapSet& maps, bool early, cudaStream_t s) {
+  const void* fn = reinterpret_cast<const void*>(attend_kernel<E, D, MT, HB>);
+  const cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  attend_kernel<E, D, MT><<<stream_ctas(), kThreads, Cfg<D>::SMEM, s>>>(P, W, maps);
-  return cudaGetLastError();
+  // boxes of several heads only where a page holds a whole tile
+  const bool whole = (1 << P.kv.page_shift) >= kStageKeys / HB;
+  const KvMaps& m = HB == 4 && whole ? maps.heads4 : HB == 2 && whole ? maps.heads2 : maps.heads1;
+  const Launch at(stream_ctas(), kThreads, Cfg<D>::SMEM, s, early);
+  return cudaLaunchKernelEx(&at.cfg, attend_kernel<E, D, MT, HB>, P, W, m);
 }
 
 template <typename E, int D>
-cudaError_t launch_typed(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
-  const Plan plan(P.G, P.B, P.ql, P.n_groups);
+cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {
+  const Plan plan(P.G, P.kv.hkv, P.B, P.ql, P.n_groups);
   const Layout L(plan, P.kv.hq, D, P.B, P.ql);
   char* w = static_cast<char*>(ws);
   auto pieces = [&](bool suffix, bool tc) {
@@ -455,26 +559,37 @@ cudaError_t launch_typed(const AttendParams& P, const KvMaps& maps, void* ws, cu
   if (plan.tc()) {
     W.first = 0;
     W.count = P.n_groups + (plan.tc_suffix ? P.B : 0);
-    e = launch_attend_tc(P, W, maps, s);
+    e = launch_attend_tc(P, W, maps.heads1, attend_tc_ctas(), s);
     if (e != cudaSuccess) return e;
   }
   if (plan.stream_rows) {
+    const bool early = plan.tc();
     W.first = plan.tc_prefix ? P.n_groups : 0;
     W.count = P.n_groups + P.B - W.first;
-    e = plan.stream_rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
-        : plan.stream_rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
-                                 : launch_stream<E, D, 4>(P, W, maps, s);
+    switch (plan.stream_rows * 8 + plan.heads) {
+      case 16 * 8 + 4: e = launch_stream<E, D, 1, 4>(P, W, maps, early, s); break;
+      case 16 * 8 + 2: e = launch_stream<E, D, 1, 2>(P, W, maps, early, s); break;
+      case 16 * 8 + 1: e = launch_stream<E, D, 1, 1>(P, W, maps, early, s); break;
+      case 32 * 8 + 2: e = launch_stream<E, D, 2, 2>(P, W, maps, early, s); break;
+      case 32 * 8 + 1: e = launch_stream<E, D, 2, 1>(P, W, maps, early, s); break;
+      default: e = launch_stream<E, D, 4, 1>(P, W, maps, early, s);
+    }
     if (e != cudaSuccess) return e;
   }
+  JoinShape shape;
+  for (int i = 0; i < 2; ++i) {
+    const bool tc = i ? plan.tc_suffix : plan.tc_prefix;
+    shape.rows[i] = tc ? kTcRows : plan.stream_rows;
+    shape.heads[i] = tc ? 1 : plan.heads;
+  }
   const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
-  join_kernel<E, D><<<(unsigned)((out_rows + 7) / 8), 256, 0, s>>>(P, W, plan.tc_prefix ? kTcRows : plan.stream_rows,
-                                                                   plan.tc_suffix ? kTcRows : plan.stream_rows);
-  return cudaGetLastError();
+  const Launch at((unsigned)((out_rows + 7) / 8), 256, 0, s, true);
+  return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
 }
 
 }  // namespace
 
-cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps) {
+cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps) {
   using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -484,22 +599,27 @@ cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps) {
   const cuuint64_t dim[4] = {(cuuint64_t)kv.d, (cuuint64_t)pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
   const cuuint64_t stride[3] = {(cuuint64_t)kv.token_stride * 2, (cuuint64_t)kv.head_stride * 2,
                                 (cuuint64_t)kv.page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(pt < kBoxTokens ? pt : kBoxTokens), 1, 1};
   const cuuint32_t step[4] = {1, 1, 1, 1};
   const auto type = kv.dtype == PW_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  for (int i = 0; i < 2; ++i)
-    if (enc(i ? &maps->v : &maps->k, type, 4, i ? kv.v : kv.k, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+  for (int heads = 1; heads <= 4; heads *= 2) {
+    const int tokens = kBoxTokens / heads;
+    if (heads > 1 && (kv.hkv % heads || pt < tokens)) continue;  // never asked for
+    KvMaps* m = heads == 1 ? &maps->heads1 : heads == 2 ? &maps->heads2 : &maps->heads4;
+    const cuuint32_t box[4] = {64, (cuuint32_t)(pt < tokens ? pt : tokens), (cuuint32_t)heads, 1};
+    for (int i = 0; i < 2; ++i)
+      if (enc(i ? &m->v : &m->k, type, 4, i ? kv.v : kv.k, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+  }
   return cudaSuccess;
 }
 
 size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups) {
-  return Layout(Plan(kv.hq / kv.hkv, B, ql, n_groups), kv.hq, kv.d, B, ql).total;
+  return Layout(Plan(kv.hq / kv.hkv, kv.hkv, B, ql, n_groups), kv.hq, kv.d, B, ql).total;
 }
 
-cudaError_t launch_attend(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s) {
+cudaError_t launch_attend(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {
   if (P.kv.dtype == PW_F16)
     return P.kv.d == 128 ? launch_typed<__half, 128>(P, maps, ws, s) : launch_typed<__half, 64>(P, maps, ws, s);
   return P.kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, ws, s)

@@ -16,6 +16,7 @@
 #include <cuda.h>
 
 #include "pw_serve.h"
+#include "pw_tc.cuh"
 
 namespace pw {
 
@@ -65,8 +66,52 @@ __device__ __forceinline__ Item attend_item(const AttendParams& P, int i, bool f
   return it;
 }
 
-// A CTA's walk over its range of the line.
-template <int ROWS, int TILE, int COST>
+// One piece of work, as the producer hands it to the CTA's other warps.
+struct __align__(16) Piece {
+  int tok0, nrows, len, causal;   // the item
+  int head, row0;                 // first key head, first row of the row tile
+  int tile0, tile1;               // key tiles; none (tile1 = 0) ends the CTA's range
+  int first;                      // holds the segment's first tile
+  int last_cta;                   // CTA that holds its last one
+  int prefix, pad;
+};
+
+constexpr int kPieces = 4;        // pieces announced ahead
+
+// Shared-memory ring of pieces: the producer writes, every reader warp takes each.
+struct PieceRing {
+  uint32_t full, empty;           // mbarriers (kPieces each)
+  Piece* at;
+  volatile int* abort_flag;
+  int* err;
+  unsigned n = 0;                 // pieces written or taken so far
+
+  // Producer, one lane.
+  __device__ __forceinline__ bool put(const Piece& p) {
+    const unsigned i = n % kPieces;
+    if (!mbar_wait(empty + 8 * i, ((n / kPieces) & 1) ^ 1, abort_flag, err)) return false;
+    at[i] = p;
+    mbar_arrive(full + 8 * i);
+    ++n;
+    return true;
+  }
+  // Reader, whole warp (or one thread of a warp that reads alone).
+  template <bool WARP>
+  __device__ __forceinline__ bool take(Piece& p) {
+    const unsigned i = n % kPieces;
+    bool ok = mbar_wait(full + 8 * i, (n / kPieces) & 1, abort_flag, err);
+    if (WARP) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    p = at[i];
+    if (WARP) __syncwarp();
+    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * i);
+    ++n;
+    return p.tile1 > 0;
+  }
+};
+
+// A CTA's walk over its range of the line.  Segments hold HB key heads.
+template <int ROWS, int TILE, int COST, int HB>
 struct AttendWalk {
   int item;             // current item
   unsigned off;         // units of the item before the current position
@@ -77,10 +122,10 @@ struct AttendWalk {
 
   static __device__ __forceinline__ unsigned units(const AttendParams& P, const Item& it) {
     if (it.len == 0 || it.nrows == 0) return 0;
-    return (unsigned)((it.len + TILE - 1) / TILE + COST) * ((it.nrows + ROWS - 1) / ROWS) * P.kv.hkv;
+    return (unsigned)((it.len + TILE - 1) / TILE + COST) * ((it.nrows + ROWS - 1) / ROWS) * (P.kv.hkv / HB);
   }
 
-  // Whole CTA: finds the CTA's range.  scratch: 64 words of shared memory.
+  // Whole CTA: finds the CTA's range.  scratch: 34 words of shared memory.
   __device__ __forceinline__ void start(const AttendParams& P, const AttendWork& W, unsigned* scratch) {
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (W.count + nt - 1) / nt;
@@ -124,40 +169,39 @@ struct AttendWalk {
     pos = u0;
   }
 
-  struct Piece {
-    Item it;
-    int head, row0;       // key head, first row of the row tile
-    int tile0, tile1;     // key tiles
-    bool first;           // holds the segment's first tile
-    int last_cta;         // CTA that holds its last one
-    bool prefix;
-  };
-
-  // The next piece with tiles in it; false at the end of the range.
-  __device__ __forceinline__ bool next(const AttendParams& P, Piece& p) {
+  // The next piece with tiles in it and its item's page table; false (and a piece without tiles) at the end of the range.
+  __device__ __forceinline__ bool next(const AttendParams& P, Piece& p, const int*& table) {
+    p.tile1 = 0;
     while (left > 0) {
-      p.it = attend_item(P, item, false);
-      const unsigned n = units(P, p.it);
+      const Item it = attend_item(P, item, false);
+      const unsigned n = units(P, it);
       if (off >= n) {
         ++item;
         off = 0;
         continue;
       }
-      const int kt = (p.it.len + TILE - 1) / TILE, rt = (p.it.nrows + ROWS - 1) / ROWS;
+      const int kt = (it.len + TILE - 1) / TILE, rt = (it.nrows + ROWS - 1) / ROWS;
       const unsigned su = kt + COST, seg = off / su, within = off - seg * su;
       const unsigned take = min(su - within, left), end = within + take;
-      p.head = seg / rt;
-      p.row0 = (seg - p.head * rt) * ROWS;
-      p.tile0 = within > COST ? within - COST : 0;
-      p.tile1 = end > COST ? end - COST : 0;
-      p.first = within <= COST;
-      p.prefix = item < P.n_groups;
       const unsigned seg_end = pos - within + su;  // the segment's end on the line
-      p.last_cta = (int)(((unsigned long long)seg_end * ctas + total - 1) / total) - 1;
       off += take;
       pos += take;
       left -= take;
-      if (p.tile1 > p.tile0) return true;
+      if (end <= COST) continue;
+      p.tok0 = it.tok0;
+      p.nrows = it.nrows;
+      p.len = it.len;
+      p.causal = it.causal;
+      p.head = seg / rt;
+      p.row0 = (seg - p.head * rt) * ROWS;
+      p.head *= HB;
+      p.tile0 = within > COST ? within - COST : 0;
+      p.tile1 = end - COST;
+      p.first = within <= COST;
+      p.last_cta = (int)(((unsigned long long)seg_end * ctas + total - 1) / total) - 1;
+      p.prefix = item < P.n_groups;
+      table = it.table;
+      return true;
     }
     return false;
   }
@@ -183,7 +227,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The tensor-core kernel for prefix groups with many rows (pw_attend_tc.cu).
 constexpr int kTcRows = 256;
-cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const KvMaps& maps, cudaStream_t s);
+cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const KvMaps& maps, int ctas, cudaStream_t s);
 int attend_tc_ctas();
 
 }  // namespace pw

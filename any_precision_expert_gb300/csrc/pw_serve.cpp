@@ -9,7 +9,7 @@ using namespace pw;
 
 struct pw_kv_s {
   KvView view;
-  KvMaps maps;
+  KvMapSet maps;
 };
 
 namespace {
@@ -115,7 +115,7 @@ extern "C" pw_status pw_kv_create(const pw_kv_desc* desc, void* k, void* v, int3
   w.page_stride = desc->page_stride;
   w.head_stride = desc->head_stride;
   w.token_stride = desc->token_stride;
-  KvMaps maps = {};
+  KvMapSet maps = {};
   if (!host_sim()) {
     const cudaError_t e = encode_kv_maps(w, &maps);
     if (e != cudaSuccess) return record_cuda_error(e);

@@ -69,13 +69,17 @@ struct VerifyParams {
 
 cudaError_t launch_rope(const RopeParams& P, int dtype, int d, cudaStream_t s);
 size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups);
-// Tensor maps of a cache's keys and values: (value, token of a page, head, page), boxes of 64 values x up to 64 tokens.
+// Tensor maps of a cache's keys and values: (value, token of a page, head, page).
 struct KvMaps {
   CUtensorMap k, v;
 };
+// Boxes of 64 values x up to 64 / heads tokens x 1, 2 or 4 heads (the latter where they divide the key heads).
+struct KvMapSet {
+  KvMaps heads1, heads2, heads4;
+};
 constexpr int kBoxTokens = 64;
-cudaError_t encode_kv_maps(const KvView& kv, KvMaps* maps);
-cudaError_t launch_attend(const AttendParams& P, const KvMaps& maps, void* ws, cudaStream_t s);
+cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps);
+cudaError_t launch_attend(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s);
 cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s);
 
 }  // namespace pw
