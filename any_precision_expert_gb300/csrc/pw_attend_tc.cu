@@ -9,9 +9,9 @@
 // A operand.
 //
 // Warps: two softmax warpgroups (one a row tile, one row a thread, so row
-// maxima and sums need no exchange), a TMA producer and one MMA thread.  While
-// one tile's softmax runs, the tensor cores work on the other tile:
-//   PV0(n) QK0(n+1) PV1(n) QK1(n+1) PV0(n+1) ...
+// maxima and sums need no exchange), a TMA producer and one MMA thread a row
+// tile.  While one tile's softmax runs, the tensor cores work on the other:
+//   PV0(n) QK0(n+1) | PV1(n) QK1(n+1) | PV0(n+1) ...
 // O is rescaled only when a row's maximum has grown by more than 2^kGrow since
 // the last time; until then the weights may reach 2^(kShift + kGrow), which
 // fp16 still holds, and nothing is lost: the reference cancels in o / l.
@@ -42,7 +42,7 @@ struct Cfg {
   static constexpr int RING_AT = 2 * SLOT;
   static constexpr int SLOTS = (226 * 1024 - RING_AT) / SLOT;
   static constexpr int BAR_AT = RING_AT + SLOTS * SLOT;
-  static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 96;
+  static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 112;
   static constexpr int SCRATCH_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
   static constexpr int SMEM = SCRATCH_AT + 144;
   static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
@@ -60,7 +60,7 @@ struct Tiles {
   __device__ __forceinline__ bool next(PieceRing& ring) {
     first = false;
     if (++t < pc.tile1) return true;
-    if (!ring.take<false>(pc)) return false;
+    if (!ring.take<true>(pc)) return false;
     t = pc.tile0;
     first = true;
     return true;
@@ -71,6 +71,12 @@ template <typename E>
 __host__ __device__ constexpr uint32_t idesc_of(int n, bool b_outer) {
   const uint32_t type = __is_same(E, __half) ? 0u : 1u;
   return idesc_f16(128, n) | (type << 7) | (type << 10) | ((b_outer ? 1u : 0u) << 16);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
 
 // Two fp32 operations in one instruction.
@@ -90,11 +96,98 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 32 bytes: a whole sector a lane.
 __device__ __forceinline__ void store8(float* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// The MMA warp of row tile I.  One warp a row tile, so that neither tile waits for the other's weights and the cost of
+// issuing is shared (an instruction of 128 x 128 x 16 takes the tensor cores 64 cycles, about what issuing one takes).
+// The whole warp walks, one lane issues: what the instructions take is then the same in every lane.
+template <typename E, int D, int I>
+__device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t full, uint32_t empty, uint32_t bars,
+                                         uint32_t tmem, volatile int* abort_flag, int* err) {
+  using C = Cfg<D>;
+  constexpr uint32_t id_qk = idesc_of<E>(kTile, false), id_pv = idesc_of<E>(D, true);
+  const uint32_t q_full = bars + 8 * I, s_full = bars + 16 + 8 * I, p_full = bars + 32 + 16 * I, o_done = bars + 64 + 8 * I;
+  const uint32_t ts = tmem + C::S_COL + I * 128, to = tmem + C::O_COL + I * 128;
+  const uint64_t q = sw128_desc(base + C::Q_AT + I * C::SLOT), k0 = sw128_desc(base + C::RING_AT);
+  const uint64_t v0 = sw128_desc_outer(base + C::RING_AT, C::HALF);
+  const uint32_t q_lo = (uint32_t)q, k_hi = (uint32_t)(k0 >> 32), v_hi = (uint32_t)(v0 >> 32);
+  const bool leader = elect_one();
+  unsigned qn = 0, pn = 0;     // phases of q_full and p_full waited for so far
+  unsigned slot = 0, par = 0;  // ring slot of the next keys or values, and its phase
+  Tiles it;
+  it.pc.tile1 = 0;
+  auto wait = [&](uint32_t bar, unsigned parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, err)) != 0;
+  };
+  bool have = it.next(ring), act = false, first = false;
+  unsigned vs = 0, vp = 0;     // the current tile's values
+  bool run = false;            // a tile is waiting for its weights
+  while (have || run) {
+    const bool k_act = have && active(it.pc, I);
+    const unsigned ks = slot, kp = par;
+    if (have) {
+      if (++slot == C::SLOTS) slot = 0, par ^= 1;
+      if (k_act && it.first && !wait(q_full, qn++)) return;
+      if (!wait(full + 8 * ks, kp)) return;   // also of keys that this tile has no use for: an arrival belongs to their phase
+    }
+    if (run) {
+      if (!wait(full + 8 * vs, vp)) return;
+      if (act) {  // O (+)= P V, as the halves of P come
+        const uint32_t v_lo = (uint32_t)v0 + vs * (C::SLOT >> 4);
+        if (!wait(p_full, pn)) return;
+        tc_fence_after();
+        if (leader) {
+          umma_ts_lo(to, ts, v_lo, v_hi, id_pv, !first);
+#pragma unroll
+          for (int c = 1; c < 4; ++c) umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, 1);
+        }
+        __syncwarp();
+        if (!wait(p_full + 8, pn++)) return;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int c = 4; c < 8; ++c) umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, 1);
+        }
+      }
+    }
+    tc_fence_after();
+    if (leader) {
+      if (k_act) {  // S = Q K^T; in order behind the product that reads the weights in its place
+        const uint32_t k_lo = (uint32_t)k0 + ks * (C::SLOT >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t step = (c / 4) * (C::HALF >> 4) + 2 * (c % 4);
+          umma_f16_lo(ts, q_lo + step, k_hi, k_lo + step, k_hi, id_qk, c != 0);
+        }
+        umma_commit(s_full);
+      }
+      if (run) {
+        if (act && (!have || it.first)) umma_commit(o_done);  // the piece's last tile
+        umma_commit(empty + 8 * vs);
+      }
+      if (have) umma_commit(empty + 8 * ks);
+    }
+    __syncwarp();
+    run = have;
+    act = k_act;
+    first = it.first;
+    if (have) {
+      vs = slot, vp = par;
+      if (++slot == C::SLOTS) slot = 0, par ^= 1;
+      have = it.next(ring);
+    }
+  }
 }
 
 template <typename E, int D>
@@ -105,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::SLOTS, bars = empty + 8 * C::SLOTS + 16 * kPieces;
   // p_full: two halves (64 keys) of each row tile's weights
-  const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_done = bars + 64;
+  const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_done = bars + 64, turn = bars + 80;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 16);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::PIECE_AT - 8);
   int* err = P.kv.err;
@@ -123,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(ring.full + 8 * i, 1);
-      mbar_init(ring.empty + 8 * i, 9);  // eight softmax warps and the MMA thread
+      mbar_init(ring.empty + 8 * i, 10);  // eight softmax warps and the MMA threads
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 128);
@@ -135,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + 8 * i, 128);
       mbar_init(p_full + 16 + 8 * i, 128);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(turn + 8 * i, 128);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -175,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     unsigned n = 0;     // tiles of this warpgroup so far
     unsigned flat = 0;  // tiles of the CTA so far
+    unsigned turns = 0, done = 0;  // turns taken, pieces finished
     bool ok = true;
     auto advance = [&]() {  // to the next piece with rows of this tile
       while (ring.take<true>(pc)) {
@@ -190,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = cur.row0 + 128 * i + r;
       const int tok = min(row, cur.nrows - 1) / P.G;
       const int vis = cur.causal ? cur.len - P.ql + 1 + tok : cur.len;  // keys this row sees
+      const bool both = active(cur, 1);
       float m = -CUDART_INF_F;
       float2 l = make_float2(0.f, 0.f);
       for (int t = cur.tile0; t < cur.tile1; ++t, ++n, ++flat) {
@@ -198,6 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t s[128];
         tmem_load128(ts, s);
+        if (both) {  // the warpgroups take turns, so that one's softmax meets the other's products
+          ok = __all_sync(0xffffffffu, mbar_wait(turn + 8 * i, (turns & 1) ^ (i ^ 1), abort_flag, err));
+          if (!ok) break;
+          ++turns;
+        }
         const int see = vis - t * kTile;
         const bool edge = __any_sync(0xffffffffu, see < kTile);
         float top = -CUDART_INF_F;
@@ -212,12 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           float t1 = -CUDART_INF_F, t2 = t1, t3 = t1;
 #pragma unroll
           for (int k = 0; k < 128; k += 8) {
-            top = fmaxf(fmaxf(top, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
-            t1 = fmaxf(fmaxf(t1, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
-            t2 = fmaxf(fmaxf(t2, __uint_as_float(s[k + 4])), __uint_as_float(s[k + 5]));
-            t3 = fmaxf(fmaxf(t3, __uint_as_float(s[k + 6])), __uint_as_float(s[k + 7]));
+            top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+            t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+            t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+            t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
           }
-          top = fmaxf(fmaxf(top, t1), fmaxf(t2, t3));
+          top = fmaxf(max3(top, t1, t2), t3);
         }
         top = top == -CUDART_INF_F ? top : top * scale2 - kShift;
         if (t == cur.tile0) {
@@ -226,9 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mm = fmaxf(m, top), f = mm == -CUDART_INF_F ? 1.f : ex2(m - mm);
           m = mm;
           l.x *= f, l.y *= f;
-          ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, (n - 1) & 1, abort_flag, err));
-          if (!ok) break;
-          tc_fence_after();
+          // these scores were issued behind the last product into O: it is done
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -252,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[k / 2] = pack2<E>(a.x, a.y);
           }
           tmem_store32(ts + 32 * h, p);
-          if (h == 0 && i == 0 && cur.len - t * kTile < kTile) {
-            // values past the length may be anything: 0 instead (one key a thread)
+          if (h == 0 && cur.len - t * kTile < kTile) {
+            // values past the length may be anything: 0 instead (one key a thread, both warpgroups alike)
             const unsigned slot = 2 * flat + 1;
             ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
             if (!ok) break;
@@ -271,12 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(p_full + 16 * i + 8 * h);
         }
         if (!ok) break;
+        if (both) mbar_arrive(turn + 8 * (i ^ 1));
       }
       if (!ok) break;
       // the last S is out of the queries' way: the next piece's queries go in before this one's sums come out
       have = advance();
       if (have) load_q();
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, (n - 1) & 1, abort_flag, err));
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
       const AttendPieces& dst = cur.prefix ? W.prefix : W.suffix;
@@ -345,77 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 9) {
-      if (lane == 0) {
-        // ---- MMA ----
-        constexpr uint32_t id_qk = idesc_of<E>(kTile, false), id_pv = idesc_of<E>(D, true);
-        unsigned qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of q_full and p_full waited for so far
-        unsigned x = 0;                           // tiles whose keys have been multiplied
-        bool ok = true;
-        Tiles it;
-        it.pc.tile1 = 0;
-        auto landed = [&](unsigned s) {
-          return mbar_wait(full + 8 * (s % C::SLOTS), (s / C::SLOTS) & 1, abort_flag, err);
-        };
-        auto qk = [&](int i, unsigned tile) {     // S_i = Q_i K^T
-          const uint64_t q = sw128_desc(base + C::Q_AT + i * C::SLOT);
-          const uint64_t k = sw128_desc(base + C::RING_AT + (2 * tile % C::SLOTS) * C::SLOT);
-  #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint32_t at = (c / 4) * (C::HALF >> 4) + 2 * (c % 4);
-            umma_f16(tmem + C::S_COL + i * 128, q + at, k + at, id_qk, c != 0);
-          }
-          umma_commit(s_full + 8 * i);
-        };
-        auto pv = [&](int i, unsigned tile, bool first) {  // O_i (+)= P_i V, as the halves of P come
-          const uint64_t v = sw128_desc_outer(base + C::RING_AT + ((2 * tile + 1) % C::SLOTS) * C::SLOT, C::HALF);
-          for (int h = 0; h < 2; ++h) {
-            if (!mbar_wait(p_full + 16 * i + 8 * h, pn[i] & 1, abort_flag, err)) return false;
-            if (h == 0 && i == 0 && !landed(2 * tile + 1)) return false;
-            tc_fence_after();
-  #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              umma_ts(tmem + C::O_COL + i * 128, tmem + C::S_COL + i * 128 + 32 * h + 8 * c, v + 512 * h + 128 * c, id_pv,
-                      !first || h + c != 0);
-          }
-          ++pn[i];
-          umma_commit(o_done + 8 * i);
-          return true;
-        };
-        bool have = it.next(ring);
-        if (have) {
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (!active(it.pc, i)) continue;
-            ok = mbar_wait(q_full + 8 * i, qn[i]++ & 1, abort_flag, err) && landed(0);
-            tc_fence_after();
-            if (ok) qk(i, 0);
-          }
-          umma_commit(empty);
-        }
-        while (ok && have) {
-          const bool second = active(it.pc, 1), first = it.first;
-          const unsigned tile = x++;
-          have = it.next(ring);
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (i == 0 || second) ok = pv(i, tile, first);
-            if (ok && have && active(it.pc, i)) {
-              if (it.first) ok = mbar_wait(q_full + 8 * i, qn[i]++ & 1, abort_flag, err);
-              ok = ok && (i > 0 || landed(2 * x));
-              tc_fence_after();
-              if (ok) qk(i, x);
-            }
-          }
-          umma_commit(empty + 8 * ((2 * tile + 1) % C::SLOTS));
-          if (have) umma_commit(empty + 8 * (2 * x % C::SLOTS));
-        }
-      }
-      __syncwarp();
+      mma_role<E, D, 0>(ring, base, full, empty, bars, tmem, abort_flag, err);
+    } else if (warp == 10) {
+      mma_role<E, D, 1>(ring, base, full, empty, bars, tmem, abort_flag, err);
     }
   }
   // ---- teardown: every MMA has completed or the wait for it has run out ----
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && warp == 9 && lane == 0) {
-    umma_commit(q_full);  // arrives when the products issued so far are done
+  if (*abort_flag && tid == 0) {  // products issued before the wait ran out end well within this time
     const long long t0 = clock64();
     while (clock64() - t0 < 1000000) {
     }
