@@ -372,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// How the prefix and suffix kernels cut rows: rows and heads of a segment.
+// How the prefix and suffix kernels cut rows: rows and heads of a segment, and CTAs.
 struct JoinShape {
-  int rows[2], heads[2];
+  int rows[2], heads[2], ctas[2];
 };
 
 // Joins a row's pieces: one warp a (query token, head).
@@ -406,9 +406,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   // Pieces of a segment: the first in the row's own place, the others in the slots of the CTAs after it.  Eight at a
   // time: their (m, l) in eight lanes, then their values, all loads of a step in flight together.
-  auto pieces = [&](const AttendPieces& from, int rows, int heads, int local) {
+  auto pieces = [&](const AttendPieces& from, int rows, int heads, int slots, int local) {
     const float4 a = from.row_ml[row];
-    const int c0 = __float_as_int(a.z), n = __float_as_int(a.w) - c0 + 1;
+    // CTAs inside the slots whatever a kernel that gave up on a wait has left there
+    const int c0 = min(max(__float_as_int(a.z), 0), slots - 1), n = min(max(__float_as_int(a.w), c0), slots - 1) - c0 + 1;
     const long long slot = ((long long)c0 * heads + h / P.G % heads) * rows + local, step = (long long)heads * rows;
     for (int p0 = 0; p0 < n; p0 += 8) {
       const int p = p0 + (lane & 7);
@@ -460,8 +461,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
   const bool pre = grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0;
   const bool suf = min(P.lens[b], P.table_stride << P.kv.page_shift) > 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
-  if (pre) pieces(W.prefix, shape.rows[0], shape.heads[0], ((n - tok0) * P.G + hl) % shape.rows[0]);
-  if (suf) pieces(W.suffix, shape.rows[1], shape.heads[1], ((n - b * P.ql) * P.G + hl) % shape.rows[1]);
+  if (pre) pieces(W.prefix, shape.rows[0], shape.heads[0], shape.ctas[0], ((n - tok0) * P.G + hl) % shape.rows[0]);
+  if (suf) pieces(W.suffix, shape.rows[1], shape.heads[1], shape.ctas[1], ((n - b * P.ql) * P.G + hl) % shape.rows[1]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + lane * PER;
 #pragma unroll
@@ -581,6 +582,7 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     const bool tc = i ? plan.tc_suffix : plan.tc_prefix;
     shape.rows[i] = tc ? kTcRows : plan.stream_rows;
     shape.heads[i] = tc ? 1 : plan.heads;
+    shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
   const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
   const Launch at((unsigned)((out_rows + 7) / 8), 256, 0, s, true);

@@ -8,9 +8,8 @@
 // the place of S, two 16-bit weights a column, and is read from there as the
 // A operand.
 //
-// Warps: two softmax warpgroups (one a row tile, one row a thread, so row
-// maxima and sums need no exchange), a TMA producer and one MMA thread a row
-// tile.  While one tile's softmax runs, the tensor cores work on the other:
+// Warps: a softmax warpgroup a row tile (one row a thread, so row maxima and
+// sums need no exchange), a TMA producer and one MMA warp a row tile.  While one tile's softmax runs, the tensor cores work on the other:
 //   PV0(n) QK0(n+1) | PV1(n) QK1(n+1) | PV0(n+1) ...
 // O is rescaled only when a row's maximum has grown by more than 2^kGrow since
 // the last time; until then the weights may reach 2^(kShift + kGrow), which
@@ -26,10 +25,12 @@ namespace pw {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile
-constexpr int kThreads = 384;
-// Registers: launched with 168 a thread; the softmax warpgroups, a row of 128 scores a thread, take what the third
-// warpgroup gives up (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+// Registers: launched with 168 a thread; the softmax warps, a row of 128 scores a thread, take what the other four give
+// up (256 * 208 + 128 * 88 = 384 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kParts = 2;            // a tile's weights are handed over in this many parts
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
 constexpr float kGrow = 8.f;
 
@@ -42,7 +43,7 @@ struct Cfg {
   static constexpr int RING_AT = 2 * SLOT;
   static constexpr int SLOTS = (226 * 1024 - RING_AT) / SLOT;
   static constexpr int BAR_AT = RING_AT + SLOTS * SLOT;
-  static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 112;
+  static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 192;
   static constexpr int SCRATCH_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
   static constexpr int SMEM = SCRATCH_AT + 144;
   static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
@@ -96,17 +97,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ uint4 load_staged(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// 32 bytes: a whole sector a lane.
-__device__ __forceinline__ void store8(float* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 
 // The MMA warp of row tile I.  One warp a row tile, so that neither tile waits for the other's weights and the cost of
@@ -117,7 +117,8 @@ __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t
                                          uint32_t tmem, volatile int* abort_flag, int* err) {
   using C = Cfg<D>;
   constexpr uint32_t id_qk = idesc_of<E>(kTile, false), id_pv = idesc_of<E>(D, true);
-  const uint32_t q_full = bars + 8 * I, s_full = bars + 16 + 8 * I, p_full = bars + 32 + 16 * I, o_done = bars + 64 + 8 * I;
+  const uint32_t q_full = bars + 8 * I, s_full = bars + 16 + 8 * I, o_done = bars + 32 + 8 * I,
+                 p_full = bars + 64 + 8 * kParts * I;
   const uint32_t ts = tmem + C::S_COL + I * 128, to = tmem + C::O_COL + I * 128;
   const uint64_t q = sw128_desc(base + C::Q_AT + I * C::SLOT), k0 = sw128_desc(base + C::RING_AT);
   const uint64_t v0 = sw128_desc_outer(base + C::RING_AT, C::HALF);
@@ -138,29 +139,32 @@ __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t
     const unsigned ks = slot, kp = par;
     if (have) {
       if (++slot == C::SLOTS) slot = 0, par ^= 1;
-      if (k_act && it.first && !wait(q_full, qn++)) return;
       if (!wait(full + 8 * ks, kp)) return;   // also of keys that this tile has no use for: an arrival belongs to their phase
     }
     if (run) {
       if (!wait(full + 8 * vs, vp)) return;
-      if (act) {  // O (+)= P V, as the halves of P come
+      if (act) {  // O (+)= P V
         const uint32_t v_lo = (uint32_t)v0 + vs * (C::SLOT >> 4);
-        if (!wait(p_full, pn)) return;
-        tc_fence_after();
-        if (leader) {
-          umma_ts_lo(to, ts, v_lo, v_hi, id_pv, !first);
 #pragma unroll
-          for (int c = 1; c < 4; ++c) umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, 1);
-        }
-        __syncwarp();
-        if (!wait(p_full + 8, pn++)) return;
-        tc_fence_after();
-        if (leader) {
+        for (int h = 0; h < kParts; ++h) {  // as the parts of P come
+          if (!wait(p_full + 8 * h, pn)) return;
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int c = 4; c < 8; ++c) umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, 1);
+            for (int c = 8 / kParts * h; c < 8 / kParts * (h + 1); ++c)
+              umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, c > 0 || !first);
+          }
+          __syncwarp();
         }
+        ++pn;
       }
     }
+    // a piece's queries come once the sums of the one before are out, so not before its last product is issued
+    if (run && act && (!have || it.first)) {
+      if (leader) umma_commit(o_done);
+      __syncwarp();
+    }
+    if (k_act && it.first && !wait(q_full, qn++)) return;
     tc_fence_after();
     if (leader) {
       if (k_act) {  // S = Q K^T; in order behind the product that reads the weights in its place
@@ -172,10 +176,7 @@ __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t
         }
         umma_commit(s_full);
       }
-      if (run) {
-        if (act && (!have || it.first)) umma_commit(o_done);  // the piece's last tile
-        umma_commit(empty + 8 * vs);
-      }
+      if (run) umma_commit(empty + 8 * vs);
       if (have) umma_commit(empty + 8 * ks);
     }
     __syncwarp();
@@ -197,8 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::SLOTS, bars = empty + 8 * C::SLOTS + 16 * kPieces;
-  // p_full: two halves (64 keys) of each row tile's weights
-  const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_done = bars + 64, turn = bars + 80;
+  const uint32_t q_full = bars, s_full = bars + 16, o_done = bars + 32, turn = bars + 48, p_full = bars + 64;  // p_full: [row tile][part]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 16);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::PIECE_AT - 8);
   int* err = P.kv.err;
@@ -220,15 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(ring.full + 8 * i, 1);
-      mbar_init(ring.empty + 8 * i, 10);  // eight softmax warps and the MMA threads
+      mbar_init(ring.empty + 8 * i, kSoftmaxWarps + 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 128);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 128);
-      mbar_init(p_full + 16 + 8 * i, 128);
       mbar_init(o_done + 8 * i, 1);
       mbar_init(turn + 8 * i, 128);
+      for (int k = 0; k < kParts; ++k) mbar_init(p_full + 8 * (kParts * i + k), 128);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -242,32 +241,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
 
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax: warpgroup i holds row tile i, one row a thread ----
-    const int i = warp >> 2, r = tid & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const int i = warp >> 2, w4 = warp & 3, r = tid & 127;
+    const uint32_t lanes = (uint32_t)w4 << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + C::S_COL + i * 128, to = tmem + lanes + C::O_COL + i * 128;
     // a negative scale turns the queries around, a scale of 0 takes them away
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = P.scale == 0.f ? 0u : 0xffffffffu;
     const float scale2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
-    const uint32_t q_at = base + C::Q_AT + i * C::SLOT + r * 128;
     Piece pc = {};
-    auto load_q = [&]() {
-      const int row = pc.row0 + 128 * i + r;
-      const bool in = row < pc.nrows;
-      const int tok = in ? row / P.G : 0, hd = in ? pc.head * P.G + row - tok * P.G : 0;
-      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride;
+    // Queries: a warp brings its 32 rows, whole lines at a time.
+    constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 32 / RPS;  // lanes a row, rows a step, steps
+    const int q_row = 32 * w4, q_sub = lane / LPR, q_col = lane % LPR;
+    const uint32_t q_base = base + C::Q_AT + i * C::SLOT;
+    auto q_src = [&](int k) {  // null past the rows
+      const int row = pc.row0 + 128 * i + q_row + k * RPS + q_sub, tok = row / P.G;
+      return row < pc.nrows ? static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
+                                  (pc.head * P.G + row - tok * P.G) * P.q.head_stride + 8 * q_col
+                            : nullptr;
+    };
+    auto call_q = [&]() {  // to the L2, while the piece before still runs
+#pragma unroll 1
+      for (int k = 0; k < STEPS; ++k) {
+        const E* src = q_src(k);
+        if (src && (q_col & 1) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+      }
+    };
+    auto place_q = [&]() {
+      uint4 qv[STEPS];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 v = in ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-        v = make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep);
-        sts128(q_at + (c / 8) * C::HALF + (((c & 7) ^ (r & 7)) << 4), v);
+      for (int k = 0; k < STEPS; ++k) {
+        const E* src = q_src(k);
+        qv[k] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const int at = q_row + k * RPS + q_sub;
+        const uint4 v = qv[k];
+        sts128(q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4),
+               make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep));
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full + 8 * i);
     };
-    unsigned n = 0;     // tiles of this warpgroup so far
+    unsigned n = 0;     // tiles of this row tile so far
     unsigned flat = 0;  // tiles of the CTA so far
     unsigned turns = 0, done = 0;  // turns taken, pieces finished
     bool ok = true;
@@ -279,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return false;
     };
     bool have = advance();
-    if (have) load_q();
+    if (have) place_q();
     while (have && ok) {
       const Piece cur = pc;
       const int row = cur.row0 + 128 * i + r;
@@ -300,9 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++turns;
         }
         const int see = vis - t * kTile;
-        const bool edge = __any_sync(0xffffffffu, see < kTile);
         float top = -CUDART_INF_F;
-        if (edge) {
+        if (__any_sync(0xffffffffu, see < kTile)) {
           // what a row does not see counts as -infinity: a weight of 0
 #pragma unroll
           for (int k = 0; k < 128; ++k) {
@@ -329,53 +346,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           l.x *= f, l.y *= f;
           // these scores were issued behind the last product into O: it is done
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_load32(to + c, o);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_load16(to + c, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_store32(to + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_store16(to + c, o);
           }
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
+        if (cur.len - t * kTile < kTile) {
+          // values past the length may be anything: 0 instead (one key a thread, every row tile for itself)
+          const unsigned slot = 2 * flat + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
+          if (!ok) break;
+          if (r >= cur.len - t * kTile) {
+            const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 64 keys: 32 columns
-          uint32_t p[32];
+            for (int b = 0; b < C::NH; ++b)
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            const int at = 64 * h + k;
+              for (int c = 0; c < 8; ++c) sts128(at + b * C::HALF + 16 * c, make_uint4(0, 0, 0, 0));
+          }
+          fence_proxy_async_smem();
+        }
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          constexpr int N = kTile / kParts;  // keys of a part, two a column
+          uint32_t p[N / 2];
+#pragma unroll
+          for (int k = 0; k < N; k += 2) {
+            const int at = N * h + k;
             float2 a = fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sc, off);
             a.x = ex2(a.x), a.y = ex2(a.y);
             l = add2(l, a);
             p[k / 2] = pack2<E>(a.x, a.y);
           }
-          tmem_store32(ts + 32 * h, p);
-          if (h == 0 && cur.len - t * kTile < kTile) {
-            // values past the length may be anything: 0 instead (one key a thread, both warpgroups alike)
-            const unsigned slot = 2 * flat + 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
-            if (!ok) break;
-            if (r >= cur.len - t * kTile) {
-              const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
 #pragma unroll
-              for (int b = 0; b < C::NH; ++b)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) sts128(at + b * C::HALF + 16 * c, make_uint4(0, 0, 0, 0));
-            }
-            fence_proxy_async_smem();
-          }
+          for (int k = 0; k < N / 2; k += 16) tmem_store16(ts + N / 2 * h + k, p + k);
           tmem_store_wait();
           tc_fence_before();
-          mbar_arrive(p_full + 16 * i + 8 * h);
+          mbar_arrive(p_full + 8 * (kParts * i + h));
         }
-        if (!ok) break;
         if (both) mbar_arrive(turn + 8 * (i ^ 1));
       }
       if (!ok) break;
-      // the last S is out of the queries' way: the next piece's queries go in before this one's sums come out
       have = advance();
-      if (have) load_q();
+      if (have) call_q();
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
@@ -383,27 +400,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in = row < cur.nrows;
       const long long grow = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + row - tok * P.G;
       const long long crow = (long long)blockIdx.x * kTcRows + 128 * i + r;
-      float* out = cur.first ? dst.row_o + grow * D : dst.cta_o + crow * D;
       if (in) {
+        const float sum = l.x + l.y;
         if (cur.first)
-          dst.row_ml[grow] = make_float4(m, l.x + l.y, __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
+          dst.row_ml[grow] = make_float4(m, sum, __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
         else
-          dst.cta_ml[crow] = make_float2(m, l.x + l.y);
+          dst.cta_ml[crow] = make_float2(m, sum);
       }
+      // Sums to rows: through the warp's own rows of the query tile (read by no product any more), so that the
+      // stores are whole lines.  CC columns at a time.
+      constexpr int CC = 32, LINE = CC / 4;  // columns a step, 16-byte words of a staged row
+      const long long my_out = !in ? -1 : (cur.first ? grow : crow);
+      float* out = cur.first ? dst.row_o : dst.cta_o;
+      const uint32_t st_base = q_base + q_row * 128;
+      auto staged = [&](int k, int word) { return st_base + k * 128 + ((word ^ (k & 7)) << 4); };
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_load32(to + c, o);
-        if (in) {
+      for (int c = 0; c < D; c += CC) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) store8(out + c + k, o + k);
+        for (int c2 = 0; c2 < CC; c2 += 16) {
+          uint32_t o[16];
+          tmem_load16(to + c + c2, o);
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            sts128(staged(lane, (c2 + k) / 4), make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]));
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 32; k += 32 / LINE) {
+          const int at = k + lane / LINE, word = lane % LINE;
+          const long long to_row = __shfl_sync(0xffffffffu, my_out, at);
+          const uint4 v = load_staged(staged(at, word));
+          if (to_row >= 0) *reinterpret_cast<uint4*>(out + to_row * D + c + 4 * word) = v;
+        }
+        __syncwarp();
       }
       tc_fence_before();
+      if (have) place_q();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
       // ---- producer: keys and values of a tile take one ring slot each; one lane a page ----
       const int shift = P.kv.page_shift, box = min(1 << shift, kBoxTokens);
       unsigned x = 0;  // slots filled so far
@@ -444,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; fills > 0 && k < (1 << 16) && !mbar_try_wait(full + 8 * i, (fills - 1) & 1); ++k) {
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == kSoftmaxWarps + 1) {
       mma_role<E, D, 0>(ring, base, full, empty, bars, tmem, abort_flag, err);
-    } else if (warp == 10) {
+    } else if (warp == kSoftmaxWarps + 2) {
       mma_role<E, D, 1>(ring, base, full, empty, bars, tmem, abort_flag, err);
     }
   }

@@ -244,6 +244,22 @@ def test_attend_matches_oracle(i, dt):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("lens,plens,off,hq,hkv,D,ql", [
+    # more segments than CTAs, so that every CTA takes several: of many rows (groups of 80 and 40 rows a key head)
+    ([9, 5] * 40, [150 + 7 * i for i in range(40)], [2 * i for i in range(40)] + [80], 64, 8, 64, 5),
+    ([5] * 60, [300] * 12 + [64, 1, 0, 129, 128, 127, 2, 500], [3 * i for i in range(21)], 64, 16, 128, 5),
+    # and of few
+    ([i % 90 for i in range(400)], [], None, 16, 4, 64, 1),
+    ([i % 70 for i in range(200)], [33], None, 12, 6, 128, 2),
+    ([2 + i % 50 for i in range(120)], [40, 1], [0, 70, 120], 21, 3, 64, 2)])
+def test_attend_several_segments_a_cta(lens, plens, off, hq, hkv, D, ql):
+    c = Case(np.random.default_rng(len(lens)), lens, plens, off, hq, hkv, D, 16, torch.float16, ql)
+    out, lse = c.run()
+    c.check(out, lse)
+    assert c.cache.check_device() == 0
+    assert torch.equal(out, c.run(lse=False)[0])
+
+
 def test_attend_strided_queries_and_a_wide_table():
     rng = np.random.default_rng(50)
     c = Case(rng, [20, 3, 150], [90], None, 8, 2, 128, 16, torch.float16, width=40)
