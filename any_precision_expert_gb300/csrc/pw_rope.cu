@@ -20,7 +20,7 @@ namespace pw {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // smaller CTAs, so that the ends of some overlap the loads of others
 
 // Row chunks of a token: queries, keys, values.
 struct Chunks {
@@ -33,6 +33,13 @@ struct Chunks {
 template <typename E>
 __device__ __forceinline__ void load_pair(const E* p, int a0, int a1, uint4& r) {
   const uint2 lo = *reinterpret_cast<const uint2*>(p + a0), hi = *reinterpret_cast<const uint2*>(p + a1);
+  r = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+
+// The same of a row that is read once: its lines are the first to leave the L2.
+template <typename E>
+__device__ __forceinline__ void stream_pair(const E* p, int a0, int a1, uint4& r) {
+  const uint2 lo = __ldcs(reinterpret_cast<const uint2*>(p + a0)), hi = __ldcs(reinterpret_cast<const uint2*>(p + a1));
   r = make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
@@ -61,7 +68,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
   for (int i = 0; i < U; ++i) {
     const int h = h0 + i * RPW;
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (h < nrows) load_pair(src + h * in.head_stride, a0, a1, raw[i]);
+    if (h < nrows) stream_pair(src + h * in.head_stride, a0, a1, raw[i]);
   }
   E* dst;
   long long dst_stride;
@@ -132,8 +139,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
     const int h = h0 + i * RPW;
     if (h >= nrows) continue;
     E* to = dst + h * dst_stride;
-    *reinterpret_cast<uint2*>(to + a0) = make_uint2(raw[i].x, raw[i].y);
-    *reinterpret_cast<uint2*>(to + a1) = make_uint2(raw[i].z, raw[i].w);
+    __stcs(reinterpret_cast<uint2*>(to + a0), make_uint2(raw[i].x, raw[i].y));
+    __stcs(reinterpret_cast<uint2*>(to + a1), make_uint2(raw[i].z, raw[i].w));
   }
 }
 
