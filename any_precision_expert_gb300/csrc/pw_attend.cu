@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int ROWS = 16 * MT, KS = kComputeWarps / (MT * HB), TILE = kStageKeys / HB, KPW = TILE / KS;
   constexpr int HEAD = TILE * 128;  // bytes of one head's rows in a column block
   // a segment's fixed cost in key tiles: about one 64-key tile's time
-  using Walk = AttendWalk<ROWS, TILE, HB, HB>;
+  using Walk = AttendWalk<ROWS, TILE, HB, HB, 1>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
@@ -101,18 +101,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
   ring.abort_flag = abort_flag;
   ring.err = P.kv.err;
-  if (tid == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, kComputeWarps);
-    }
-    for (int i = 0; i < kPieces; ++i) {
-      mbar_init(ring.full + 8 * i, 1);
-      mbar_init(ring.empty + 8 * i, kComputeWarps);
-    }
-    *abort_flag = 0;
+  if (tid < 2 * (C::STAGES + kPieces)) {  // one thread a barrier: stages (full, empty), pieces (full, empty)
+    const bool one = tid < C::STAGES || (tid >= 2 * C::STAGES && tid < 2 * C::STAGES + kPieces);
+    mbar_init(full + 8 * tid, one ? 1 : kComputeWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) *abort_flag = 0;
   Walk walk;
   walk.start(P, W, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
   Piece pc;
@@ -377,14 +371,15 @@ struct JoinShape {
   int rows[2], heads[2], ctas[2];
 };
 
-// Joins a row's pieces: one warp a (query token, head).
+// Joins a row's pieces: one warp a (query token, head).  All its reads go out in two rounds: the records of the row's
+// first pieces, then the (m, l) and the values of up to eight pieces at once.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const AttendWork W, const JoinShape shape) {
   constexpr int PER = D / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= (long long)P.B * P.ql * P.kv.hq) return;
-  const int n = (int)(row / P.kv.hq), h = (int)(row % P.kv.hq), b = n / P.ql;
+  const int n = (int)(row / P.kv.hq), h = (int)(row - (long long)n * P.kv.hq), b = n / P.ql, hk = h / P.G, hl = h - hk * P.G;
   // the group of the sequence
   int grp = -1, tok0 = 0;
   for (int i = 0; i < P.n_groups && grp < 0; i += 32) {
@@ -401,72 +396,86 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
       tok0 = __shfl_sync(0xffffffffu, lo, src) * P.ql;
     }
   }
+  const bool has[2] = {grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0,
+                       min(P.lens[b], P.table_stride << P.kv.page_shift) > 0};
+  const int item_row[2] = {(n - tok0) * P.G + hl, (n - b * P.ql) * P.G + hl};
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
+  // pieces 0 .. np - 1 of the prefix, then those of the suffix: the first in the row's own place, the others in the
+  // slots of the CTAs after it
+  float2 first[2];
+  const float* cta_o[2];
+  const float2* cta_ml[2];
+  int count[2], step[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const AttendPieces& from = i ? W.suffix : W.prefix;
+    float4 a = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+    if (has[i]) a = from.row_ml[row];
+    first[i] = make_float2(a.x, a.y);
+    // CTAs inside the slots whatever a kernel that gave up on a wait has left there
+    const int c0 = min(max(__float_as_int(a.z), 0), shape.ctas[i] - 1);
+    const int c1 = min(max(__float_as_int(a.w), c0), shape.ctas[i] - 1);
+    count[i] = has[i] ? c1 - c0 + 1 : 0;
+    step[i] = shape.heads[i] * shape.rows[i];
+    const long long slot = (long long)(c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] +
+                           item_row[i] % shape.rows[i];
+    cta_o[i] = from.cta_o + slot * D + lane * PER;
+    cta_ml[i] = from.cta_ml + slot;
+  }
   float m = -CUDART_INF_F, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  // Pieces of a segment: the first in the row's own place, the others in the slots of the CTAs after it.  Eight at a
-  // time: their (m, l) in eight lanes, then their values, all loads of a step in flight together.
-  auto pieces = [&](const AttendPieces& from, int rows, int heads, int slots, int local) {
-    const float4 a = from.row_ml[row];
-    // CTAs inside the slots whatever a kernel that gave up on a wait has left there
-    const int c0 = min(max(__float_as_int(a.z), 0), slots - 1), n = min(max(__float_as_int(a.w), c0), slots - 1) - c0 + 1;
-    const long long slot = ((long long)c0 * heads + h / P.G % heads) * rows + local, step = (long long)heads * rows;
-    for (int p0 = 0; p0 < n; p0 += 8) {
-      const int p = p0 + (lane & 7);
-      float pm = -CUDART_INF_F, pl = 0.f;
-      if (p == 0) {
-        pm = a.x, pl = a.y;
-      } else if (p < n) {
-        const float2 y = from.cta_ml[slot + p * step];
-        pm = y.x, pl = y.y;
-      }
-      float v[8][PER];
+  const int all = count[0] + count[1];
+  for (int p0 = 0; p0 < all; p0 += 8) {
+    float v[8][PER];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; ++j) {
+      const int p = p0 + j, s = p >= count[0], q = p - (s ? count[0] : 0);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[j][i] = 0.f;
-        if (p0 + j < n) {
-          const float* src = (p0 + j == 0 ? from.row_o + row * D : from.cta_o + (slot + (p0 + j) * step) * D) + lane * PER;
-          if constexpr (PER == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(src);
-            v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
-          } else {
-            const float2 y = *reinterpret_cast<const float2*>(src);
-            v[j][0] = y.x, v[j][1] = y.y;
-          }
-        }
-      }
-      float mm = fmaxf(m, pm);
-#pragma unroll
-      for (int d = 4; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-      const float rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), f = ex2(pm - rr);
-      m = mm;
-      float add = pl * f;
-#pragma unroll
-      for (int d = 4; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-      l = l * fa + add;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] *= fa;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = __shfl_sync(0xffffffffu, f, j);
-        if (p0 + j < n) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) o[i] = fmaf(v[j][i], w, o[i]);
+      for (int i = 0; i < PER; ++i) v[j][i] = 0.f;
+      if (p < all) {
+        const float* src = q == 0 ? (s ? W.suffix.row_o : W.prefix.row_o) + row * D + lane * PER
+                                  : (s ? cta_o[1] : cta_o[0]) + (long long)q * (s ? step[1] : step[0]) * D;
+        if constexpr (PER == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          v[j][0] = y.x, v[j][1] = y.y;
         }
       }
     }
-  };
-  const int hl = h % P.G;
-  const bool pre = grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0;
-  const bool suf = min(P.lens[b], P.table_stride << P.kv.page_shift) > 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
-  if (pre) pieces(W.prefix, shape.rows[0], shape.heads[0], shape.ctas[0], ((n - tok0) * P.G + hl) % shape.rows[0]);
-  if (suf) pieces(W.suffix, shape.rows[1], shape.heads[1], shape.ctas[1], ((n - b * P.ql) * P.G + hl) % shape.rows[1]);
+    float2 ml = make_float2(-CUDART_INF_F, 0.f);  // of piece p0 + lane % 8
+    {
+      const int p = p0 + (lane & 7), s = p >= count[0], q = p - (s ? count[0] : 0);
+      if (p < all) ml = q == 0 ? (s ? first[1] : first[0]) : (s ? cta_ml[1] : cta_ml[0])[(long long)q * (s ? step[1] : step[0])];
+    }
+    float mm = fmaxf(m, ml.x);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+    const float rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), f = ex2(ml.x - rr);
+    m = mm;
+    float add = ml.y * f;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+    l = l * fa + add;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] *= fa;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float w = __shfl_sync(0xffffffffu, f, j);
+      if (p0 + j < all) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[i] = fmaf(v[j][i], w, o[i]);
+      }
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + lane * PER;
-#pragma unroll
-  for (int i = 0; i < PER; i += 2) *reinterpret_cast<uint32_t*>(out + i) = pack2<E>(o[i] * inv, o[i + 1] * inv);
+  if constexpr (PER == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<E>(o[0] * inv, o[1] * inv), pack2<E>(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack2<E>(o[0] * inv, o[1] * inv);
   if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 

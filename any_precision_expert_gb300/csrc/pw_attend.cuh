@@ -110,15 +110,15 @@ struct PieceRing {
   }
 };
 
-// A CTA's walk over its range of the line.  Segments hold HB key heads.
-template <int ROWS, int TILE, int COST, int HB>
+// A CTA's walk over its range of the line.  Segments hold HB key heads and cost COST tiles beside their own; a CTA gets
+// LEAST units or none, so that its fixed costs and the partial sums of a split stay in proportion.
+template <int ROWS, int TILE, int COST, int HB, int LEAST>
 struct AttendWalk {
   int item;             // current item
   unsigned off;         // units of the item before the current position
   unsigned left;        // units of the range not walked yet
   unsigned pos;         // position on the line
-  unsigned total;       // length of the line
-  int ctas;             // CTAs that share it
+  unsigned share, more; // CTAs 0 .. more - 1 take share + 1 units, the others share
 
   static __device__ __forceinline__ unsigned units(const AttendParams& P, const Item& it) {
     if (it.len == 0 || it.nrows == 0) return 0;
@@ -131,6 +131,7 @@ struct AttendWalk {
     const int per = (W.count + nt - 1) / nt;
     const int i0 = min(tid * per, W.count), i1 = min(i0 + per, W.count);
     unsigned sum = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) sum += units(P, attend_item(P, W.first + i, blockIdx.x == 0));
     unsigned scan = sum;
 #pragma unroll
@@ -141,37 +142,44 @@ struct AttendWalk {
     if (lane == 31) scratch[warp] = scan;
     if (tid == 0) scratch[32] = scratch[33] = 0;
     __syncthreads();
-    unsigned before = scan - sum;
-    total = 0;
+    unsigned before = scan - sum, total = 0;
+#pragma unroll 1
     for (int w = 0; w < nt / 32; ++w) {
       if (w < warp) before += scratch[w];
       total += scratch[w];
     }
-    ctas = min((unsigned)gridDim.x, total);
-    const unsigned u0 = blockIdx.x < ctas ? (unsigned)((unsigned long long)total * blockIdx.x / ctas) : total;
-    const unsigned u1 = blockIdx.x < ctas ? (unsigned)((unsigned long long)total * (blockIdx.x + 1) / ctas) : total;
-    if (u0 < u1 && u0 >= before && u0 < before + sum) {  // one thread's items hold the start
-      unsigned at = before;
-      for (int i = i0; i < i1; ++i) {
-        const unsigned n = units(P, attend_item(P, W.first + i, false));
-        if (u0 < at + n) {
-          scratch[32] = W.first + i;
-          scratch[33] = u0 - at;
-          break;
-        }
+    const unsigned ctas = min((unsigned)gridDim.x, max(1u, total / LEAST)), c = blockIdx.x;
+    share = total / ctas;
+    more = total - share * ctas;
+    pos = c * share + min(c, more);
+    left = c < ctas ? share + (c < more) : 0;
+    if (left > 0 && pos >= before && pos < before + sum) {  // one thread's items hold the start
+      unsigned at = before, n = sum;
+      int i = i0;
+#pragma unroll 1
+      for (; per > 1 && i < i1; ++i) {
+        n = units(P, attend_item(P, W.first + i, false));
+        if (pos < at + n) break;
         at += n;
       }
+      scratch[32] = W.first + i;
+      scratch[33] = pos - at;
     }
     __syncthreads();
     item = (int)scratch[32];
     off = scratch[33];
-    left = u1 - u0;
-    pos = u0;
+  }
+
+  // The CTA whose range holds position x.
+  __device__ __forceinline__ int owner(unsigned x) const {
+    const unsigned big = more * (share + 1);
+    return (int)(x < big ? x / (share + 1) : more + (x - big) / share);
   }
 
   // The next piece with tiles in it and its item's page table; false (and a piece without tiles) at the end of the range.
   __device__ __forceinline__ bool next(const AttendParams& P, Piece& p, const int*& table) {
     p.tile1 = 0;
+#pragma unroll 1
     while (left > 0) {
       const Item it = attend_item(P, item, false);
       const unsigned n = units(P, it);
@@ -183,7 +191,7 @@ struct AttendWalk {
       const int kt = (it.len + TILE - 1) / TILE, rt = (it.nrows + ROWS - 1) / ROWS;
       const unsigned su = kt + COST, seg = off / su, within = off - seg * su;
       const unsigned take = min(su - within, left), end = within + take;
-      const unsigned seg_end = pos - within + su;  // the segment's end on the line
+      const unsigned seg_last = pos - within + su - 1;  // the segment's last unit
       off += take;
       pos += take;
       left -= take;
@@ -192,13 +200,13 @@ struct AttendWalk {
       p.nrows = it.nrows;
       p.len = it.len;
       p.causal = it.causal;
-      p.head = seg / rt;
+      p.head = rt == 1 ? seg : seg / rt;
       p.row0 = (seg - p.head * rt) * ROWS;
       p.head *= HB;
       p.tile0 = within > COST ? within - COST : 0;
       p.tile1 = end - COST;
       p.first = within <= COST;
-      p.last_cta = (int)(((unsigned long long)seg_end * ctas + total - 1) / total) - 1;
+      p.last_cta = owner(seg_last);
       p.prefix = item < P.n_groups;
       table = it.table;
       return true;

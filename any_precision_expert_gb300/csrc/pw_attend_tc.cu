@@ -32,6 +32,7 @@ constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kParts = 2;            // a tile's weights are handed over in this many parts
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
+constexpr int kLeastUnits = 6;       // tiles a CTA takes at least
 constexpr float kGrow = 8.f;
 
 template <int D>
@@ -49,7 +50,7 @@ struct Cfg {
   static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
 };
 
-using Walk = AttendWalk<kTcRows, kTile, kSegmentCost, 1>;
+using Walk = AttendWalk<kTcRows, kTile, kSegmentCost, 1, kLeastUnits>;
 
 __device__ __forceinline__ bool active(const Piece& pc, int i) { return i == 0 || pc.row0 + 128 < pc.nrows; }
 
@@ -213,27 +214,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
   ring.abort_flag = abort_flag;
   ring.err = err;
-  if (tid == 0) {
-    for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 2);
+  {
+    // the barriers lie side by side, one thread each: ring slots (full, empty), pieces (full, empty), then by row tile
+    // queries, scores, sums, turns and the parts of the weights
+    constexpr int kNear = 2 * C::SLOTS + 2 * kPieces, kAll = kNear + 8 + 2 * kParts;
+    if (tid < kAll) {
+      const int k = tid - kNear;
+      const int count = tid < C::SLOTS ? 1 : tid < 2 * C::SLOTS ? 2 : tid < 2 * C::SLOTS + kPieces ? 1
+                        : k < 0 ? kSoftmaxWarps + 2 : k < 2 ? 128 : k < 6 ? 1 : 128;
+      mbar_init(full + 8 * tid, count);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = 0; i < kPieces; ++i) {
-      mbar_init(ring.full + 8 * i, 1);
-      mbar_init(ring.empty + 8 * i, kSoftmaxWarps + 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 128);
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(o_done + 8 * i, 1);
-      mbar_init(turn + 8 * i, 128);
-      for (int k = 0; k < kParts; ++k) mbar_init(p_full + 8 * (kParts * i + k), 128);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (tid == 0) *abort_flag = 0;
   }
   asm volatile("griddepcontrol.launch_dependents;");
-  if (warp == 0) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
+  if (warp == kSoftmaxWarps + 3) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
   Walk walk;
   walk.start(P, W, reinterpret_cast<unsigned*>(smem + C::SCRATCH_AT));
   tc_fence_before();
@@ -255,32 +250,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 32 / RPS;  // lanes a row, rows a step, steps
     const int q_row = 32 * w4, q_sub = lane / LPR, q_col = lane % LPR;
     const uint32_t q_base = base + C::Q_AT + i * C::SLOT;
-    auto q_src = [&](int k) {  // null past the rows
-      const int row = pc.row0 + 128 * i + q_row + k * RPS + q_sub, tok = row / P.G;
-      return row < pc.nrows ? static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
-                                  (pc.head * P.G + row - tok * P.G) * P.q.head_stride + 8 * q_col
-                            : nullptr;
+    // the lane's rows, RPS apart: f(k, source or null past the rows)
+    auto each_row = [&](int k0, int k1, auto f) {
+      int row = pc.row0 + 128 * i + q_row + k0 * RPS + q_sub, tok = row / P.G, hd = row - tok * P.G;
+#pragma unroll
+      for (int k = k0; k < k1; ++k) {
+        f(k, row < pc.nrows ? static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
+                                  (pc.head * P.G + hd) * P.q.head_stride + 8 * q_col
+                            : nullptr);
+        row += RPS;
+        hd += RPS;
+        while (hd >= P.G) hd -= P.G, ++tok;
+      }
     };
     auto call_q = [&]() {  // to the L2, while the piece before still runs
 #pragma unroll 1
-      for (int k = 0; k < STEPS; ++k) {
-        const E* src = q_src(k);
-        if (src && (q_col & 1) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-      }
+      for (int k = 0; k < STEPS; ++k)
+        each_row(k, k + 1, [&](int, const E* src) {
+          if (src && (q_col & 1) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        });
     };
     auto place_q = [&]() {
-      uint4 qv[STEPS];
+      // eight rows at a time: enough in flight, and little code (most CTAs come here once, with cold instructions)
+#pragma unroll 1
+      for (int k0 = 0; k0 < STEPS; k0 += 8) {
+        uint4 qv[8];
+        each_row(k0, k0 + 8, [&](int k, const E* src) {
+          qv[k - k0] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+        });
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        const E* src = q_src(k);
-        qv[k] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        const int at = q_row + k * RPS + q_sub;
-        const uint4 v = qv[k];
-        sts128(q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4),
-               make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep));
+        for (int k = 0; k < 8; ++k) {
+          const int at = q_row + (k0 + k) * RPS + q_sub;
+          const uint4 v = qv[k];
+          sts128(q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4),
+                 make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep));
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full + 8 * i);
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {
+  if (warp == kSoftmaxWarps + 3) {
     tmem_relinquish();
     tmem_dealloc(tmem, 512);
   }
