@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) atomicExch(P.kv.err, kErrLayout);
     return;
   }
+  const typename Walk::Mine mine = Walk::mine(P, W);
   PieceRing ring;
   ring.full = empty + 8 * C::STAGES;
   ring.empty = ring.full + 8 * kPieces;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (tid == 0) *abort_flag = 0;
   Walk walk;
-  walk.start(P, W, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
+  walk.start(P, W, mine, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
   Piece pc;
   int stage = 0, phase = 0;
 
@@ -118,10 +119,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int box = min(1 << shift, TILE);  // tokens of a box
     const int* table;
     bool ok = true;
+    // a suffix is read once: its lines are the first to leave the L2, and the partial sums stay
+    uint64_t once, normal, policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
     while (ok) {
       const bool more = walk.next(P, pc, table);
       ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
       if (!more) break;
+      policy = pc.prefix ? normal : once;
       for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
         const int keys = min(TILE, pc.len - t * TILE), boxes = (keys + box - 1) / box;
         const int at = t * TILE + lane * box;
@@ -141,14 +147,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int h = 0; h < C::NH; ++h) {
             if (HB == 1 || box == TILE) {
-              tma_load_page(dst + h * C::HALF, &maps.k, 64 * h, tok, pc.head, page, full + 8 * stage);
-              tma_load_page(dst + (C::NH + h) * C::HALF, &maps.v, 64 * h, tok, pc.head, page, full + 8 * stage);
+              tma_load_page(dst + h * C::HALF, &maps.k, 64 * h, tok, pc.head, page, full + 8 * stage, policy);
+              tma_load_page(dst + (C::NH + h) * C::HALF, &maps.v, 64 * h, tok, pc.head, page, full + 8 * stage, policy);
             } else {
 #pragma unroll
               for (int g = 0; g < HB; ++g) {
-                tma_load_page(dst + h * C::HALF + g * HEAD, &maps.k, 64 * h, tok, pc.head + g, page, full + 8 * stage);
+                tma_load_page(dst + h * C::HALF + g * HEAD, &maps.k, 64 * h, tok, pc.head + g, page, full + 8 * stage,
+                              policy);
                 tma_load_page(dst + (C::NH + h) * C::HALF + g * HEAD, &maps.v, 64 * h, tok, pc.head + g, page,
-                              full + 8 * stage);
+                              full + 8 * stage, policy);
               }
             }
           }
@@ -366,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// How the prefix and suffix kernels cut rows: rows and heads of a segment, and CTAs.
+// How the prefix and the suffix kernel cut rows: rows and heads of a segment, CTAs, and whether it is the tcgen05 one.
 struct JoinShape {
-  int rows[2], heads[2], ctas[2];
+  int rows[2], heads[2], ctas[2], tc[2];
 };
 
 // Joins a row's pieces: one warp a (query token, head).  All its reads go out in two rounds: the records of the row's
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
   // pieces 0 .. np - 1 of the prefix, then those of the suffix: the first in the row's own place, the others in the
   // slots of the CTAs after it
   float2 first[2];
-  const float* cta_o[2];
+  const float *row_o[2], *cta_o[2];  // this lane's values
   const float2* cta_ml[2];
   int count[2], step[2];
 #pragma unroll
@@ -417,10 +424,17 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
     const int c1 = min(max(__float_as_int(a.w), c0), shape.ctas[i] - 1);
     count[i] = has[i] ? c1 - c0 + 1 : 0;
     step[i] = shape.heads[i] * shape.rows[i];
-    const long long slot = (long long)(c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] +
-                           item_row[i] % shape.rows[i];
-    cta_o[i] = from.cta_o + slot * D + lane * PER;
-    cta_ml[i] = from.cta_ml + slot;
+    const int in_tile = item_row[i] % shape.rows[i];
+    cta_ml[i] = from.cta_ml + (c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] + in_tile;
+    if (shape.tc[i]) {
+      const int at = (lane * PER / 8 * kTcRows + in_tile) * 8 + lane * PER % 8;  // in a block of 8-value columns
+      const long long block = tc_block(tok0, P.G, grp, item_row[i] / kTcRows, P.kv.hkv, hk);
+      row_o[i] = i ? from.row_o + row * D + lane * PER : from.row_o + block * kTcRows * D + at;
+      cta_o[i] = from.cta_o + (long long)c0 * kTcRows * D + at;
+    } else {
+      row_o[i] = from.row_o + row * D + lane * PER;
+      cta_o[i] = from.cta_o + ((long long)(c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] + in_tile) * D + lane * PER;
+    }
   }
   float m = -CUDART_INF_F, l = 0.f, o[PER];
 #pragma unroll
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const A
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[j][i] = 0.f;
       if (p < all) {
-        const float* src = q == 0 ? (s ? W.suffix.row_o : W.prefix.row_o) + row * D + lane * PER
+        const float* src = q == 0 ? (s ? row_o[1] : row_o[0])
                                   : (s ? cta_o[1] : cta_o[0]) + (long long)q * (s ? step[1] : step[0]) * D;
         if constexpr (PER == 4) {
           const float4 y = *reinterpret_cast<const float4*>(src);
@@ -501,7 +515,7 @@ struct Plan {
 
 struct Layout {
   size_t row_o[2], row_ml[2], cta_o[2], cta_ml[2], total;  // [prefix, suffix], [streaming, tcgen05]
-  Layout(const Plan& plan, int hq, int d, int B, int ql) {
+  Layout(const Plan& plan, int hq, int hkv, int d, int B, int ql, int n_groups) {
     const size_t rows = (size_t)B * ql * hq;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -510,7 +524,8 @@ struct Layout {
       return was;
     };
     for (int i = 0; i < 2; ++i) {
-      row_o[i] = take(rows * d * 4);
+      const size_t blocks = tc_block((long long)B * ql, hq / hkv, n_groups, 0, hkv, 0) + hkv;
+      row_o[i] = take(i == 1 ? rows * d * 4 : n_groups == 0 ? 0 : (plan.tc_prefix ? blocks * kTcRows : rows) * d * 4);
       row_ml[i] = take(rows * 16);
       const size_t most = i ? (plan.tc() ? (size_t)attend_tc_ctas() * kTcRows : 0) : (size_t)stream_ctas() * plan.stream_rows * plan.heads;
       cta_o[i] = take(most * d * 4);
@@ -552,7 +567,7 @@ cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMa
 template <typename E, int D>
 cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {
   const Plan plan(P.G, P.kv.hkv, P.B, P.ql, P.n_groups);
-  const Layout L(plan, P.kv.hq, D, P.B, P.ql);
+  const Layout L(plan, P.kv.hq, P.kv.hkv, D, P.B, P.ql, P.n_groups);
   char* w = static_cast<char*>(ws);
   auto pieces = [&](bool suffix, bool tc) {
     AttendPieces p;
@@ -591,6 +606,7 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     const bool tc = i ? plan.tc_suffix : plan.tc_prefix;
     shape.rows[i] = tc ? kTcRows : plan.stream_rows;
     shape.heads[i] = tc ? 1 : plan.heads;
+    shape.tc[i] = tc;
     shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
   const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
@@ -627,7 +643,7 @@ cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps) {
 }
 
 size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups) {
-  return Layout(Plan(kv.hq / kv.hkv, kv.hkv, B, ql, n_groups), kv.hq, kv.d, B, ql).total;
+  return Layout(Plan(kv.hq / kv.hkv, kv.hkv, B, ql, n_groups), kv.hq, kv.hkv, kv.d, B, ql, n_groups).total;
 }
 
 cudaError_t launch_attend(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {

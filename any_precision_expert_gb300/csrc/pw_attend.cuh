@@ -22,12 +22,23 @@ namespace pw {
 
 // Where the pieces of a launch go.  Values are sums relative to the piece's
 // reference m: o = sum 2^(s - m) v, l = sum 2^(s - m), s in log2 units.
+// The streaming kernel writes plain rows: a first piece's in the row's place
+// (query token, head), a further one's in slots [cta][HB][ROWS].  The tcgen05
+// kernel, whose threads hold a row each, writes blocks of 256 rows in 8-value
+// columns [D / 8][256][8], so that a warp's stores are whole lines: a prefix's
+// first piece in block (row tile, key head), a further piece in block [cta];
+// first pieces of suffixes are plain rows here too.
 struct AttendPieces {
-  float* row_o;      // [rows][D]: segments' first pieces, one row a (query token, head)
-  float4* row_ml;    // m, l, and the CTAs that hold the further pieces: (first, last] as int bits
-  float* cta_o;      // [ctas][ROWS][D]: pieces that continue a segment
-  float2* cta_ml;    // [ctas][ROWS]
+  float* row_o;      // segments' first pieces
+  float4* row_ml;    // [rows]: m, l, and the CTAs that hold the further pieces: (first, last] as int bits
+  float* cta_o;      // pieces that continue a segment
+  float2* cta_ml;    // their m and l
 };
+
+// Block of an item's row tile: items' tiles numbered without gaps larger than one.
+__host__ __device__ inline long long tc_block(long long tok0, int G, int item, int tile, int hkv, int head) {
+  return (tok0 * G / 256 + item + tile) * hkv + head;
+}
 
 struct AttendWork {
   int first, count;       // items of this launch: 0 .. n_groups - 1 prefixes, then the sequences
@@ -73,7 +84,7 @@ struct __align__(16) Piece {
   int tile0, tile1;               // key tiles; none (tile1 = 0) ends the CTA's range
   int first;                      // holds the segment's first tile
   int last_cta;                   // CTA that holds its last one
-  int prefix, pad;
+  int prefix, item;
 };
 
 constexpr int kPieces = 4;        // pieces announced ahead
@@ -125,14 +136,26 @@ struct AttendWalk {
     return (unsigned)((it.len + TILE - 1) / TILE + COST) * ((it.nrows + ROWS - 1) / ROWS) * (P.kv.hkv / HB);
   }
 
-  // Whole CTA: finds the CTA's range.  scratch: 34 words of shared memory.
-  __device__ __forceinline__ void start(const AttendParams& P, const AttendWork& W, unsigned* scratch) {
-    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (W.count + nt - 1) / nt;
-    const int i0 = min(tid * per, W.count), i1 = min(i0 + per, W.count);
-    unsigned sum = 0;
+  // Each thread's share of the items, read at the kernel's start so that the reads overlap the set-up.
+  struct Mine {
+    int i0, i1;
+    unsigned sum;
+  };
+  static __device__ __forceinline__ Mine mine(const AttendParams& P, const AttendWork& W) {
+    const int per = (W.count + blockDim.x - 1) / blockDim.x;
+    Mine m;
+    m.i0 = min((int)threadIdx.x * per, W.count);
+    m.i1 = min(m.i0 + per, W.count);
+    m.sum = 0;
 #pragma unroll 1
-    for (int i = i0; i < i1; ++i) sum += units(P, attend_item(P, W.first + i, blockIdx.x == 0));
+    for (int i = m.i0; i < m.i1; ++i) m.sum += units(P, attend_item(P, W.first + i, blockIdx.x == 0));
+    return m;
+  }
+
+  // Whole CTA: finds the CTA's range.  scratch: 34 words of shared memory.
+  __device__ __forceinline__ void start(const AttendParams& P, const AttendWork& W, const Mine& my, unsigned* scratch) {
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned sum = my.sum;
     unsigned scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -155,9 +178,9 @@ struct AttendWalk {
     left = c < ctas ? share + (c < more) : 0;
     if (left > 0 && pos >= before && pos < before + sum) {  // one thread's items hold the start
       unsigned at = before, n = sum;
-      int i = i0;
+      int i = my.i0;
 #pragma unroll 1
-      for (; per > 1 && i < i1; ++i) {
+      for (; my.i1 - my.i0 > 1 && i < my.i1; ++i) {
         n = units(P, attend_item(P, W.first + i, false));
         if (pos < at + n) break;
         at += n;
@@ -208,6 +231,7 @@ struct AttendWalk {
       p.first = within <= COST;
       p.last_cta = owner(seg_last);
       p.prefix = item < P.n_groups;
+      p.item = item;
       table = it.table;
       return true;
     }
@@ -224,6 +248,15 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
           "r"(dst),
       "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(mbar)
+      : "memory");
+}
+// The same with an L2 policy.
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page,
+                                              uint32_t mbar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(mbar), "l"(policy)
       : "memory");
 }
 

@@ -98,10 +98,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ uint4 load_staged(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
+// 32 bytes: a whole sector a lane.
+__device__ __forceinline__ void store8(float* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicExch(err, kErrLayout);
     return;
   }
+  const Walk::Mine mine = Walk::mine(P, W);
   PieceRing ring;
   ring.full = empty + 8 * C::SLOTS;
   ring.empty = ring.full + 8 * kPieces;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   if (warp == kSoftmaxWarps + 3) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
   Walk walk;
-  walk.start(P, W, reinterpret_cast<unsigned*>(smem + C::SCRATCH_AT));
+  walk.start(P, W, mine, reinterpret_cast<unsigned*>(smem + C::SCRATCH_AT));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -242,50 +244,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >> 2, w4 = warp & 3, r = tid & 127;
     const uint32_t lanes = (uint32_t)w4 << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + C::S_COL + i * 128, to = tmem + lanes + C::O_COL + i * 128;
-    // a negative scale turns the queries around, a scale of 0 takes them away
-    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = P.scale == 0.f ? 0u : 0xffffffffu;
+    const float sign = P.scale < 0.f ? -1.f : P.scale == 0.f ? 0.f : 1.f;  // other than 1: applied to the scores
     const float scale2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
     Piece pc = {};
     // Queries: a warp brings its 32 rows, whole lines at a time.
     constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 32 / RPS;  // lanes a row, rows a step, steps
     const int q_row = 32 * w4, q_sub = lane / LPR, q_col = lane % LPR;
     const uint32_t q_base = base + C::Q_AT + i * C::SLOT;
-    // the lane's rows, RPS apart: f(k, source or null past the rows)
-    auto each_row = [&](int k0, int k1, auto f) {
-      int row = pc.row0 + 128 * i + q_row + k0 * RPS + q_sub, tok = row / P.G, hd = row - tok * P.G;
-#pragma unroll
-      for (int k = k0; k < k1; ++k) {
-        f(k, row < pc.nrows ? static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
-                                  (pc.head * P.G + hd) * P.q.head_stride + 8 * q_col
-                            : nullptr);
-        row += RPS;
+    // The lane's rows, RPS apart: f(k, source or null past the rows).
+    auto each_row = [&](auto f) {
+      const int row0 = pc.row0 + 128 * i + q_row + q_sub, tok = row0 / P.G;
+      int hd = row0 - tok * P.G, left = pc.nrows - row0;
+      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
+                     (pc.head * P.G + hd) * P.q.head_stride + 8 * q_col;
+      const long long turn_over = P.q.token_stride - P.G * P.q.head_stride;
+#pragma unroll 4
+      for (int k = 0; k < STEPS; ++k) {
+        f(k, left > 0 ? src : nullptr);
+        left -= RPS;
         hd += RPS;
-        while (hd >= P.G) hd -= P.G, ++tok;
+        src += RPS * P.q.head_stride;
+        while (hd >= P.G) hd -= P.G, src += turn_over;
       }
-    };
-    auto call_q = [&]() {  // to the L2, while the piece before still runs
-#pragma unroll 1
-      for (int k = 0; k < STEPS; ++k)
-        each_row(k, k + 1, [&](int, const E* src) {
-          if (src && (q_col & 1) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-        });
     };
     auto place_q = [&]() {
-      // eight rows at a time: enough in flight, and little code (most CTAs come here once, with cold instructions)
-#pragma unroll 1
-      for (int k0 = 0; k0 < STEPS; k0 += 8) {
-        uint4 qv[8];
-        each_row(k0, k0 + 8, [&](int k, const E* src) {
-          qv[k - k0] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-        });
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int at = q_row + (k0 + k) * RPS + q_sub;
-          const uint4 v = qv[k];
-          sts128(q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4),
-                 make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep));
-        }
-      }
+      each_row([&](int k, const E* src) {
+        const int at = q_row + k * RPS + q_sub;
+        const uint32_t dst = q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4);
+        if (src)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        else
+          sts128(dst, make_uint4(0, 0, 0, 0));
+      });
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       mbar_arrive(q_full + 8 * i);
     };
@@ -320,6 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(turn + 8 * i, (turns & 1) ^ (i ^ 1), abort_flag, err));
           if (!ok) break;
           ++turns;
+        }
+        if (sign != 1.f) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * sign);
         }
         const int see = vis - t * kTile;
         float top = -CUDART_INF_F;
@@ -395,15 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (both) mbar_arrive(turn + 8 * (i ^ 1));
       }
       if (!ok) break;
+      // the last S is out of the queries' way: the next piece's go in before this one's sums come out
       have = advance();
-      if (have) call_q();
+      if (have) place_q();
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
       const AttendPieces& dst = cur.prefix ? W.prefix : W.suffix;
       const bool in = row < cur.nrows;
       const long long grow = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + row - tok * P.G;
-      const long long crow = (long long)blockIdx.x * kTcRows + 128 * i + r;
+      const int crow = blockIdx.x * kTcRows + 128 * i + r;
       if (in) {
         const float sum = l.x + l.y;
         if (cur.first)
@@ -411,35 +407,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           dst.cta_ml[crow] = make_float2(m, sum);
       }
-      // Sums to rows: through the warp's own rows of the query tile (read by no product any more), so that the
-      // stores are whole lines.  CC columns at a time.
-      constexpr int CC = 32, LINE = CC / 4;  // columns a step, 16-byte words of a staged row
-      const long long my_out = !in ? -1 : (cur.first ? grow : crow);
-      float* out = cur.first ? dst.row_o : dst.cta_o;
-      const uint32_t st_base = q_base + q_row * 128;
-      auto staged = [&](int k, int word) { return st_base + k * 128 + ((word ^ (k & 7)) << 4); };
+      // blocks of 8-value columns; a suffix's first pieces, which would leave most of a block empty, in plain rows
+      const bool plain = cur.first && !cur.prefix;
+      const int column = plain ? 8 : kTcRows * 8;
+      float* out = plain       ? dst.row_o + grow * D
+                   : cur.first ? dst.row_o + tc_block(cur.tok0, P.G, cur.item, cur.row0 / kTcRows, P.kv.hkv, cur.head) * kTcRows * D +
+                                     (128 * i + r) * 8
+                               : dst.cta_o + (long long)blockIdx.x * kTcRows * D + (128 * i + r) * 8;
 #pragma unroll 1
-      for (int c = 0; c < D; c += CC) {
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_load32(to + c, o);
+        if (in) {
 #pragma unroll
-        for (int c2 = 0; c2 < CC; c2 += 16) {
-          uint32_t o[16];
-          tmem_load16(to + c + c2, o);
-#pragma unroll
-          for (int k = 0; k < 16; k += 4)
-            sts128(staged(lane, (c2 + k) / 4), make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+          for (int k = 0; k < 32; k += 8) store8(out + (c + k) / 8 * column, o + k);
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 32; k += 32 / LINE) {
-          const int at = k + lane / LINE, word = lane % LINE;
-          const long long to_row = __shfl_sync(0xffffffffu, my_out, at);
-          const uint4 v = load_staged(staged(at, word));
-          if (to_row >= 0) *reinterpret_cast<uint4*>(out + to_row * D + c + 4 * word) = v;
-        }
-        __syncwarp();
       }
       tc_fence_before();
-      if (have) place_q();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
