@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   using C = Cfg<D>;
   constexpr int ROWS = 16 * MT, KS = kComputeWarps / (MT * HB), TILE = kStageKeys / HB, KPW = TILE / KS;
   constexpr int HEAD = TILE * 128;  // bytes of one head's rows in a column block
-  // a segment's fixed cost in key tiles: about one 64-key tile's time
-  using Walk = AttendWalk<ROWS, TILE, HB, HB, 1>;
+  // a segment's fixed cost and a CTA's least work: about a 64-key tile's time
+  using Walk = AttendWalk<ROWS, TILE, HB, HB, HB>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
@@ -378,119 +378,127 @@ struct JoinShape {
   int rows[2], heads[2], ctas[2], tc[2];
 };
 
-// Joins a row's pieces: one warp a (query token, head).  All its reads go out in two rounds: the records of the row's
-// first pieces, then the (m, l) and the values of up to eight pieces at once.
+constexpr int kJoinWarps = 4;
+
+// A row's pieces of one kind, as one lane of the join sees them.
+struct Pieces {
+  float2 first;        // m and l of the first, in the row's own place
+  const float* row_o;  // this lane's values of it
+  const float2* ml;    // of piece p >= 1: ml[p * step], o[p * step * D], in the slots of the CTAs after the first's
+  const float* o;
+  int count, step, far;  // far: from a lane's first 8 values to its second
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+
+// Joins the pieces of the rows.  A warp takes four adjacent rows of a key head (the tcgen05 blocks' lines hold 8 values
+// of four rows), eight lanes a row, 8 values at a time, and goes through the pieces of the prefix and then of the suffix
+// in their order, four in flight.  No exchange between lanes, and little code: its instructions are as cold as its data.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams P, const AttendWork W, const JoinShape shape) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)P.B * P.ql * P.kv.hq) return;
-  const int n = (int)(row / P.kv.hq), h = (int)(row - (long long)n * P.kv.hq), b = n / P.ql, hk = h / P.G, hl = h - hk * P.G;
-  // the group of the sequence
-  int grp = -1, tok0 = 0;
-  for (int i = 0; i < P.n_groups && grp < 0; i += 32) {
-    const int gi = i + lane;
-    int lo = 0, hi = 0;
-    if (gi < P.n_groups) {
-      lo = P.group_offsets ? min(max(P.group_offsets[gi], 0), P.B) : 0;
-      hi = P.group_offsets ? min(max(P.group_offsets[gi + 1], lo), P.B) : P.B;
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParams P, const AttendWork W,
+                                                               const JoinShape shape) {
+  constexpr int NC = D / 64;  // times 8 values a lane
+  const int lane = threadIdx.x & 31, hk = blockIdx.y, c8 = lane >> 2;
+  const int r = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * 4 + (lane & 3);  // rows (query token, head of the group)
+  if (r >= P.B * P.ql * P.G) return;
+  const int n = r / P.G, h = hk * P.G + r - n * P.G, b = n / P.ql;
+  int grp = P.n_groups - 1, tok0 = 0;  // the group of the sequence: the last that begins at or before it
+  if (P.group_offsets && P.n_groups > 0) {
+    int lo = 0, hi = P.n_groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (P.group_offsets[mid] <= b) lo = mid;
+      else hi = mid - 1;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, b >= lo && b < hi);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      grp = i + src;
-      tok0 = __shfl_sync(0xffffffffu, lo, src) * P.ql;
-    }
+    const int first = min(max(P.group_offsets[lo], 0), P.B), last = min(max(P.group_offsets[lo + 1], first), P.B);
+    grp = b >= first && b < last ? lo : -1;
+    tok0 = first * P.ql;
   }
   const bool has[2] = {grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0,
                        min(P.lens[b], P.table_stride << P.kv.page_shift) > 0};
-  const int item_row[2] = {(n - tok0) * P.G + hl, (n - b * P.ql) * P.G + hl};
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
-  // pieces 0 .. np - 1 of the prefix, then those of the suffix: the first in the row's own place, the others in the
-  // slots of the CTAs after it
-  float2 first[2];
-  const float *row_o[2], *cta_o[2];  // this lane's values
-  const float2* cta_ml[2];
-  int count[2], step[2];
+  const long long row = (long long)n * P.kv.hq + h;
+  Pieces pc[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const AttendPieces& from = i ? W.suffix : W.prefix;
-    float4 a = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
-    if (has[i]) a = from.row_ml[row];
-    first[i] = make_float2(a.x, a.y);
+    const float4 rec = has[i] ? from.row_ml[row] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
     // CTAs inside the slots whatever a kernel that gave up on a wait has left there
-    const int c0 = min(max(__float_as_int(a.z), 0), shape.ctas[i] - 1);
-    const int c1 = min(max(__float_as_int(a.w), c0), shape.ctas[i] - 1);
-    count[i] = has[i] ? c1 - c0 + 1 : 0;
-    step[i] = shape.heads[i] * shape.rows[i];
-    const int in_tile = item_row[i] % shape.rows[i];
-    cta_ml[i] = from.cta_ml + (c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] + in_tile;
-    if (shape.tc[i]) {
-      const int at = (lane * PER / 8 * kTcRows + in_tile) * 8 + lane * PER % 8;  // in a block of 8-value columns
-      const long long block = tc_block(tok0, P.G, grp, item_row[i] / kTcRows, P.kv.hkv, hk);
-      row_o[i] = i ? from.row_o + row * D + lane * PER : from.row_o + block * kTcRows * D + at;
-      cta_o[i] = from.cta_o + (long long)c0 * kTcRows * D + at;
-    } else {
-      row_o[i] = from.row_o + row * D + lane * PER;
-      cta_o[i] = from.cta_o + ((long long)(c0 * shape.heads[i] + hk % shape.heads[i]) * shape.rows[i] + in_tile) * D + lane * PER;
-    }
+    const int c0 = min(max(__float_as_int(rec.z), 0), shape.ctas[i] - 1);
+    const int c1 = min(max(__float_as_int(rec.w), c0), shape.ctas[i] - 1);
+    const int item_row = r - (i ? b * P.ql : tok0) * P.G, in_tile = item_row & (shape.rows[i] - 1);
+    const int slot = (c0 * shape.heads[i] + (hk & (shape.heads[i] - 1))) * shape.rows[i] + in_tile;
+    pc[i].first = make_float2(rec.x, rec.y);
+    pc[i].count = has[i] ? c1 - c0 + 1 : 0;
+    pc[i].step = shape.heads[i] * shape.rows[i];
+    pc[i].ml = from.cta_ml + slot;
+    pc[i].far = shape.tc[i] ? 8 * kTcRows * 8 : 64;
+    const int column = c8 * 8 * (shape.tc[i] ? kTcRows : 1);
+    pc[i].o = from.cta_o + (shape.tc[i] ? (long long)c0 * kTcRows * D + in_tile * 8 : (long long)slot * D) + column;
+    pc[i].row_o = from.row_o + row * D + c8 * 8;
+    if (shape.tc[i] && i == 0)
+      pc[i].row_o = from.row_o + tc_block(tok0, P.G, grp, item_row / kTcRows, P.kv.hkv, hk) * kTcRows * D + in_tile * 8 + column;
   }
-  float m = -CUDART_INF_F, l = 0.f, o[PER];
+  float m = -CUDART_INF_F, l = 0.f, o[NC * 8];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  const int all = count[0] + count[1];
-  for (int p0 = 0; p0 < all; p0 += 8) {
-    float v[8][PER];
+  for (int k = 0; k < NC * 8; ++k) o[k] = 0.f;
+  const int all = pc[0].count + pc[1].count;
+#pragma unroll 1
+  for (int p0 = 0; p0 < all; p0 += 4) {
+    float2 ml[4];
+    float v[4][NC][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int p = p0 + j, s = p >= count[0], q = p - (s ? count[0] : 0);
+    for (int j = 0; j < 4; ++j) {
+      const bool suf = p0 + j >= pc[0].count;
+      const int p = p0 + j - (suf ? pc[0].count : 0), step = suf ? pc[1].step : pc[0].step;
+      ml[j] = make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[j][i] = 0.f;
-      if (p < all) {
-        const float* src = q == 0 ? (s ? row_o[1] : row_o[0])
-                                  : (s ? cta_o[1] : cta_o[0]) + (long long)q * (s ? step[1] : step[0]) * D;
-        if constexpr (PER == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          v[j][0] = y.x, v[j][1] = y.y;
-        }
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][c][k] = 0.f;
+      if (p0 + j >= all) continue;
+      const float* src = suf ? pc[1].row_o : pc[0].row_o;
+      int far = suf ? 64 : pc[0].far;  // a suffix's first piece is a plain row
+      if (p == 0) {
+        ml[j] = suf ? pc[1].first : pc[0].first;
+      } else {
+        ml[j] = (suf ? pc[1].ml : pc[0].ml)[p * step];
+        src = (suf ? pc[1].o : pc[0].o) + (long long)p * step * D;
+        far = suf ? pc[1].far : pc[0].far;
       }
-    }
-    float2 ml = make_float2(-CUDART_INF_F, 0.f);  // of piece p0 + lane % 8
-    {
-      const int p = p0 + (lane & 7), s = p >= count[0], q = p - (s ? count[0] : 0);
-      if (p < all) ml = q == 0 ? (s ? first[1] : first[0]) : (s ? cta_ml[1] : cta_ml[0])[(long long)q * (s ? step[1] : step[0])];
-    }
-    float mm = fmaxf(m, ml.x);
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-    const float rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), f = ex2(ml.x - rr);
+      for (int c = 0; c < NC; ++c) load8(src + c * far, v[j][c]);
+    }
+    const float mm = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    const float rr = mm == -CUDART_INF_F ? 0.f : mm, keep = ex2(m - rr);
     m = mm;
-    float add = ml.y * f;
+    l *= keep;
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-    l = l * fa + add;
+    for (int k = 0; k < NC * 8; ++k) o[k] *= keep;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= fa;
+    for (int j = 0; j < 4; ++j) {
+      const float w = ex2(ml[j].x - rr);
+      l = fmaf(ml[j].y, w, l);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float w = __shfl_sync(0xffffffffu, f, j);
-      if (p0 + j < all) {
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) o[i] = fmaf(v[j][i], w, o[i]);
-      }
+        for (int k = 0; k < 8; ++k) o[c * 8 + k] = fmaf(v[j][c][k], w, o[c * 8 + k]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + lane * PER;
-  if constexpr (PER == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<E>(o[0] * inv, o[1] * inv), pack2<E>(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack2<E>(o[0] * inv, o[1] * inv);
-  if (lane == 0 && P.lse) P.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+  E* out = static_cast<E*>(P.out.ptr) + n * P.out.token_stride + h * P.out.head_stride + c8 * 8;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = o[c * 8 + k] * inv;
+    *reinterpret_cast<uint4*>(out + c * 64) = pack8<E>(v);
+  }
+  if (c8 == 0 && P.lse) P.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 int stream_ctas() { return 2 * sm_count(); }
@@ -540,8 +548,8 @@ struct Layout {
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  Launch(unsigned grid, unsigned block, size_t smem, cudaStream_t s, bool early) {
-    cfg.gridDim = dim3(grid);
+  Launch(dim3 grid, unsigned block, size_t smem, cudaStream_t s, bool early) {
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -560,7 +568,7 @@ cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMa
   // boxes of several heads only where a page holds a whole tile
   const bool whole = (1 << P.kv.page_shift) >= kStageKeys / HB;
   const KvMaps& m = HB == 4 && whole ? maps.heads4 : HB == 2 && whole ? maps.heads2 : maps.heads1;
-  const Launch at(stream_ctas(), kThreads, Cfg<D>::SMEM, s, early);
+  const Launch at(dim3(stream_ctas()), kThreads, Cfg<D>::SMEM, s, early);
   return cudaLaunchKernelEx(&at.cfg, attend_kernel<E, D, MT, HB>, P, W, m);
 }
 
@@ -609,8 +617,8 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     shape.tc[i] = tc;
     shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
-  const long long out_rows = (long long)P.B * P.ql * P.kv.hq;
-  const Launch at((unsigned)((out_rows + 7) / 8), 256, 0, s, true);
+  const int join_rows = P.B * P.ql * P.G;
+  const Launch at(dim3((join_rows + 4 * kJoinWarps - 1) / (4 * kJoinWarps), P.kv.hkv), kJoinWarps * 32, 0, s, true);
   return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
 }
 
