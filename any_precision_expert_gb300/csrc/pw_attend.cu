@@ -376,9 +376,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 // How the prefix and the suffix kernel cut rows: rows and heads of a segment, CTAs, and whether it is the tcgen05 one.
 struct JoinShape {
   int rows[2], heads[2], ctas[2], tc[2];
+  int split;  // warps that share four rows: 1 or 4
 };
 
 constexpr int kJoinWarps = 4;
+constexpr int kJoinSplitRows = 4096;
 
 // A row's pieces of one kind, as one lane of the join sees them.
 struct Pieces {
@@ -398,14 +400,17 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 // Joins the pieces of the rows.  A warp takes four adjacent rows of a key head (the tcgen05 blocks' lines hold 8 values
 // of four rows), eight lanes a row, 8 values at a time, and goes through the pieces of the prefix and then of the suffix
 // in their order, four in flight.  No exchange between lanes, and little code: its instructions are as cold as its data.
+// With few rows the four warps of a CTA share them (split 4): each takes every fourth four pieces, and the first adds up.
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParams P, const AttendWork W,
                                                                const JoinShape shape) {
   constexpr int NC = D / 64;  // times 8 values a lane
   const int lane = threadIdx.x & 31, hk = blockIdx.y, c8 = lane >> 2;
-  const int r = (blockIdx.x * kJoinWarps + (threadIdx.x >> 5)) * 4 + (lane & 3);  // rows (query token, head of the group)
-  if (r >= P.B * P.ql * P.G) return;
-  const int n = r / P.G, h = hk * P.G + r - n * P.G, b = n / P.ql;
+  const int warp = threadIdx.x >> 5, part = warp & (shape.split - 1);
+  const int r = (blockIdx.x * (kJoinWarps / shape.split) + warp / shape.split) * 4 + (lane & 3);  // (query token, head of the group)
+  if (shape.split == 1 && r >= P.B * P.ql * P.G) return;
+  const bool live = r < P.B * P.ql * P.G;
+  const int n = live ? r / P.G : 0, h = live ? hk * P.G + r - n * P.G : 0, b = n / P.ql;
   int grp = P.n_groups - 1, tok0 = 0;  // the group of the sequence: the last that begins at or before it
   if (P.group_offsets && P.n_groups > 0) {
     int lo = 0, hi = P.n_groups - 1;
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParam
   for (int k = 0; k < NC * 8; ++k) o[k] = 0.f;
   const int all = pc[0].count + pc[1].count;
 #pragma unroll 1
-  for (int p0 = 0; p0 < all; p0 += 4) {
+  for (int p0 = 4 * part; p0 < all; p0 += 4 * shape.split) {
     float2 ml[4];
     float v[4][NC][8];
 #pragma unroll
@@ -487,6 +492,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParam
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[c * 8 + k] = fmaf(v[j][c][k], w, o[c * 8 + k]);
+    }
+  }
+  if (shape.split > 1) {
+    __shared__ float2 other_ml[kJoinWarps][32];
+    __shared__ float4 other_o[kJoinWarps][NC * 2][32];
+    if (part != 0) {
+      other_ml[warp][lane] = make_float2(m, l);
+#pragma unroll
+      for (int k = 0; k < NC * 2; ++k)
+        other_o[warp][k][lane] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    }
+    __syncthreads();
+    if (part != 0 || !live) return;
+#pragma unroll 1
+    for (int w = warp + 1; w < warp + shape.split; ++w) {
+      const float2 y = other_ml[w][lane];
+      const float mm = fmaxf(m, y.x), rr = mm == -CUDART_INF_F ? 0.f : mm, fa = ex2(m - rr), fb = ex2(y.x - rr);
+      m = mm;
+      l = l * fa + y.y * fb;
+#pragma unroll
+      for (int k = 0; k < NC * 2; ++k) {
+        const float4 v = other_o[w][k][lane];
+        o[4 * k] = o[4 * k] * fa + v.x * fb;
+        o[4 * k + 1] = o[4 * k + 1] * fa + v.y * fb;
+        o[4 * k + 2] = o[4 * k + 2] * fa + v.z * fb;
+        o[4 * k + 3] = o[4 * k + 3] * fa + v.w * fb;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -618,7 +650,9 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
   const int join_rows = P.B * P.ql * P.G;
-  const Launch at(dim3((join_rows + 4 * kJoinWarps - 1) / (4 * kJoinWarps), P.kv.hkv), kJoinWarps * 32, 0, s, true);
+  shape.split = (long long)join_rows * P.kv.hkv <= kJoinSplitRows ? kJoinWarps : 1;
+  const int cta_rows = 4 * kJoinWarps / shape.split;
+  const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), kJoinWarps * 32, 0, s, true);
   return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
 }
 
