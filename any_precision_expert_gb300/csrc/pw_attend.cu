@@ -376,11 +376,22 @@ __global__ void __launch_bounds__(kThreads, 2)
 // How the prefix and the suffix kernel cut rows: rows and heads of a segment, CTAs, and whether it is the tcgen05 one.
 struct JoinShape {
   int rows[2], heads[2], ctas[2], tc[2];
-  int split;  // warps that share four rows: 1 or 4
+  int split;  // warps that share four rows
 };
 
-constexpr int kJoinWarps = 4;
-constexpr int kJoinSplitRows = 4096;
+// Warps that share four rows' pieces, by the number of rows (query tokens x heads): a lone sequence on a long prefix has
+// a piece from every CTA (measured: 20 rows of 300 pieces, the call 41 us with 4 warps, 31 with 16), many rows fill the
+// GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).
+constexpr int kJoinWarps = 4;         // a CTA's, but for
+constexpr int kJoinMost = 16;
+inline int join_split(long long rows, long long keys) {
+  return rows <= 608 && keys > 64 * 32 ? kJoinMost : rows <= 4096 ? kJoinWarps : 1;
+}
+
+// With fewer segments than this every one is split among many CTAs: stages of one head then, whose four warps join their
+// keys in the CTA, leave a quarter of the pieces (measured: one sequence of 4 key heads on 19327 tokens 31 -> 21 us; at
+// 64 segments and more four heads a stage are as good or better).
+constexpr int kFewSegments = 16;
 
 // A row's pieces of one kind, as one lane of the join sees them.
 struct Pieces {
@@ -400,14 +411,14 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 // Joins the pieces of the rows.  A warp takes four adjacent rows of a key head (the tcgen05 blocks' lines hold 8 values
 // of four rows), eight lanes a row, 8 values at a time, and goes through the pieces of the prefix and then of the suffix
 // in their order, four in flight.  No exchange between lanes, and little code: its instructions are as cold as its data.
-// With few rows the four warps of a CTA share them (split 4): each takes every fourth four pieces, and the first adds up.
+// With few rows several warps share them: each takes its four of every 4 x split pieces, and the first adds up.
 template <typename E, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParams P, const AttendWork W,
+__global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams P, const AttendWork W,
                                                                const JoinShape shape) {
   constexpr int NC = D / 64;  // times 8 values a lane
   const int lane = threadIdx.x & 31, hk = blockIdx.y, c8 = lane >> 2;
   const int warp = threadIdx.x >> 5, part = warp & (shape.split - 1);
-  const int r = (blockIdx.x * (kJoinWarps / shape.split) + warp / shape.split) * 4 + (lane & 3);  // (query token, head of the group)
+  const int r = (blockIdx.x * (blockDim.x / 32 / shape.split) + warp / shape.split) * 4 + (lane & 3);  // (query token, head of the group)
   if (shape.split == 1 && r >= P.B * P.ql * P.G) return;
   const bool live = r < P.B * P.ql * P.G;
   const int n = live ? r / P.G : 0, h = live ? hk * P.G + r - n * P.G : 0, b = n / P.ql;
@@ -495,8 +506,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendParam
     }
   }
   if (shape.split > 1) {
-    __shared__ float2 other_ml[kJoinWarps][32];
-    __shared__ float4 other_o[kJoinWarps][NC * 2][32];
+    __shared__ float2 other_ml[kJoinMost][32];
+    __shared__ float4 other_o[kJoinMost][NC * 2][32];
     if (part != 0) {
       other_ml[warp][lane] = make_float2(m, l);
 #pragma unroll
@@ -548,7 +559,7 @@ struct Plan {
     const long long rows = !tc_suffix && !tc_prefix && shared > own ? shared : own;
     stream_rows = tc_suffix ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     heads = stream_rows == 16 ? 4 : stream_rows == 32 ? 2 : 1;
-    while (hkv % heads) heads /= 2;
+    while (hkv % heads || (heads > 1 && (long long)(B + (tc_prefix ? 0 : n_groups)) * (hkv / heads) < kFewSegments)) heads /= 2;
   }
   bool tc() const { return tc_prefix || tc_suffix; }
 };
@@ -650,9 +661,10 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
   const int join_rows = P.B * P.ql * P.G;
-  shape.split = (long long)join_rows * P.kv.hkv <= kJoinSplitRows ? kJoinWarps : 1;
-  const int cta_rows = 4 * kJoinWarps / shape.split;
-  const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), kJoinWarps * 32, 0, s, true);
+  shape.split = join_split((long long)join_rows * P.kv.hkv,
+                           (long long)(P.table_stride + (P.n_groups ? P.prefix_stride : 0)) << P.kv.page_shift);
+  const int warps = shape.split > kJoinWarps ? shape.split : kJoinWarps, cta_rows = 4 * warps / shape.split;
+  const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), warps * 32, 0, s, true);
   return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
 }
 

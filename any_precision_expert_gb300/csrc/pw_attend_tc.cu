@@ -32,7 +32,7 @@ constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kParts = 2;            // a tile's weights are handed over in this many parts
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
-constexpr int kLeastUnits = 6;       // tiles a CTA takes at least
+constexpr int kLeastUnits = 3;       // tiles a CTA takes at least
 constexpr float kGrow = 8.f;
 
 template <int D>
