@@ -27,7 +27,7 @@ inline bool bad_tokens(int T) { return T < 0 || T > (1 << 20); }
 
 pw_status check_heads(const pw_heads& h) {
   if (h.dtype != PW_F16 && h.dtype != PW_BF16) return PW_ERR_INVALID_ARG;
-  if (h.n_heads < 1 || h.n_kv_heads < 1 || h.n_heads > 65536 || h.n_heads % h.n_kv_heads != 0)
+  if (h.n_heads < 1 || h.n_kv_heads < 1 || h.n_heads > 16384 || h.n_heads % h.n_kv_heads != 0)
     return PW_ERR_INVALID_ARG;
   if (h.n_heads / h.n_kv_heads > kMaxGroup) return PW_ERR_UNSUPPORTED;
   if (h.head_dim != 64 && h.head_dim != 128) return PW_ERR_UNSUPPORTED;

@@ -554,7 +554,7 @@ typedef enum { PW_F16 = 0, PW_BF16 = 1 } pw_dtype;
 
 typedef struct {
   int dtype;        /* pw_dtype of every head row */
-  int n_heads;      /* query heads */
+  int n_heads;      /* query heads, 1..16384 */
   int n_kv_heads;   /* key / value heads, divides n_heads */
   int head_dim;     /* 64 or 128 (PW_ERR_UNSUPPORTED otherwise) */
 } pw_heads;

@@ -348,6 +348,33 @@ def test_attend_on_a_side_stream_and_in_a_graph():
     c.check(out, None)
 
 
+@pytest.mark.parametrize("many", [1, 80])
+def test_attend_scale_of_zero_is_the_mean(many):
+    c = Case(np.random.default_rng(17), [50] * many, [70], None, 4, 1, 64, 16, torch.float16, layout="token")
+    c.scale = 0.0
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("hkv", [4, 6, 3])
+def test_cache_with_heads_outermost(hkv):
+    c = Case(np.random.default_rng(18), [100, 3, 41], [60], None, 2 * hkv, hkv, 128, 16, torch.bfloat16)
+    want = c.run()[0]
+    c.k, c.v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (c.k, c.v))  # [heads][pages][tokens]
+    c.cache = pw.KvCache(c.k, c.v, n_heads=2 * hkv)
+    out, lse = c.run()
+    assert torch.equal(out, want)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("hkv,D", [(8, 128), (2, 64), (1, 128)])
+def test_attend_one_sequence_on_a_long_prefix(hkv, D):
+    # every CTA holds a piece of every row
+    c = Case(np.random.default_rng(19), [9], [9000], None, 5 * hkv, hkv, D, 128, torch.float16)
+    out, lse = c.run()
+    c.check(out, lse)
+    assert torch.equal(out, c.run(lse=False)[0])
+
+
 def test_cache_offsets_past_32_bits():
     page, D = 64, 128
     pages = (5 << 30) // (page * D * 2)          # 5 GB of keys: element offsets past 2^31
