@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) atomicExch(P.kv.err, kErrLayout);
     return;
   }
+  // behind the tcgen05 kernel of the same call there is nothing to wait for here, only before the end
+  if (W.behind) behind_the_stream();
   const typename Walk::Mine mine = Walk::mine(P, W);
   PieceRing ring;
   ring.full = empty + 8 * C::STAGES;
@@ -168,9 +170,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < C::STAGES; ++i)
         for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
         }
-    asm volatile("griddepcontrol.launch_dependents;");  // the join may take its place beside the last pieces
-    // the tcgen05 kernel of the same call may still run: this launch ends after it
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();  // the join may take its place beside the last pieces
+    if (!W.behind) behind_the_stream();
     return;
   }
 
@@ -436,7 +437,8 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
   }
   const bool has[2] = {grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0,
                        min(P.lens[b], P.table_stride << P.kv.page_shift) > 0};
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes before reads the call's inputs only
+  behind_the_stream();  // what comes before reads inputs that the kernels before this one read, too
+  let_next_start();
   const long long row = (long long)n * P.kv.hq + h;
   Pieces pc[2];
 #pragma unroll
@@ -586,32 +588,15 @@ struct Layout {
   }
 };
 
-// Launch attributes: `early` lets the kernel start while the one before it in the stream still runs (it waits for it
-// before it reads what that one writes, and before it ends).
-struct Launch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  Launch(dim3 grid, unsigned block, size_t smem, cudaStream_t s, bool early) {
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
-  }
-};
-
 template <typename E, int D, int MT, int HB>
-cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMapSet& maps, bool early, cudaStream_t s) {
+cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMapSet& maps, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(attend_kernel<E, D, MT, HB>);
   const cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   // boxes of several heads only where a page holds a whole tile
   const bool whole = (1 << P.kv.page_shift) >= kStageKeys / HB;
   const KvMaps& m = HB == 4 && whole ? maps.heads4 : HB == 2 && whole ? maps.heads2 : maps.heads1;
-  const Launch at(dim3(stream_ctas()), kThreads, Cfg<D>::SMEM, s, early);
+  const Launch at(dim3(stream_ctas()), kThreads, Cfg<D>::SMEM, s);
   return cudaLaunchKernelEx(&at.cfg, attend_kernel<E, D, MT, HB>, P, W, m);
 }
 
@@ -633,22 +618,23 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
   W.suffix = pieces(true, plan.tc_suffix);
   cudaError_t e = cudaSuccess;
   if (plan.tc()) {
+    W.behind = true;
     W.first = 0;
     W.count = P.n_groups + (plan.tc_suffix ? P.B : 0);
     e = launch_attend_tc(P, W, maps.heads1, attend_tc_ctas(), s);
     if (e != cudaSuccess) return e;
   }
   if (plan.stream_rows) {
-    const bool early = plan.tc();
+    W.behind = !plan.tc();
     W.first = plan.tc_prefix ? P.n_groups : 0;
     W.count = P.n_groups + P.B - W.first;
     switch (plan.stream_rows * 8 + plan.heads) {
-      case 16 * 8 + 4: e = launch_stream<E, D, 1, 4>(P, W, maps, early, s); break;
-      case 16 * 8 + 2: e = launch_stream<E, D, 1, 2>(P, W, maps, early, s); break;
-      case 16 * 8 + 1: e = launch_stream<E, D, 1, 1>(P, W, maps, early, s); break;
-      case 32 * 8 + 2: e = launch_stream<E, D, 2, 2>(P, W, maps, early, s); break;
-      case 32 * 8 + 1: e = launch_stream<E, D, 2, 1>(P, W, maps, early, s); break;
-      default: e = launch_stream<E, D, 4, 1>(P, W, maps, early, s);
+      case 16 * 8 + 4: e = launch_stream<E, D, 1, 4>(P, W, maps, s); break;
+      case 16 * 8 + 2: e = launch_stream<E, D, 1, 2>(P, W, maps, s); break;
+      case 16 * 8 + 1: e = launch_stream<E, D, 1, 1>(P, W, maps, s); break;
+      case 32 * 8 + 2: e = launch_stream<E, D, 2, 2>(P, W, maps, s); break;
+      case 32 * 8 + 1: e = launch_stream<E, D, 2, 1>(P, W, maps, s); break;
+      default: e = launch_stream<E, D, 4, 1>(P, W, maps, s);
     }
     if (e != cudaSuccess) return e;
   }
@@ -664,7 +650,7 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
   shape.split = join_split((long long)join_rows * P.kv.hkv,
                            (long long)(P.table_stride + (P.n_groups ? P.prefix_stride : 0)) << P.kv.page_shift);
   const int warps = shape.split > kJoinWarps ? shape.split : kJoinWarps, cta_rows = 4 * warps / shape.split;
-  const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), warps * 32, 0, s, true);
+  const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), warps * 32, 0, s);
   return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
 }
 

@@ -42,6 +42,7 @@ __host__ __device__ inline long long tc_block(long long tok0, int G, int item, i
 
 struct AttendWork {
   int first, count;       // items of this launch: 0 .. n_groups - 1 prefixes, then the sequences
+  bool behind;            // the call's first kernel: waits for what comes before it in the stream
   AttendPieces prefix, suffix;
 };
 

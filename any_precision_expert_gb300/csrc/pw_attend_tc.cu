@@ -209,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicExch(err, kErrLayout);
     return;
   }
+  behind_the_stream();
+  let_next_start();
   const Walk::Mine mine = Walk::mine(P, W);
   PieceRing ring;
   ring.full = empty + 8 * C::SLOTS;
@@ -229,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) *abort_flag = 0;
   }
-  asm volatile("griddepcontrol.launch_dependents;");
   if (warp == kSoftmaxWarps + 3) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
   Walk walk;
   walk.start(P, W, mine, reinterpret_cast<unsigned*>(smem + C::SCRATCH_AT));
@@ -495,8 +496,8 @@ cudaError_t launch_typed(const AttendParams& P, const AttendWork& W, const KvMap
   const void* fn = reinterpret_cast<const void*>(attend_tc_kernel<E, D>);
   cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  attend_tc_kernel<E, D><<<ctas, kThreads, Cfg<D>::SMEM, s>>>(P, W, maps);
-  return cudaGetLastError();
+  const Launch at(dim3(ctas), kThreads, Cfg<D>::SMEM, s);
+  return cudaLaunchKernelEx(&at.cfg, attend_tc_kernel<E, D>, P, W, maps);
 }
 
 }  // namespace

@@ -45,6 +45,8 @@ __device__ __forceinline__ void stream_pair(const E* p, int a0, int a1, uint4& r
 
 template <typename E, int D, int U, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) {
+  behind_the_stream();
+  let_next_start();
   constexpr int LPR = D / 8;          // lanes a row
   constexpr int RPW = 32 / LPR;       // rows a warp holds side by side
   constexpr int ROWS = RPW * U;       // rows of a unit
@@ -149,11 +151,9 @@ cudaError_t launch_one(const RopeParams& P, cudaStream_t s) {
   const long long units = (long long)P.T * Chunks(P, 32 / (D / 8) * U).all();
   const long long blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (blocks > 0x7fffffffll || units > 0xffffff00ll) return cudaErrorInvalidConfiguration;
-  if (P.interleaved)
-    rope_kernel<E, D, U, true><<<(unsigned)blocks, kRopeThreads, 0, s>>>(P);
-  else
-    rope_kernel<E, D, U, false><<<(unsigned)blocks, kRopeThreads, 0, s>>>(P);
-  return cudaGetLastError();
+  const Launch at(dim3((unsigned)blocks), kRopeThreads, 0, s);
+  return P.interleaved ? cudaLaunchKernelEx(&at.cfg, rope_kernel<E, D, U, true>, P)
+                       : cudaLaunchKernelEx(&at.cfg, rope_kernel<E, D, U, false>, P);
 }
 
 template <typename E>

@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2048 / kVerifyThreads) verify_
   __shared__ Best all_best[2][kMaxCluster];   // [pass][CTA of the cluster], written by all of them
   __shared__ int all_any[2][kMaxCluster];
   __shared__ int s_any, s_best, s_kept, s_n;
+  behind_the_stream();
+  let_next_start();
   const cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
   const int b = blockIdx.x / parts, tid = threadIdx.x, lane = tid & 31, K = P.K, V = P.V;
@@ -185,17 +187,8 @@ cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s) {
   while (parts < most && P.V > 4 * kVerifyThreads * parts) parts *= 2;
   const bool vec = P.V % 4 == 0 && ((reinterpret_cast<uintptr_t>(P.p) | reinterpret_cast<uintptr_t>(P.q) |
                                      reinterpret_cast<uintptr_t>(P.noise)) & 15) == 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.B * parts);
-  cfg.blockDim = dim3(kVerifyThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, P) : cudaLaunchKernelEx(&cfg, verify_kernel<false>, P);
+  const Launch at(dim3(P.B * parts), kVerifyThreads, 0, s, parts);
+  return vec ? cudaLaunchKernelEx(&at.cfg, verify_kernel<true>, P) : cudaLaunchKernelEx(&at.cfg, verify_kernel<false>, P);
 }
 
 }  // namespace pw

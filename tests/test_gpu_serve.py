@@ -375,6 +375,78 @@ def test_attend_one_sequence_on_a_long_prefix(hkv, D):
     assert torch.equal(out, c.run(lse=False)[0])
 
 
+def test_calls_follow_each_other_and_other_kernels():
+    """Each call reads what the one before it in the stream wrote, with and without kernels of others between, many
+    times over and from a captured graph (copies, fills and joined streams in front of the calls)."""
+    rng = np.random.default_rng(20)
+    B, H, hk, D, page = 3, 8, 2, 64, 16
+    cache = pw.KvCache(*(torch.zeros(40, hk, page, D, dtype=torch.float16, device="cuda") for _ in range(2)), n_heads=H)
+    r = pw.Rotary(cos_sin(600, D), *(rand(rng, D, dtype=torch.float16) for _ in range(2)))
+    table = torch.arange(39, dtype=torch.int32, device="cuda").view(B, 13)
+    ws = torch.empty(cache.attend_workspace_size(B, 1, 0), dtype=torch.uint8, device="cuda")
+    steps = 100
+    k, v = (rand(rng, steps, B, hk, D, dtype=torch.float16) for _ in range(2))
+    q = rand(rng, steps, B, H, D, dtype=torch.float16)
+    lens, pos = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    x, qo, out = (torch.zeros(B, H, D, dtype=torch.float16, device="cuda") for _ in range(3))
+    kk, vv = (torch.zeros(B, hk, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    at = torch.zeros(1, dtype=torch.int64, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kk.copy_(k.index_select(0, at)[0])
+        vv.copy_(v.index_select(0, at)[0])
+        x.copy_(q.index_select(0, at)[0])
+        main.wait_stream(side)
+        slots = table.gather(1, (at // page).expand(B, 1))[:, 0] * page + (at % page).to(torch.int32)
+        pos.copy_(at.expand(B))
+        cache.append(kk, vv, slots.to(torch.int32), rotary=r, positions=pos, q=x, q_out=qo)
+        lens.add_(1)
+        cache.attend(qo, table, lens, out, ws)
+        cache.attend(out, table, lens, qo, ws)        # straight behind, on the same workspace
+        pw.qk_norm_rope(r, qo, None, pos, qo, None)   # in place, straight behind
+        pw.qk_norm_rope(r, qo, None, pos, out, None)
+        at.add_(1)
+        return out.clone()
+
+    eager = []
+    for _ in range(steps):
+        eager.append(step())
+    torch.cuda.synchronize()
+    assert cache.check_device() == 0
+    # each call alone, the device waited for in between
+    for t in (cache.k, cache.v, lens, at):
+        t.zero_()
+    for i in range(steps):
+        torch.cuda.synchronize()
+        for n in range(B):
+            pos[n] = i
+        slots = (table[:, i // page] * page + i % page).to(torch.int32)
+        cache.append(k[i], v[i], slots, rotary=r, positions=pos, q=q[i], q_out=qo)
+        torch.cuda.synchronize()
+        lens.fill_(i + 1)
+        cache.attend(qo, table, lens, out, ws)
+        torch.cuda.synchronize()
+        cache.attend(out, table, lens, qo, ws)
+        torch.cuda.synchronize()
+        pw.qk_norm_rope(r, qo, None, pos, qo, None)
+        torch.cuda.synchronize()
+        pw.qk_norm_rope(r, qo, None, pos, out, None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i]), i
+    for t in (cache.k, cache.v, lens, at):
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(steps):
+        g.replay()
+        assert torch.equal(got, eager[i]), i
+
+
 def test_cache_offsets_past_32_bits():
     page, D = 64, 128
     pages = (5 << 30) // (page * D * 2)          # 5 GB of keys: element offsets past 2^31
