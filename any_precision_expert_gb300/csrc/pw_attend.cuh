@@ -107,16 +107,13 @@ struct PieceRing {
     ++n;
     return true;
   }
-  // Reader, whole warp (or one thread of a warp that reads alone).
-  template <bool WARP>
+  // Reader, whole warp.
   __device__ __forceinline__ bool take(Piece& p) {
     const unsigned i = n % kPieces;
-    bool ok = mbar_wait(full + 8 * i, (n / kPieces) & 1, abort_flag, err);
-    if (WARP) ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * i, (n / kPieces) & 1, abort_flag, err))) return false;
     p = at[i];
-    if (WARP) __syncwarp();
-    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * i);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * i);
     ++n;
     return p.tile1 > 0;
   }

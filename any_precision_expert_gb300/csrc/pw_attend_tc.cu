@@ -6,14 +6,24 @@
 // 128-key tiles: S = Q K^T and O += P V are tcgen05.mma with accumulators in
 // tensor memory (S of both tiles, O of both tiles: all 512 columns); P takes
 // the place of S, two 16-bit weights a column, and is read from there as the
-// A operand.
+// A operand, which leaves shared memory to K, V and Q.
 //
 // Warps: a softmax warpgroup a row tile (one row a thread, so row maxima and
-// sums need no exchange), a TMA producer and one MMA warp a row tile.  While one tile's softmax runs, the tensor cores work on the other:
+// sums need no exchange), a TMA producer and one MMA warp a row tile.  While
+// one tile's softmax runs, the tensor cores work on the other:
 //   PV0(n) QK0(n+1) | PV1(n) QK1(n+1) | PV0(n+1) ...
 // O is rescaled only when a row's maximum has grown by more than 2^kGrow since
 // the last time; until then the weights may reach 2^(kShift + kGrow), which
 // fp16 still holds, and nothing is lost: the reference cancels in o / l.
+//
+// Measured (heads of 128, 1.9 GHz): 2850-2950 cycles a tile pair whose MMAs
+// take 2048, so 70% of their rate once it runs; what is left is the chain
+// scores -> softmax (1.2-1.4 k cycles) -> weights -> products of one row tile,
+// as P and S share their columns.  256 sequences of 4 rows a head on 32768
+// keys: 108 us, 1270 TFLOP/s, of which 6 us pass before a CTA's first scores
+// and 3 after its last.  One MMA warp for both row tiles took 3600 cycles,
+// half a row a softmax thread 3070-3250, weights in 4 parts 3190, in one part
+// 2945, the warpgroups not in turns 3450-4030.
 #include <math_constants.h>
 
 #include "pw_attend.cuh"
@@ -30,9 +40,11 @@ constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 // Registers: launched with 168 a thread; the softmax warps, a row of 128 scores a thread, take what the other four give
 // up (256 * 208 + 128 * 88 = 384 * 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kParts = 2;            // a tile's weights are handed over in this many parts
+constexpr int kParts = 2;            // a tile's weights are handed over in halves: P V starts on the first
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
-constexpr int kLeastUnits = 3;       // tiles a CTA takes at least
+// Tiles a CTA takes at least: fewer CTAs leave SMs to the streaming kernel and write fewer partial sums, more share the
+// work (64 sequences on a 2048-token prefix 96 / 94 / 97 / 101 us the call with 2 / 3 / 6 / 10).
+constexpr int kLeastUnits = 3;
 constexpr float kGrow = 8.f;
 
 template <int D>
@@ -62,7 +74,7 @@ struct Tiles {
   __device__ __forceinline__ bool next(PieceRing& ring) {
     first = false;
     if (++t < pc.tile1) return true;
-    if (!ring.take<true>(pc)) return false;
+    if (!ring.take(pc)) return false;
     t = pc.tile0;
     first = true;
     return true;
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned turns = 0, done = 0;  // turns taken, pieces finished
     bool ok = true;
     auto advance = [&]() {  // to the next piece with rows of this tile
-      while (ring.take<true>(pc)) {
+      while (ring.take(pc)) {
         if (active(pc, i)) return true;
         flat += pc.tile1 - pc.tile0;
       }
@@ -356,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
-        if (cur.len - t * kTile < kTile) {
-          // values past the length may be anything: 0 instead (one key a thread, every row tile for itself)
+        if (i == 0 && cur.len - t * kTile < kTile) {
+          // values past the length may be anything: 0 instead (one key a thread; the other row tile's turn comes after)
           const unsigned slot = 2 * flat + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
           if (!ok) break;

@@ -13,6 +13,9 @@
 // for long prompts, launch and load latency for a decode step.  A warp takes U
 // steps of rows of one token and kind (query, key or value), so that its loads
 // are in flight together and its cosines, sines and weights are loaded once.
+// Measured: 16384 tokens of 40 heads of 128 in 55 us, 6.3 TB/s (one row a warp
+// in flight 100 us, eight 76; with partners exchanged by shuffles 169); one
+// token 2.2 us, the launch.
 #include "pw_heads.cuh"
 #include "pw_serve.h"
 
@@ -158,7 +161,9 @@ cudaError_t launch_one(const RopeParams& P, cudaStream_t s) {
 
 template <typename E>
 cudaError_t launch_typed(const RopeParams& P, int d, cudaStream_t s) {
-  const bool few = (long long)P.T * (P.hq + P.hk + P.hv) * d < (1 << 21);
+  // Below 2^20 values one row step a warp, so that there are more warps (append of 128 tokens of 48 heads of 128: 2.26 us,
+  // 2.61 with four; of 256: 3.01 and 2.89; of 1024: 8.0 and 6.2).
+  const bool few = (long long)P.T * (P.hq + P.hk + P.hv) * d < (1 << 20);
   if (d == 128) return few ? launch_one<E, 128, 1>(P, s) : launch_one<E, 128, 4>(P, s);
   return few ? launch_one<E, 64, 1>(P, s) : launch_one<E, 64, 4>(P, s);
 }
