@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!more) break;
       policy = pc.prefix ? normal : once;
       for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
-        const int keys = min(TILE, pc.len - t * TILE), boxes = (keys + box - 1) / box;
-        const int at = t * TILE + lane * box;
+        const int kt = key_tile<TILE>(pc, t), keys = min(TILE, pc.len - kt * TILE), boxes = (keys + box - 1) / box;
+        const int at = kt * TILE + lane * box;
         int page = 0;
         if (lane < boxes) {
           page = table[at >> shift];
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int t = cur.tile0; t < cur.tile1; ++t) {
       // a wait that gives up leaves the sums as they are; the walk goes on, so that every barrier is met
       const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
-      const int first = t * TILE + k0;  // this warp's first key
+      const int first = key_tile<TILE>(cur, t) * TILE + k0;  // this warp's first key
       if (landed && first < cur.len) {
         const uint32_t kb = base + stage * C::STAGE + hb * HEAD, vb = kb + C::NH * C::HALF;
         float s[KPW / 8][4];

@@ -86,9 +86,17 @@ struct __align__(16) Piece {
   int first;                      // holds the segment's first tile
   int last_cta;                   // CTA that holds its last one
   int prefix, item;
+  int turn, pad[3];               // tile t of the piece is key tile t - turn, or that + tiles of the segment where negative
 };
 
 constexpr int kPieces = 4;        // pieces announced ahead
+
+// The key tile that a piece's tile t stands for.
+template <int TILE>
+__device__ __forceinline__ int key_tile(const Piece& p, int t) {
+  const int k = t - p.turn;
+  return k < 0 ? k + (p.len + TILE - 1) / TILE : k;
+}
 
 // Shared-memory ring of pieces: the producer writes, every reader warp takes each.
 struct PieceRing {
@@ -230,6 +238,14 @@ struct AttendWalk {
       p.last_cta = owner(seg_last);
       p.prefix = item < P.n_groups;
       p.item = item;
+      // Row tiles of the same keys begin at the same key tile in the first CTA that begins in them, so that these CTAs
+      // go through the keys side by side and find each other's lines in the L2.
+      p.turn = 0;
+      if (rt > 1) {
+        const unsigned begin = seg_last + 1 - su, c = owner(begin), at = c * share + min(c, more);
+        const unsigned ahead = at == begin ? 0 : at + share + (c < more) - begin;  // units up to the next CTA's start
+        if (ahead > COST && ahead - COST < (unsigned)kt) p.turn = ahead - COST;
+      }
       table = it.table;
       return true;
     }

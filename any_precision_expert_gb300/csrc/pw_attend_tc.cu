@@ -20,10 +20,12 @@
 // take 2048, so 70% of their rate once it runs; what is left is the chain
 // scores -> softmax (1.2-1.4 k cycles) -> weights -> products of one row tile,
 // as P and S share their columns.  256 sequences of 4 rows a head on 32768
-// keys: 108 us, 1270 TFLOP/s, of which 6 us pass before a CTA's first scores
-// and 3 after its last.  One MMA warp for both row tiles took 3600 cycles,
+// keys: 104 us, 1320 TFLOP/s, of which 6 us pass before a CTA's first scores
+// and 3 after its last.  Tried: one MMA warp for both row tiles 3600 cycles,
 // half a row a softmax thread 3070-3250, weights in 4 parts 3190, in one part
-// 2945, the warpgroups not in turns 3450-4030.
+// 3010, the warpgroups not in turns 3450-4030, the first half's weights taken
+// before the tile's maximum is known 3720, a branch for the scale's sign in
+// every tile 3150.
 #include <math_constants.h>
 
 #include "pw_attend.cuh"
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >> 2, w4 = warp & 3, r = tid & 127;
     const uint32_t lanes = (uint32_t)w4 << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + C::S_COL + i * 128, to = tmem + lanes + C::O_COL + i * 128;
-    const float sign = P.scale < 0.f ? -1.f : P.scale == 0.f ? 0.f : 1.f;  // other than 1: applied to the scores
+    const bool plain_q = P.scale > 0.f;  // a negative scale turns the queries around, a scale of 0 takes them away
     const float scale2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
     Piece pc = {};
     // Queries: a warp brings its 32 rows, whole lines at a time.
@@ -284,10 +286,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       each_row([&](int k, const E* src) {
         const int at = q_row + k * RPS + q_sub;
         const uint32_t dst = q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4);
-        if (src)
+        if (src && plain_q) {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        else
-          sts128(dst, make_uint4(0, 0, 0, 0));
+        } else {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (src && P.scale < 0.f) {
+            v = *reinterpret_cast<const uint4*>(src);
+            v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+          }
+          sts128(dst, v);
+        }
       });
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -311,10 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = cur.row0 + 128 * i + r;
       const int tok = min(row, cur.nrows - 1) / P.G;
       const int vis = cur.causal ? cur.len - P.ql + 1 + tok : cur.len;  // keys this row sees
+      const int sure = cur.causal ? cur.len - P.ql + 1 : cur.len;  // keys that every row sees
       const bool both = active(cur, 1);
       float m = -CUDART_INF_F;
       float2 l = make_float2(0.f, 0.f);
-      for (int t = cur.tile0; t < cur.tile1; ++t, ++n, ++flat) {
+      const int key_tiles = (cur.len + kTile - 1) / kTile;
+      int kt = key_tile<kTile>(cur, cur.tile0);
+      for (int t = cur.tile0; t < cur.tile1; ++t, ++n, ++flat, kt = kt + 1 == key_tiles ? 0 : kt + 1) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * i, n & 1, abort_flag, err));
         if (!ok) break;
         tc_fence_after();
@@ -325,13 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++turns;
         }
-        if (sign != 1.f) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * sign);
-        }
-        const int see = vis - t * kTile;
+        const int see = vis - kt * kTile;
         float top = -CUDART_INF_F;
-        if (__any_sync(0xffffffffu, see < kTile)) {
+        if ((kt + 1) * kTile > sure) {
           // what a row does not see counts as -infinity: a weight of 0
 #pragma unroll
           for (int k = 0; k < 128; ++k) {
@@ -368,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
-        if (i == 0 && cur.len - t * kTile < kTile) {
-          // values past the length may be anything: 0 instead (one key a thread; the other row tile's turn comes after)
+        if (i == 0 && cur.len - kt * kTile < kTile) {
+          // values past the length may be anything: 0 instead (one key a thread; the other row tile's turn comes after this)
           const unsigned slot = 2 * flat + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
           if (!ok) break;
-          if (r >= cur.len - t * kTile) {
+          if (r >= cur.len - kt * kTile) {
             const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
 #pragma unroll
             for (int b = 0; b < C::NH; ++b)
@@ -399,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_store_wait();
           tc_fence_before();
           mbar_arrive(p_full + 8 * (kParts * i + h));
+          if (h == 0 && both) mbar_arrive(turn + 8 * (i ^ 1));
         }
-        if (both) mbar_arrive(turn + 8 * (i ^ 1));
       }
       if (!ok) break;
       // the last S is out of the queries' way: the next piece's go in before this one's sums come out
@@ -452,8 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
         if (!more) break;
         for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
-          const int keys = min(kTile, pc.len - t * kTile), boxes = (keys + box - 1) / box;
-          const int at = t * kTile + lane * box, tok = at & ((1 << shift) - 1);
+          const int kt = key_tile<kTile>(pc, t);
+        const int keys = min(kTile, pc.len - kt * kTile), boxes = (keys + box - 1) / box;
+          const int at = kt * kTile + lane * box, tok = at & ((1 << shift) - 1);
           int page = 0;
           if (lane < boxes) {
             page = table[at >> shift];
