@@ -388,6 +388,7 @@ struct JoinShape {
 // GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).
 constexpr int kJoinWarps = 4;         // a CTA's, but for
 constexpr int kJoinMost = 16;
+constexpr int kJoinFlight = 4;        // pieces of a row that a warp has in flight
 inline int join_split(long long rows, long long keys) {
   return rows <= 608 && keys > 64 * 32 ? kJoinMost : rows <= 4096 ? kJoinWarps : 1;
 }
@@ -422,10 +423,11 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
   constexpr int NC = D / 64;  // times 8 values a lane
   const int lane = threadIdx.x & 31, hk = blockIdx.y, c8 = lane >> 2;
   const int warp = threadIdx.x >> 5, part = warp & (shape.split - 1);
-  const int r = (blockIdx.x * (blockDim.x / 32 / shape.split) + warp / shape.split) * 4 + (lane & 3);  // (query token, head of the group)
-  if (shape.split == 1 && r >= P.B * P.ql * P.G) return;
-  const bool live = r < P.B * P.ql * P.G;
-  const int n = live ? r / P.G : 0, h = live ? hk * P.G + r - n * P.G : 0, b = n / P.ql;
+  const int rows = P.B * P.ql * P.G;  // (query token, head of the group)
+  const int mine = (blockIdx.x * (blockDim.x / 32 / shape.split) + warp / shape.split) * 4 + (lane & 3);
+  const bool live = mine < rows;
+  if (shape.split == 1 && !live) return;
+  const int r = live ? mine : 0, n = r / P.G, h = hk * P.G + r - n * P.G, b = n / P.ql;
   int grp = P.n_groups - 1, tok0 = 0;  // the group of the sequence: the last that begins at or before it
   if (P.group_offsets && P.n_groups > 0) {
     int lo = 0, hi = P.n_groups - 1;
@@ -469,11 +471,11 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
   for (int k = 0; k < NC * 8; ++k) o[k] = 0.f;
   const int all = pc[0].count + pc[1].count;
 #pragma unroll 1
-  for (int p0 = 4 * part; p0 < all; p0 += 4 * shape.split) {
-    float2 ml[4];
-    float v[4][NC][8];
+  for (int p0 = kJoinFlight * part; p0 < all; p0 += kJoinFlight * shape.split) {
+    float2 ml[kJoinFlight];
+    float v[kJoinFlight][NC][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kJoinFlight; ++j) {
       const bool suf = p0 + j >= pc[0].count;
       const int p = p0 + j - (suf ? pc[0].count : 0), step = suf ? pc[1].step : pc[0].step;
       ml[j] = make_float2(-CUDART_INF_F, 0.f);
@@ -494,14 +496,16 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
 #pragma unroll
       for (int c = 0; c < NC; ++c) load8(src + c * far, v[j][c]);
     }
-    const float mm = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    float mm = m;
+#pragma unroll
+    for (int j = 0; j < kJoinFlight; ++j) mm = fmaxf(mm, ml[j].x);
     const float rr = mm == -CUDART_INF_F ? 0.f : mm, keep = ex2(m - rr);
     m = mm;
     l *= keep;
 #pragma unroll
     for (int k = 0; k < NC * 8; ++k) o[k] *= keep;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kJoinFlight; ++j) {
       const float w = ex2(ml[j].x - rr);
       l = fmaf(ml[j].y, w, l);
 #pragma unroll
