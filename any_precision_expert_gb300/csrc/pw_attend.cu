@@ -555,17 +555,28 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
 
 int stream_ctas() { return 2 * sm_count(); }
 
+// A prefix of little work (rows x keys x key heads, by what its table can hold) goes through the streaming kernel with
+// the suffixes: its own launch would cost more (12 sequences of 25 rows behind 3 tokens 16.1 -> 10.5 us, 23 of 11 behind
+// 1289 16.8 -> 11.7; 100 of 55 rows behind 320 48.8 -> 53.1 at 2.2e6, 70 of 25 behind 1116 24.9 -> 32.4 at 7.8e6).  Where
+// long suffixes keep that kernel waiting for HBM it takes eight times as much along (64 sequences of 4 rows, suffixes to
+// 1000: 35.5 -> 29.2 us at 2.1e6, to 4095: 95.2 -> 89.4 at 4.2e6; 32 of 4, to 4000: 62 -> 56 at 8.2e6).
+constexpr double kLittlePrefix = 2e6, kLongSuffix = 262144;  // the latter in keys x key heads of the whole batch
+
 // Which kernel takes which items.  Up to 64 rows a key head the streaming
 // kernel is bound by its loads; beyond, its products are.
 struct Plan {
   bool tc_prefix, tc_suffix;
   int stream_rows;     // rows of the streaming kernel's tiles, 0 when it has no items
   int heads;           // key heads of its stages
-  Plan(int G, int hkv, int B, int ql, int n_groups) {
+  // prefix_keys, suffix_keys: what a row of the prefix's and of the suffix's table can hold
+  Plan(int G, int hkv, int B, int ql, int n_groups, long long prefix_keys, long long suffix_keys) {
     const long long own = (long long)ql * G, shared = n_groups > 0 ? (B * own + n_groups - 1) / n_groups : 0;
+    const double work = (double)B * own * hkv * prefix_keys;
+    const bool waits = own <= 16 && (double)B * hkv * suffix_keys >= kLongSuffix;
+    const bool little = work <= (waits ? 8 : 1) * kLittlePrefix;
     tc_suffix = own > 64;
-    tc_prefix = n_groups > 0 && (shared > 64 || tc_suffix);
-    const long long rows = !tc_suffix && !tc_prefix && shared > own ? shared : own;
+    tc_prefix = n_groups > 0 && ((shared > 64 && !little) || tc_suffix);
+    const long long rows = !tc_suffix && !tc_prefix && shared > own && shared <= 64 ? shared : own;
     stream_rows = tc_suffix ? 0 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     heads = stream_rows == 16 ? 4 : stream_rows == 32 ? 2 : 1;
     while (hkv % heads || (heads > 1 && (long long)(B + (tc_prefix ? 0 : n_groups)) * (hkv / heads) < kFewSegments)) heads /= 2;
@@ -609,7 +620,8 @@ cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const KvMa
 
 template <typename E, int D>
 cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {
-  const Plan plan(P.G, P.kv.hkv, P.B, P.ql, P.n_groups);
+  const Plan plan(P.G, P.kv.hkv, P.B, P.ql, P.n_groups, (long long)P.prefix_stride << P.kv.page_shift,
+                  (long long)P.table_stride << P.kv.page_shift);
   const Layout L(plan, P.kv.hq, P.kv.hkv, D, P.B, P.ql, P.n_groups);
   char* w = static_cast<char*>(ws);
   auto pieces = [&](bool suffix, bool tc) {
@@ -690,7 +702,12 @@ cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps) {
 }
 
 size_t attend_ws_bytes(const KvView& kv, int B, int ql, int n_groups) {
-  return Layout(Plan(kv.hq / kv.hkv, kv.hkv, B, ql, n_groups), kv.hq, kv.hkv, kv.d, B, ql, n_groups).total;
+  size_t most = 0;  // whichever kernel a call's prefix table leads to
+  for (long long keys : {0ll, 1ll << 40}) {
+    const size_t n = Layout(Plan(kv.hq / kv.hkv, kv.hkv, B, ql, n_groups, keys, 0), kv.hq, kv.hkv, kv.d, B, ql, n_groups).total;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_attend(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s) {

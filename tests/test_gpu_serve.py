@@ -150,9 +150,11 @@ def test_append_flags_slots_past_the_cache():
 # ---- attention --------------------------------------------------------------
 
 class Case:
-    """A cache whose pages outside the sequences' own tokens hold NaN, with shuffled pages."""
+    """A cache whose pages outside the sequences' own tokens hold NaN, with shuffled pages.  wide: a prefix table with room
+    for a million tokens, so that groups of more than 64 rows take the tcgen05 kernel however short their prefixes are."""
 
-    def __init__(self, rng, lens, plens, offsets, hq, hkv, D, page, dtype, q_len=1, layout="head", width=None, qscale=2.0):
+    def __init__(self, rng, lens, plens, offsets, hq, hkv, D, page, dtype, q_len=1, layout="head", width=None, qscale=2.0,
+                 wide=False):
         B = len(lens)
         need = [-(-max(0, n) // page) for n in list(plens) + list(lens)]
         pages = rng.permutation(sum(need) + 2)
@@ -160,7 +162,8 @@ class Case:
         vc = kc.copy()
         width = max(need[len(plens):] + [0]) if width is None else width
         self.table = np.full((B, width), int(pages[-1]), dtype=np.int32)
-        self.ptable = np.full((len(plens), max(need[:len(plens)] + [0])), int(pages[-1]), dtype=np.int32)
+        pwidth = (1 << 20) // page if wide else max(need[:len(plens)] + [0])
+        self.ptable = np.full((len(plens), pwidth), int(pages[-1]), dtype=np.int32)
         at = 0
         for i, n in enumerate(list(plens) + list(lens)):
             row = self.ptable[i] if i < len(plens) else self.table[i - len(plens)]
@@ -232,10 +235,14 @@ ATTEND = [
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("i", range(len(ATTEND)))
-def test_attend_matches_oracle(i, dt):
+def test_attend_matches_oracle(i, wide, dt):
     lens, plens, off, hq, hkv, D, page, ql = ATTEND[i]
-    c = Case(np.random.default_rng(i), lens, plens, off, hq, hkv, D, page, TYPES[dt], ql, layout="token" if i % 3 == 1 else "head")
+    if wide and not plens:
+        pytest.skip("no prefix")
+    c = Case(np.random.default_rng(i), lens, plens, off, hq, hkv, D, page, TYPES[dt], ql, wide=wide,
+             layout="token" if i % 3 == 1 else "head")
     out, lse = c.run()
     c.check(out, lse)
     assert c.cache.check_device() == 0
@@ -244,6 +251,7 @@ def test_attend_matches_oracle(i, dt):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens,plens,off,hq,hkv,D,ql", [
     # more segments than CTAs, so that every CTA takes several: of many rows (groups of 80 and 40 rows a key head)
     ([9, 5] * 40, [150 + 7 * i for i in range(40)], [2 * i for i in range(40)] + [80], 64, 8, 64, 5),
@@ -252,8 +260,10 @@ def test_attend_matches_oracle(i, dt):
     ([i % 90 for i in range(400)], [], None, 16, 4, 64, 1),
     ([i % 70 for i in range(200)], [33], None, 12, 6, 128, 2),
     ([2 + i % 50 for i in range(120)], [40, 1], [0, 70, 120], 21, 3, 64, 2)])
-def test_attend_several_segments_a_cta(lens, plens, off, hq, hkv, D, ql):
-    c = Case(np.random.default_rng(len(lens)), lens, plens, off, hq, hkv, D, 16, torch.float16, ql)
+def test_attend_several_segments_a_cta(lens, plens, off, hq, hkv, D, ql, wide):
+    if wide and not plens:
+        pytest.skip("no prefix")
+    c = Case(np.random.default_rng(len(lens)), lens, plens, off, hq, hkv, D, 16, torch.float16, ql, wide=wide)
     out, lse = c.run()
     c.check(out, lse)
     assert c.cache.check_device() == 0
@@ -273,16 +283,17 @@ def test_attend_strided_queries_and_a_wide_table():
 @pytest.mark.parametrize("qscale", [0.0, 30.0])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_attend_flat_and_peaked_scores(dt, qscale):
-    c = Case(np.random.default_rng(8), [700, 33], [400], None, 8, 2, 64, 16, TYPES[dt], qscale=qscale)
-    c.check(*c.run())
-    c.scale = -c.scale
-    c.check(*c.run())
+    for lens, wide in (([700, 33], False), ([20, 3] * 20, True)):
+        c = Case(np.random.default_rng(8), lens, [400], None, 8, 2, 64, 16, TYPES[dt], qscale=qscale, wide=wide)
+        c.check(*c.run())
+        c.scale = -c.scale
+        c.check(*c.run())
 
 
 @pytest.mark.parametrize("ql,many", [(1, 1), (5, 1), (1, 80)])
 def test_attend_scores_that_keep_growing(ql, many):
     # every key beats the ones before it by more than any threshold a running maximum may wait for
-    c = Case(np.random.default_rng(9), [600] * many, [700], None, 4, 1, 64, 16, torch.float16, ql)
+    c = Case(np.random.default_rng(9), [600] * many, [700], None, 4, 1, 64, 16, torch.float16, ql, wide=many > 1)
     c.q[:] = 0
     c.q[..., 0] = 8.0
     for row, n in [(c.ptable[0], 700)] + [(c.table[b], 600) for b in range(many)]:
@@ -297,6 +308,15 @@ def test_attend_infinite_scores_follow_the_definition():
     out, _ = c.run()
     ref = S.attend(host(c.q)[:, 1:], host(c.k), host(c.v), c.table, c.lens, 1, c.scale, c.ptable, c.plens)[0]
     assert np.abs(host(out)[:, 1:] - ref).max() < 0.02  # the neighbouring head is not disturbed
+
+
+@pytest.mark.parametrize("page", [10 ** 6, -1, 2 ** 31 - 1])
+def test_attend_bad_prefix_pages_on_both_kernels(page):
+    for lens, wide in (([20, 3], False), ([20, 3] * 20, True)):
+        c = Case(np.random.default_rng(21), lens, [100], None, 8, 2, 128, 16, torch.bfloat16, wide=wide)
+        c.ptable[0, 2] = page       # reads as zeros
+        c.check(*c.run())
+        assert c.cache.check_device() == DEVICE_CHECK
 
 
 def test_attend_bad_tables_are_flagged_and_stay_inside():
@@ -324,8 +344,9 @@ def test_attend_bad_tables_are_flagged_and_stay_inside():
     assert torch.isfinite(out).all() and e.cache.check_device() == DEVICE_CHECK
 
 
-def test_attend_on_a_side_stream_and_in_a_graph():
-    c = Case(np.random.default_rng(15), [100, 7, 300] * 4, [200], None, 16, 4, 128, 16, torch.float16, 2)
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_on_a_side_stream_and_in_a_graph(wide):
+    c = Case(np.random.default_rng(15), [100, 7, 300] * 4, [200], None, 32, 4, 128, 16, torch.float16, 2, wide=wide)
     want, wl = c.run()
     s = torch.cuda.Stream()
     got, _ = c.run(stream=s)
@@ -350,7 +371,7 @@ def test_attend_on_a_side_stream_and_in_a_graph():
 
 @pytest.mark.parametrize("many", [1, 80])
 def test_attend_scale_of_zero_is_the_mean(many):
-    c = Case(np.random.default_rng(17), [50] * many, [70], None, 4, 1, 64, 16, torch.float16, layout="token")
+    c = Case(np.random.default_rng(17), [50] * many, [70], None, 4, 1, 64, 16, torch.float16, layout="token", wide=many > 1)
     c.scale = 0.0
     c.check(*c.run())
 
