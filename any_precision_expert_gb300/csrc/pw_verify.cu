@@ -19,8 +19,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 256;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 
 // The largest quotient so far and its index; the lower index wins among equal ones.
@@ -53,54 +51,63 @@ __device__ __forceinline__ void weigh(Best& best, int* cta_best, float r, float 
   }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void scan(Best& best, float& most, int* cta_best, const float* p, const float* q,
-                                     const float* e, int lo, int hi) {
-  constexpr int N = VEC ? 4 : 1, UN = VEC ? 1 : 4;  // values a load, loads of an array in flight
-  for (int i0 = lo + N * threadIdx.x; i0 < hi; i0 += N * UN * kVerifyThreads) {
-    float r[UN][N], c[UN][N];
+// N x UN values of each array in flight a thread: all loads of a step go out before anything waits for one.
+template <int N, int UN, bool Q>
+__device__ __forceinline__ void scan_step(Best& best, float& most, int* cta_best, const float* p, const float* q,
+                                          const float* e, int i0, int step) {
+  float r[UN][N], c[UN][N], d[UN][N];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int i = i0 + N * u * kVerifyThreads;
-#pragma unroll
-      for (int k = 0; k < N; ++k) r[u][k] = 0.f, c[u][k] = 1.f;
-      if (i >= hi) continue;
-      if constexpr (VEC) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i)), d = __ldcs(reinterpret_cast<const float4*>(e + i));
-        r[u][0] = a.x, r[u][1] = a.y, r[u][2] = a.z, r[u][3] = a.w;
-        c[u][0] = d.x, c[u][1] = d.y, c[u][2] = d.z, c[u][3] = d.w;
-        if (q) {
-          const float4 b = __ldcs(reinterpret_cast<const float4*>(q + i));
-          r[u][0] -= b.x, r[u][1] -= b.y, r[u][2] -= b.z, r[u][3] -= b.w;
-        }
-      } else {
-        r[u][0] = __ldcs(p + i);
-        c[u][0] = __ldcs(e + i);
-        if (q) r[u][0] -= __ldcs(q + i);
+  for (int u = 0; u < UN; ++u) {
+    const int i = i0 + u * step;
+    if constexpr (N == 4) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(p + i)), y = __ldcs(reinterpret_cast<const float4*>(e + i));
+      r[u][0] = x.x, r[u][1] = x.y, r[u][2] = x.z, r[u][3] = x.w;
+      c[u][0] = y.x, c[u][1] = y.y, c[u][2] = y.z, c[u][3] = y.w;
+      if constexpr (Q) {
+        const float4 z = __ldcs(reinterpret_cast<const float4*>(q + i));
+        d[u][0] = z.x, d[u][1] = z.y, d[u][2] = z.z, d[u][3] = z.w;
       }
+    } else {
+      r[u][0] = __ldcs(p + i);
+      c[u][0] = __ldcs(e + i);
+      if constexpr (Q) d[u][0] = __ldcs(q + i);
     }
-    const float bar = bar_of(__int_as_float(*reinterpret_cast<volatile int*>(cta_best)));
-    bool some = false;
+  }
+  const float bar = bar_of(__int_as_float(*reinterpret_cast<volatile int*>(cta_best)));
+  bool some = false;
+#pragma unroll
+  for (int u = 0; u < UN; ++u)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if constexpr (Q) r[u][k] -= d[u][k];
+      most = fmaxf(most, r[u][k]);
+      some |= r[u][k] >= bar * c[u][k];
+    }
+  if (some) {
 #pragma unroll
     for (int u = 0; u < UN; ++u)
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        most = fmaxf(most, r[u][k]);
-        some |= r[u][k] >= bar * c[u][k];
-      }
-    if (some) {
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (r[u][k] >= bar * c[u][k]) weigh(best, cta_best, r[u][k], c[u][k], i0 + N * u * kVerifyThreads + k);
-    }
+      for (int k = 0; k < N; ++k)
+        if (r[u][k] >= bar * c[u][k]) weigh(best, cta_best, r[u][k], c[u][k], i0 + u * step + k);
   }
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads, 2048 / kVerifyThreads) verify_kernel(const VerifyParams P) {
-  __shared__ Best warp_best[kVerifyWarps];
+template <bool VEC, int NT, bool Q>
+__device__ __forceinline__ void scan(Best& best, float& most, int* cta_best, const float* p, const float* q,
+                                     const float* e, int lo, int hi) {
+  constexpr int N = VEC ? 4 : 1, UN = VEC ? 1 : 4, STEP = N * NT;
+  int i = lo + N * threadIdx.x;
+#pragma unroll 1
+  for (; i + (UN - 1) * STEP < hi; i += UN * STEP) scan_step<N, UN, Q>(best, most, cta_best, p, q, e, i, STEP);
+  if constexpr (UN > 1) {
+#pragma unroll 1
+    for (; i < hi; i += STEP) scan_step<N, 1, Q>(best, most, cta_best, p, q, e, i, STEP);
+  }
+}
+
+template <bool VEC, int NT>
+__global__ void __launch_bounds__(NT, 2048 / NT) verify_kernel(const VerifyParams P) {
+  __shared__ Best warp_best[(NT / 32)];
   __shared__ Best all_best[2][kMaxCluster];   // [pass][CTA of the cluster], written by all of them
   __shared__ int all_any[2][kMaxCluster];
   __shared__ int s_any, s_best, s_kept, s_n;
@@ -149,13 +156,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2048 / kVerifyThreads) verify_
   for (int pass = 0; pass < 2; ++pass) {  // the second only where the residual has no positive entry
     Best best = {0.f, lo < V ? lo : 0x7fffffff};  // quotients of 0: the lowest index
     float most = 0.f;
-    scan<VEC>(best, most, &s_best, p, q, e, lo, hi);
+    if (q)
+      scan<VEC, NT, true>(best, most, &s_best, p, q, e, lo, hi);
+    else
+      scan<VEC, NT, false>(best, most, &s_best, p, q, e, lo, hi);
     best.warp();
     if (lane == 0) warp_best[tid >> 5] = best;
     if (most > 0.f) s_any = 1;
     __syncthreads();
     if (tid < 32) {
-      best = lane < kVerifyWarps ? warp_best[lane] : Best{0.f, 0x7fffffff};
+      best = lane < (NT / 32) ? warp_best[lane] : Best{0.f, 0x7fffffff};
       best.warp();
       if (lane < parts) {
         *cluster.map_shared_rank(&all_best[pass][part], lane) = best;
@@ -174,23 +184,31 @@ __global__ void __launch_bounds__(kVerifyThreads, 2048 / kVerifyThreads) verify_
     q = nullptr;
   }
   if (part != 0) return;
-  for (int i = tid; i <= K; i += kVerifyThreads)
+  for (int i = tid; i <= K; i += NT)
     P.out[(size_t)b * (K + 1) + i] = i < kept ? P.tokens[(size_t)b * K + i] : i == kept ? next : -1;
   if (tid == 0) P.accepted[b] = kept;
 }
 
 }  // namespace
 
+namespace {
+template <int NT>
+cudaError_t launch_shape(const VerifyParams& P, bool vec, int parts, cudaStream_t s) {
+  const Launch at(dim3(P.B * parts), NT, 0, s, parts);
+  return vec ? cudaLaunchKernelEx(&at.cfg, verify_kernel<true, NT>, P) : cudaLaunchKernelEx(&at.cfg, verify_kernel<false, NT>, P);
+}
+}  // namespace
+
 cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s) {
-  // Shares of at least one step of every thread; eight CTAs a sequence, four where those fill the GPU twice over
-  // (measured: 256 sequences of 131072 54 us with four, 57 with eight; 4 of 32000 8.2 and 6.3 us).
-  const int most = 4 * P.B >= 2 * sm_count() ? 4 : kMaxCluster;
-  int parts = 1;
-  while (parts < most && P.V > 4 * kVerifyThreads * parts) parts *= 2;
   const bool vec = P.V % 4 == 0 && ((reinterpret_cast<uintptr_t>(P.p) | reinterpret_cast<uintptr_t>(P.q) |
                                      reinterpret_cast<uintptr_t>(P.noise)) & 15) == 0;
-  const Launch at(dim3(P.B * parts), kVerifyThreads, 0, s, parts);
-  return vec ? cudaLaunchKernelEx(&at.cfg, verify_kernel<true>, P) : cudaLaunchKernelEx(&at.cfg, verify_kernel<false>, P);
+  // Eight CTAs a sequence and at least a step of every thread, four where those alone are many (256 sequences of 131072 50.7
+  // us with four, 52.6 with eight); CTAs of 512 threads while two of 256 on every SM would not be filled (14 sequences of
+  // 131072 9.8 and 14.1 us, 91 of 94207 23.1 and 21.6).
+  const int most = 4 * P.B >= 1000 ? 4 : kMaxCluster;
+  int parts = 1;
+  while (parts < most && P.V > 1024 * parts) parts *= 2;
+  return (long long)P.B * parts > 2 * sm_count() ? launch_shape<256>(P, vec, parts, s) : launch_shape<512>(P, vec, parts, s);
 }
 
 }  // namespace pw
