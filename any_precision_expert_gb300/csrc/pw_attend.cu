@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(kJoinMost * 32) join_kernel(const AttendParams
   }
   const bool has[2] = {grp >= 0 && min(P.prefix_lens[grp], P.prefix_stride << P.kv.page_shift) > 0,
                        min(P.lens[b], P.table_stride << P.kv.page_shift) > 0};
-  behind_the_stream();  // what comes before reads inputs that the kernels before this one read, too
+  // What comes before this line reads the call's inputs only: this kernel starts once every CTA of the one before it in
+  // the call has waited for the stream itself.
+  behind_the_stream();
   let_next_start();
   const long long row = (long long)n * P.kv.hq + h;
   Pieces pc[2];

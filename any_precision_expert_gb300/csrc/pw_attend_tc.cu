@@ -45,7 +45,7 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kParts = 2;            // a tile's weights are handed over in halves: P V starts on the first
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
 // Tiles a CTA takes at least: fewer CTAs leave SMs to the streaming kernel and write fewer partial sums, more share the
-// work (64 sequences on a 2048-token prefix 96 / 94 / 97 / 101 us the call with 2 / 3 / 6 / 10).
+// work (64 sequences on a 2048-token prefix, sent here: 96 / 94 / 97 / 101 us the call with 2 / 3 / 6 / 10).
 constexpr int kLeastUnits = 3;
 constexpr float kGrow = 8.f;
 
