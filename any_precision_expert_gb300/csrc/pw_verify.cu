@@ -11,6 +11,8 @@
 // (6.4 TB/s; 108 us when every index was divided); 4 over 32000 4.7 us.
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "pw_serve.h"
 
 namespace pw {
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) verify_kernel(const VerifyParam
   behind_the_stream();
   let_next_start();
   const cg::cluster_group cluster = cg::this_cluster();
+  auto started = cluster.barrier_arrive();  // every CTA runs before another one writes to its shared memory
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
   const int b = blockIdx.x / parts, tid = threadIdx.x, lane = tid & 31, K = P.K, V = P.V;
   if (tid == 0) s_any = s_best = 0;
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) verify_kernel(const VerifyParam
     if (lane == 0) warp_best[tid >> 5] = best;
     if (most > 0.f) s_any = 1;
     __syncthreads();
+    if (pass == 0) cluster.barrier_wait(std::move(started));
     if (tid < 32) {
       best = lane < (NT / 32) ? warp_best[lane] : Best{0.f, 0x7fffffff};
       best.warp();
