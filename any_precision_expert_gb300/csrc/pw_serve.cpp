@@ -194,8 +194,8 @@ extern "C" pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* a, void* ws,
   const pw_status st = pw_kv_attend_workspace_size(kv, a->batch, a->q_len, a->n_groups, &need);
   if (st != PW_OK) return st;
   if (!std::isfinite(a->scale) || a->table_stride < 0 || a->prefix_stride < 0) return PW_ERR_INVALID_ARG;
-  if (((long long)a->table_stride << w.page_shift) > 0x7fffffffll ||
-      ((long long)a->prefix_stride << w.page_shift) > 0x7fffffffll)
+  constexpr long long kMostKeys = 0x7ffff000ll;  // whole tiles of them still count in 32 bits
+  if (((long long)a->table_stride << w.page_shift) > kMostKeys || ((long long)a->prefix_stride << w.page_shift) > kMostKeys)
     return PW_ERR_INVALID_ARG;
   if (a->batch > 0) {
     if (bad_rows(&a->q) || bad_rows(&a->out) || !aligned4(a->lse)) return PW_ERR_INVALID_ARG;

@@ -124,6 +124,18 @@ def test_attend_arguments(want, kw):
     lib.pw_kv_destroy(h)
 
 
+@pytest.mark.parametrize("side", ["table_stride", "prefix_stride"])
+def test_attend_keys_that_do_not_count_in_32_bits(side):
+    st, h = cache()  # pages of 16
+    for stride, want in (((1 << 27) - 1, INVALID), ((1 << 27) - 255, INVALID), ((1 << 27) - 256, UNSUPPORTED)):
+        d = dict(q=Rows(*ROWS), out=Rows(*ROWS), lse=None, batch=1, q_len=1, scale=1.0, table=P, table_stride=4, lens=P,
+                 n_groups=1, group_offsets=None, prefix_table=P, prefix_stride=4, prefix_lens=P)
+        d[side] = stride
+        desc = AttendDesc(**d)
+        assert lib.pw_kv_attend(h, C.byref(desc), P, C.c_size_t(1 << 30), None) == want
+    lib.pw_kv_destroy(h)
+
+
 @pytest.mark.parametrize("want,kw", [
     (UNSUPPORTED, {}), (UNSUPPORTED, dict(B=0)), (UNSUPPORTED, dict(K=0, q=None, tokens=None, n=None, u=None)),
     (INVALID, dict(B=-1)), (INVALID, dict(B=65536)), (INVALID, dict(K=-1)), (INVALID, dict(K=65)), (INVALID, dict(V=0)),
