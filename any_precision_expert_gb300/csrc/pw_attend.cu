@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
+    bool odd_seen = false;
     for (int t = cur.tile0; t < cur.tile1; ++t) {
       // a wait that gives up leaves the sums as they are; the walk goes on, so that every barrier is met
       const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
@@ -281,6 +282,15 @@ __global__ void __launch_bounds__(kThreads, 2)
           pf[n / 2][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
           pf[n / 2][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
         }
+        bool odd = false;  // some value that is no number, at a key that some rows do not see
+        if (first + KPW > sure && sure < cur.len) {
+          const int lo = max(sure - first, 0), hi = min(cur.len - first, KPW);
+          for (int k = 8 * C::NH * lo + lane; k < 8 * C::NH * hi; k += 32)
+            odd |= !all_finite<E>(shared16(vb + (k & (C::NH - 1)) * C::HALF + (k0 + k / (8 * C::NH)) * 128 +
+                                           16 * (k / C::NH & 7)));
+          odd = __any_sync(0xffffffffu, odd);
+          odd_seen |= odd;
+        }
         const bool tail = first + KPW > cur.len;  // values past the length may be anything: 0 instead
 #pragma unroll
         for (int n = 0; n < KPW / 16; ++n) {
@@ -295,6 +305,11 @@ __global__ void __launch_bounds__(kThreads, 2)
               b[0] = keep_keys(b[0], 2 * t4, left), b[1] = keep_keys(b[1], 2 * t4 + 8, left);
               b[2] = keep_keys(b[2], 2 * t4, left), b[3] = keep_keys(b[3], 2 * t4 + 8, left);
             }
+            if (odd) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                b[i] = finite_bits<E>(b[i]) & b[i] | keep_keys(b[i], 2 * t4 + 8 * (i & 1), sure - first - 16 * n);
+            }
             mma16816<E>(o[2 * d], pf[n], b[0], b[1]);
             mma16816<E>(o[2 * d + 1], pf[n], b[2], b[3]);
           }
@@ -305,6 +320,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (++stage == C::STAGES) stage = 0, phase ^= 1;
     }
 
+    if (odd_seen) {  // the rows that see them get them here
+      const int* table = P.table + (long long)(cur.item - P.n_groups) * P.table_stride;
+#pragma unroll 1
+      for (int t = cur.tile0; t < cur.tile1; ++t) {
+        const int at = key_tile<TILE>(cur, t) * TILE + k0;
+#pragma unroll 1
+        for (int key = max(max(sure, 0), at); key < min(cur.len, at + KPW); ++key) {
+          const int page = table[key >> P.kv.page_shift];
+          if (page < 0 || page >= P.kv.n_pages) continue;
+          const E* src = reinterpret_cast<const E*>(P.kv.v) + page * P.kv.page_stride + (cur.head + hb) * P.kv.head_stride +
+                         (key & ((1 << P.kv.page_shift) - 1)) * P.kv.token_stride + 2 * t4;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 x = Pair<E>::up(*reinterpret_cast<const typename Pair<E>::V*>(src + 8 * d));
+              if (key < vis[i]) {
+                if (!isfinite(x.x)) o[d][2 * i] += x.x;
+                if (!isfinite(x.y)) o[d][2 * i + 1] += x.y;
+              }
+            }
+        }
+      }
+    }
     have = ring.take(pc);
     if (have) load_q();  // on their way while this piece's sums are stored
 

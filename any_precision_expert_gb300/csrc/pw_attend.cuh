@@ -280,6 +280,25 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A query's weight for a key that it does not see is 0, but 0 times an infinity or NaN is NaN.  Values at keys that only
+// some rows of a sequence see (the last q_len - 1) are therefore looked at, and those that are no numbers kept from the
+// other rows.
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// Ones where the two 16-bit values of a word are finite.
+template <typename E>
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7c00u : 0x7f80u;
+  return ((w & kExp) == kExp ? 0u : 0xffffu) | ((w >> 16 & kExp) == kExp ? 0u : 0xffff0000u);
+}
+template <typename E>
+__device__ __forceinline__ bool all_finite(const uint4& v) {
+  return (finite_bits<E>(v.x) & finite_bits<E>(v.y) & finite_bits<E>(v.z) & finite_bits<E>(v.w)) == 0xffffffffu;
+}
+
 // The tensor-core kernel for prefix groups with many rows (pw_attend_tc.cu).
 constexpr int kTcRows = 256;
 cudaError_t launch_attend_tc(const AttendParams& P, const AttendWork& W, const KvMaps& maps, int ctas, cudaStream_t s);

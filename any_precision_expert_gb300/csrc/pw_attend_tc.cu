@@ -207,6 +207,31 @@ __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t
   }
 }
 
+// Adds to 32 of a row's sums the values that are no numbers, of the piece's keys from lo on that the row sees.
+template <typename E>
+__device__ __forceinline__ void add_odd(const AttendParams& P, const Piece& pc, int lo, int vis, int col, uint32_t (&o)[32]) {
+  const int* table = P.table + (long long)(pc.item - P.n_groups) * P.table_stride;
+#pragma unroll 1
+  for (int t = pc.tile0; t < pc.tile1; ++t) {
+    const int at = key_tile<kTile>(pc, t) * kTile;
+#pragma unroll 1
+    for (int key = max(max(lo, 0), at); key < min(vis, at + kTile); ++key) {
+      const int page = table[key >> P.kv.page_shift];
+      if (page < 0 || page >= P.kv.n_pages) continue;
+      const E* src = reinterpret_cast<const E*>(P.kv.v) + page * P.kv.page_stride + pc.head * P.kv.head_stride +
+                     (key & ((1 << P.kv.page_shift) - 1)) * P.kv.token_stride + col;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        float x[8];
+        unpack8<E>(*reinterpret_cast<const uint4*>(src + c), x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (!isfinite(x[k])) o[c + k] = __float_as_uint(__uint_as_float(o[c + k]) + x[k]);
+      }
+    }
+  }
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ KvMaps maps) {
@@ -216,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::SLOTS, bars = empty + 8 * C::SLOTS + 16 * kPieces;
   const uint32_t q_full = bars, s_full = bars + 16, o_done = bars + 32, turn = bars + 48, p_full = bars + 64;  // p_full: [row tile][part]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 16);
+  volatile int* odd_seen = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 12);  // values that are no numbers were taken out
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::PIECE_AT - 8);
   int* err = P.kv.err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -243,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full + 8 * tid, count);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid == 0) *abort_flag = 0;
+    if (tid == 0) *abort_flag = *odd_seen = 0;
   }
   if (warp == kSoftmaxWarps + 3) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
   Walk walk;
@@ -375,13 +401,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
-        if (i == 0 && cur.len - kt * kTile < kTile) {
-          // values past the length may be anything: 0 instead (one key a thread; the other row tile's turn comes after this)
+        if (i == 0 && (kt + 1) * kTile > sure) {
+          // values past the length may be anything: 0 instead (one key a thread; the other row tile's turn comes after
+          // this); so for those that are no numbers and that some rows do not see, which the others get at the end
           const unsigned slot = 2 * flat + 1;
           ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
           if (!ok) break;
-          if (r >= cur.len - kt * kTile) {
-            const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
+          const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
+          const int key = kt * kTile + r;
+          if (key >= sure && key < cur.len) {
+#pragma unroll 1
+            for (int c = 0; c < 8 * C::NH; ++c) {
+              const uint32_t to = at + (c >> 3) * C::HALF + 16 * (c & 7);
+              const uint4 v = shared16(to);
+              if (!all_finite<E>(v)) {
+                sts128(to, make_uint4(v.x & finite_bits<E>(v.x), v.y & finite_bits<E>(v.y), v.z & finite_bits<E>(v.z),
+                                      v.w & finite_bits<E>(v.w)));
+                *odd_seen = 1;
+              }
+            }
+          }
+          if (key >= cur.len) {
 #pragma unroll
             for (int b = 0; b < C::NH; ++b)
 #pragma unroll
@@ -416,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
+      // the wait is over already: it makes what any thread of the first row tile has seen known here
+      const bool odd = sure < cur.len && mbar_wait(p_full + 8 * (kParts * i + kParts - 1), (n - 1) & 1, abort_flag, err) && *odd_seen;
       const AttendPieces& dst = cur.prefix ? W.prefix : W.suffix;
       const bool in = row < cur.nrows;
       const long long grow = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + row - tok * P.G;
@@ -438,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_load32(to + c, o);
+        if (odd && in) add_odd<E>(P, cur, sure, vis, c, o);
         if (in) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8) store8(out + (c + k) / 8 * column, o + k);
@@ -460,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
         for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
           const int kt = key_tile<kTile>(pc, t);
-        const int keys = min(kTile, pc.len - kt * kTile), boxes = (keys + box - 1) / box;
+          const int keys = min(kTile, pc.len - kt * kTile), boxes = (keys + box - 1) / box;
           const int at = kt * kTile + lane * box, tok = at & ((1 << shift) - 1);
           int page = 0;
           if (lane < boxes) {

@@ -646,7 +646,8 @@ pw_status pw_kv_append(pw_kv_t kv, const pw_rotary* rot, const int32_t* position
  * (q . key) over what a query sees,
  *   out = sum e^s value / sum e^s,   lse = ln(sum e^s)
  * A query that sees nothing gets out = 0 and lse = -infinity.  Cache contents
- * at and past a length are never used, whatever they hold (NaN included).
+ * at and past a length are never used, whatever they hold (NaN included), nor
+ * are keys and values of the q_len tokens by a query that comes before them.
  * Scores, the softmax and the sums are fp32; the weights e^s are rounded to
  * the heads' type for the products with the values.
  */
@@ -671,6 +672,7 @@ typedef struct {
  * o[g] <= o[g+1] <= batch, and a page outside [0, n_pages) reads as zeros; all
  * three are flagged.  A sequence outside every group has no prefix; one that
  * descending offsets put into two groups gets unspecified values.
+ * PW_ERR_INVALID_ARG when a table's row could hold more than 2^31 - 4096 tokens,
  * PW_ERR_UNSUPPORTED when the tables could hold more than 2 * 10^9 (64 tokens x
  * 16 query rows x key head) tiles.
  * ws: device scratch of at least pw_kv_attend_workspace_size() bytes, 256-byte

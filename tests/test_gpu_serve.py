@@ -310,6 +310,36 @@ def test_attend_infinite_scores_follow_the_definition():
     assert np.abs(host(out)[:, 1:] - ref).max() < 0.02  # the neighbouring head is not disturbed
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,plens,hq,hkv,D,page,ql,wide", [
+    ([40, 130, 3, 5, 300], [], 8, 2, 128, 16, 5, False),
+    ([66, 2, 64], [30], 4, 4, 64, 8, 3, False),                    # four heads a stage
+    ([129, 700], [50], 16, 1, 128, 64, 4, False),                  # 64 rows
+    ([131] * 30, [300], 8, 2, 64, 16, 2, True),
+    ([40, 140, 257], [], 8, 2, 128, 16, 17, False),                # suffixes in the tcgen05 kernel
+    ([33, 190, 10], [20], 32, 2, 64, 16, 33, False),               # several row tiles
+    ([64, 128, 129], [], 4, 2, 128, 256, 64, False)])
+def test_attend_values_that_are_no_numbers_reach_only_the_queries_that_see_them(lens, plens, hq, hkv, D, page, ql, wide, dt):
+    c = Case(np.random.default_rng(31), lens, plens, None, hq, hkv, D, page, TYPES[dt], ql, qscale=0.5, wide=wide)
+    clean, lse = c.run()
+    want = clean.clone()
+    for b, n in enumerate(lens):
+        for i, (t, x) in enumerate([(n - 1, float("nan")), (n - 1, float("-inf")), (n - ql + 1, float("inf")),
+                                    (n - 1 - ql // 2, float("nan"))]):
+            if t < 0:
+                continue
+            h, d = i % hkv, (37 * i + 5 + b) % D
+            c.v[int(c.table[b, t // page]), h, t % page, d] = x
+            first = max(0, t - n + ql)   # the first query that sees key t
+            G = hq // hkv
+            want[b * ql + first:(b + 1) * ql, h * G:(h + 1) * G, d] = x
+    out, lse2 = c.run()
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(out, nan=7.0), torch.nan_to_num(want, nan=7.0))
+    assert torch.equal(lse, lse2)
+    assert c.cache.check_device() == 0
+
+
 @pytest.mark.parametrize("page", [10 ** 6, -1, 2 ** 31 - 1])
 def test_attend_bad_prefix_pages_on_both_kernels(page):
     for lens, wide in (([20, 3], False), ([20, 3] * 20, True)):
