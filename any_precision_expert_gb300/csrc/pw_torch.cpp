@@ -45,7 +45,7 @@ int dtype_of(const at::Tensor& t, const char* what) {
   fail(what, "heads are float16 or bfloat16");
 }
 
-// [T][H][D] head rows of a type on the device of `like`.
+// [T][H][D] head rows of the type and on the device of `like`.
 pw_rows rows(const at::Tensor& t, int64_t T, int64_t H, int64_t D, const at::Tensor& like, const char* what) {
   if (t.dim() != 3 || t.size(0) != T || t.size(1) != H || t.size(2) != D) fail(what, "wrong shape");
   if (t.scalar_type() != like.scalar_type()) fail(what, "wrong type");
@@ -122,50 +122,56 @@ pw_status rope(PyObject* const* a) {
                          vec<int32_t>(a[6], at::kInt, *some, "err", 1), stream(a[7], *some));
 }
 
-// (handle, n_heads, n_kv_heads, head_dim, k, v, slots, rotary, positions, q, q_out, stream)
+// The cache's keys [pages][key heads][tokens][D] come with its calls: the library reads head rows by the handle's type, so
+// every tensor of a call is held against the cache's own type and device here.
+
+// (handle, cache k, n_heads, k, v, slots, rotary, positions, q, q_out, stream)
 pw_status append(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
-  const int64_t hq = integer(a[1]), hk = integer(a[2]), D = integer(a[3]);
-  const at::Tensor &k = tensor(a[4], "k"), &v = tensor(a[5], "v");
+  const at::Tensor& cache = tensor(a[1], "cache");
+  const int64_t hq = integer(a[2]), hk = cache.size(1), D = cache.size(3);
+  const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
   const int64_t T = k.dim() == 3 ? k.size(0) : -1;
-  const pw_rows rk = rows(k, T, hk, D, k, "k"), rv = rows(v, T, hk, D, k, "v");
-  const pw_rotary* r = rotary(a[7], dtype_of(k, "k"), D);
-  const at::Tensor* q = maybe(a[9], "q");
+  const pw_rows rk = rows(k, T, hk, D, cache, "k"), rv = rows(v, T, hk, D, cache, "v");
+  const pw_rotary* r = rotary(a[6], dtype_of(cache, "cache"), D);
+  const at::Tensor* q = maybe(a[8], "q");
   pw_rows rq = {}, rqo = {};
-  if (q) rq = rows(*q, T, hq, D, k, "q"), rqo = rows(tensor(a[10], "q_out"), T, hq, D, k, "q_out");
-  return pw_kv_append(kv, r, vec<const int32_t>(a[8], at::kInt, k, "positions", T),
-                      vec<const int32_t>(a[6], at::kInt, k, "slots", T), (int)T, &rk, &rv, &rq, &rqo, stream(a[11], k));
+  if (q) rq = rows(*q, T, hq, D, cache, "q"), rqo = rows(tensor(a[9], "q_out"), T, hq, D, cache, "q_out");
+  return pw_kv_append(kv, r, vec<const int32_t>(a[7], at::kInt, cache, "positions", T),
+                      vec<const int32_t>(a[5], at::kInt, cache, "slots", T), (int)T, &rk, &rv, &rq, &rqo,
+                      stream(a[10], cache));
 }
 
-// (handle, n_heads, head_dim, q, table, lens, out, ws, q_len, scale, prefix_table, prefix_lens, group_offsets, lse, stream)
+// (handle, cache k, n_heads, q, table, lens, out, ws, q_len, scale, prefix_table, prefix_lens, group_offsets, lse, stream)
 pw_status attend(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
-  const int64_t hq = integer(a[1]), D = integer(a[2]);
+  const at::Tensor& cache = tensor(a[1], "cache");
+  const int64_t hq = integer(a[2]), D = cache.size(3);
   const at::Tensor &q = tensor(a[3], "q"), &table = tensor(a[4], "table"), &out = tensor(a[6], "out");
   if (table.dim() != 2) fail("table", "must be [batch, pages]");
   pw_attend_desc d = {};
   const int64_t B = table.size(0);
   d.batch = (int)B;
   d.q_len = small(a[8], "q_len");
-  d.q = rows(q, B * d.q_len, hq, D, q, "q");
-  d.out = rows(out, B * d.q_len, hq, D, q, "out");
-  d.lse = vec<float>(a[13], at::kFloat, q, "lse", B * d.q_len, hq);
+  d.q = rows(q, B * d.q_len, hq, D, cache, "q");
+  d.out = rows(out, B * d.q_len, hq, D, cache, "out");
+  d.lse = vec<float>(a[13], at::kFloat, cache, "lse", B * d.q_len, hq);
   d.scale = (float)PyFloat_AsDouble(a[9]);
   if (PyErr_Occurred()) throw Bad();
   d.table_stride = (int)table.size(1);
-  d.table = vec<const int32_t>(a[4], at::kInt, q, "table", B, d.table_stride);
-  d.lens = vec<const int32_t>(a[5], at::kInt, q, "lens", B);
+  d.table = vec<const int32_t>(a[4], at::kInt, cache, "table", B, d.table_stride);
+  d.lens = vec<const int32_t>(a[5], at::kInt, cache, "lens", B);
   if (a[11] != Py_None) {
     const at::Tensor& pt = tensor(a[10], "prefix_table");
     if (pt.dim() != 2) fail("prefix_table", "must be [groups, pages]");
     d.n_groups = (int)pt.size(0);
     d.prefix_stride = (int)pt.size(1);
-    d.prefix_table = vec<const int32_t>(a[10], at::kInt, q, "prefix_table", d.n_groups, d.prefix_stride);
-    d.prefix_lens = vec<const int32_t>(a[11], at::kInt, q, "prefix_lens", d.n_groups);
-    d.group_offsets = vec<const int32_t>(a[12], at::kInt, q, "group_offsets", d.n_groups + 1);
+    d.prefix_table = vec<const int32_t>(a[10], at::kInt, cache, "prefix_table", d.n_groups, d.prefix_stride);
+    d.prefix_lens = vec<const int32_t>(a[11], at::kInt, cache, "prefix_lens", d.n_groups);
+    d.group_offsets = vec<const int32_t>(a[12], at::kInt, cache, "group_offsets", d.n_groups + 1);
   }
   const at::Tensor* ws = maybe(a[7], "ws");
-  return pw_kv_attend(kv, &d, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, stream(a[14], q));
+  return pw_kv_attend(kv, &d, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, stream(a[14], cache));
 }
 
 // (target_p, draft_p, tokens, n_draft, u, noise, out, accepted, err, stream)
@@ -184,7 +190,7 @@ pw_status verify(PyObject* const* a) {
 }
 
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<rope>(a, n, 8); }
-PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<append>(a, n, 12); }
+PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<append>(a, n, 11); }
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<attend>(a, n, 15); }
 PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<verify>(a, n, 10); }
 

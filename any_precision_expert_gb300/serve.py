@@ -83,8 +83,8 @@ class KvCache:
     def append(self, k, v, slots, rotary: Rotary = None, positions=None, q=None, q_out=None, stream=None):
         """Append keys (normed and rotated when rotary is given) and values [T, Hkv, D] at int32 slots [T], and norm
         and rotate the queries q [T, Hq, D] into q_out in the same launch (pw_kv_append)."""
-        st = _pw_torch.append(self.handle, self.n_heads, self.n_kv_heads, self.head_dim, k, v, slots,
-                              None if rotary is None else rotary._key, positions, q, q_out, stream)
+        st = _pw_torch.append(self.handle, self.k, self.n_heads, k, v, slots, None if rotary is None else rotary._key,
+                              positions, q, q_out, stream)
         if st:
             check(st, "pw_kv_append")
 
@@ -100,7 +100,7 @@ class KvCache:
         behind its group's shared prefix (prefix_table int32 [groups, pages], prefix_lens int32 [groups],
         group_offsets int32 [groups + 1]; one group over the whole batch needs no offsets), into out and, when given,
         lse fp32 [B * q_len, Hq] (pw_kv_attend).  ws: uint8 scratch of attend_workspace_size bytes."""
-        st = _pw_torch.attend(self.handle, self.n_heads, self.head_dim, q, table, lens, out, ws, q_len,
+        st = _pw_torch.attend(self.handle, self.k, self.n_heads, q, table, lens, out, ws, q_len,
                               self.head_dim ** -0.5 if scale is None else scale, prefix_table, prefix_lens,
                               group_offsets, lse, stream)
         if st:

@@ -1,0 +1,92 @@
+"""What the Python calls around the layer refuse before anything is enqueued: whole calls of another type than the cache's,
+arguments that only make sense together, memory that a kernel cannot use.  Runs without a GPU (host-simulated device, where
+an accepted call answers PW_ERR_UNSUPPORTED)."""
+import pytest
+import torch
+
+import any_precision_expert_gb300 as pw
+from any_precision_expert_gb300._lib import lib
+
+UNSUPPORTED = 2
+F16, BF16 = torch.float16, torch.bfloat16
+HQ, HK, D = 4, 2, 64
+
+
+@pytest.fixture(autouse=True)
+def sim():
+    lib.pw_testing_host_sim(1)
+    yield
+    lib.pw_testing_host_sim(0)
+
+
+def cache(dtype=F16):
+    k = torch.zeros(4, HK, 16, D, dtype=dtype)
+    return pw.KvCache(k, k.clone(), n_heads=HQ)
+
+
+def ints(*shape, device="cpu"):
+    return torch.zeros(*shape, dtype=torch.int32, device=device)
+
+
+def workspace(c):
+    ws = torch.empty(c.attend_workspace_size(3, 1, 1) + 256, dtype=torch.uint8)
+    return ws[-ws.data_ptr() % 256:]
+
+
+def append(c, dtype=F16, device="cpu", **kw):
+    k, q = (torch.zeros(3, h, D, dtype=dtype, device=device) for h in (HK, HQ))
+    a = {**dict(k=k, v=k.clone(), slots=ints(3, device=device), q=q, q_out=torch.empty_like(q)), **kw}
+    c.append(**a)
+
+
+def attend(c, dtype=F16, device="cpu", **kw):
+    q = torch.zeros(3, HQ, D, dtype=dtype, device=device)
+    a = {**dict(q=q, table=ints(3, 2, device=device), lens=ints(3, device=device), out=torch.empty_like(q), ws=workspace(c),
+                prefix_table=ints(1, 2, device=device), prefix_lens=ints(1, device=device)), **kw}
+    c.attend(**a)
+
+
+def accepted(f, *a, **kw):
+    with pytest.raises(pw.PwError) as e:
+        f(*a, **kw)
+    assert e.value.status == UNSUPPORTED
+
+
+@pytest.mark.parametrize("of", [F16, BF16])
+@pytest.mark.parametrize("call", [append, attend])
+def test_calls_hold_the_caches_type(call, of):
+    c = cache(of)
+    accepted(call, c, of)
+    for other in (F16, BF16, torch.float32, torch.uint8, torch.int16, torch.int64, torch.float64):
+        if other != of:
+            with pytest.raises(ValueError):
+                call(c, other)
+
+
+@pytest.mark.parametrize("name,heads", [("k", HK), ("v", HK), ("q", HQ), ("q_out", HQ)])
+def test_append_one_argument_of_another_type(name, heads):
+    with pytest.raises(ValueError):
+        append(cache(), **{name: torch.zeros(3, heads, D, dtype=BF16)})
+
+
+@pytest.mark.parametrize("name", ["q", "out"])
+def test_attend_one_argument_of_another_type(name):
+    with pytest.raises(ValueError):
+        attend(cache(), **{name: torch.zeros(3, HQ, D, dtype=BF16)})
+
+
+def test_append_norm_weights_have_the_caches_type():
+    pos = ints(3)
+    for dtype in (F16, BF16):
+        r = pw.Rotary(torch.zeros(8, D), k_weight=torch.zeros(D, dtype=dtype))
+        if dtype == F16:
+            accepted(append, cache(F16), rotary=r, positions=pos)
+        else:
+            with pytest.raises(ValueError):
+                append(cache(F16), rotary=r, positions=pos)
+
+
+@pytest.mark.parametrize("call", [append, attend])
+def test_calls_hold_the_caches_device(call):
+    with pytest.raises(ValueError):
+        call(cache(), device="meta")
