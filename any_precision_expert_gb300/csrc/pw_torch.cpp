@@ -161,6 +161,9 @@ pw_status attend(PyObject* const* a) {
   d.table_stride = (int)table.size(1);
   d.table = vec<const int32_t>(a[4], at::kInt, cache, "table", B, d.table_stride);
   d.lens = vec<const int32_t>(a[5], at::kInt, cache, "lens", B);
+  // a prefix left out by mistake would still give an answer, without it
+  if ((a[10] == Py_None) != (a[11] == Py_None)) fail("prefix_table, prefix_lens", "both or neither");
+  if (a[11] == Py_None && a[12] != Py_None) fail("group_offsets", "needs prefix_table and prefix_lens");
   if (a[11] != Py_None) {
     const at::Tensor& pt = tensor(a[10], "prefix_table");
     if (pt.dim() != 2) fail("prefix_table", "must be [groups, pages]");

@@ -98,8 +98,8 @@ class KvCache:
                prefix_lens=None, group_offsets=None, lse=None, stream=None):
         """Attention of q [B * q_len, Hq, D] over each sequence's own pages table int32 [B, pages] (lens int32 [B])
         behind its group's shared prefix (prefix_table int32 [groups, pages], prefix_lens int32 [groups],
-        group_offsets int32 [groups + 1]; one group over the whole batch needs no offsets), into out and, when given,
-        lse fp32 [B * q_len, Hq] (pw_kv_attend).  ws: uint8 scratch of attend_workspace_size bytes."""
+        group_offsets int32 [groups + 1]; one group over the whole batch needs no offsets; no prefix: all three None),
+        into out and, when given, lse fp32 [B * q_len, Hq] (pw_kv_attend).  ws: uint8 scratch of attend_workspace_size bytes."""
         st = _pw_torch.attend(self.handle, self.k, self.n_heads, q, table, lens, out, ws, q_len,
                               self.head_dim ** -0.5 if scale is None else scale, prefix_table, prefix_lens,
                               group_offsets, lse, stream)

@@ -90,3 +90,16 @@ def test_append_norm_weights_have_the_caches_type():
 def test_calls_hold_the_caches_device(call):
     with pytest.raises(ValueError):
         call(cache(), device="meta")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(prefix_lens=None), dict(prefix_table=None), dict(prefix_lens=None, group_offsets=ints(2)),
+    dict(prefix_table=None, prefix_lens=None, group_offsets=ints(2))])
+def test_attend_takes_a_prefix_whole_or_not_at_all(kw):
+    with pytest.raises(ValueError):
+        attend(cache(), **kw)
+
+
+def test_attend_with_and_without_a_prefix():
+    accepted(attend, cache(), group_offsets=ints(2))
+    accepted(attend, cache(), prefix_table=None, prefix_lens=None)
