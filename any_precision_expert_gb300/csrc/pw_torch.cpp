@@ -136,6 +136,7 @@ pw_status append(PyObject* const* a) {
   const pw_rotary* r = rotary(a[6], dtype_of(cache, "cache"), D);
   const at::Tensor* q = maybe(a[8], "q");
   pw_rows rq = {}, rqo = {};
+  if (!q && a[9] != Py_None) fail("q_out", "needs q");
   if (q) rq = rows(*q, T, hq, D, cache, "q"), rqo = rows(tensor(a[9], "q_out"), T, hq, D, cache, "q_out");
   return pw_kv_append(kv, r, vec<const int32_t>(a[7], at::kInt, cache, "positions", T),
                       vec<const int32_t>(a[5], at::kInt, cache, "slots", T), (int)T, &rk, &rv, &rq, &rqo,

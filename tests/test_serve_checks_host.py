@@ -103,3 +103,10 @@ def test_attend_takes_a_prefix_whole_or_not_at_all(kw):
 def test_attend_with_and_without_a_prefix():
     accepted(attend, cache(), group_offsets=ints(2))
     accepted(attend, cache(), prefix_table=None, prefix_lens=None)
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(q_out=None)])
+def test_append_takes_queries_and_their_place_together(kw):
+    with pytest.raises(ValueError):
+        append(cache(), **kw)
+    accepted(append, cache(), q=None, q_out=None)
