@@ -175,6 +175,8 @@ pw_status attend(PyObject* const* a) {
     d.group_offsets = vec<const int32_t>(a[12], at::kInt, cache, "group_offsets", d.n_groups + 1);
   }
   const at::Tensor* ws = maybe(a[7], "ws");
+  if (ws && ws->device() != cache.device()) fail("ws", "on another device");
+  if (ws && !ws->is_contiguous()) fail("ws", "must be contiguous");  // else it has fewer bytes than its sizes say
   return pw_kv_attend(kv, &d, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, stream(a[14], cache));
 }
 

@@ -110,3 +110,12 @@ def test_append_takes_queries_and_their_place_together(kw):
     with pytest.raises(ValueError):
         append(cache(), **kw)
     accepted(append, cache(), q=None, q_out=None)
+
+
+def test_attend_workspace_is_memory_of_the_caches_device():
+    c = cache()
+    n = c.attend_workspace_size(3, 1, 1)
+    for ws in (torch.empty(n + 256, dtype=torch.uint8, device="meta"), workspace(c)[:1].expand(1 << 30),
+               torch.empty(2 * n + 512, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            attend(c, ws=ws)
