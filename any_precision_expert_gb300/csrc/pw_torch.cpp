@@ -80,10 +80,12 @@ void* stream(PyObject* o, const at::Tensor& like) {
   return p;
 }
 
-// A Rotary as (address of its pw_rotary, type of its weights or -1, their length).
-const pw_rotary* rotary(PyObject* o, int dtype, int64_t D) {
+// A Rotary as (address of its pw_rotary, type of its weights or -1, their length, one of its tensors or None).
+const pw_rotary* rotary(PyObject* o, int dtype, int64_t D, const at::Tensor& like) {
   if (o == Py_None) return nullptr;
-  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3) fail("rotary", "must be a Rotary's key");
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) fail("rotary", "must be a Rotary's key");
+  const at::Tensor* some = maybe(PyTuple_GET_ITEM(o, 3), "rotary");
+  if (some && some->device() != like.device()) fail("rotary", "on another device");
   const long long type = integer(PyTuple_GET_ITEM(o, 1));
   if (type >= 0 && (type != dtype || integer(PyTuple_GET_ITEM(o, 2)) != D))
     fail("rotary", "norm weights must be [head_dim] of the heads' type");
@@ -114,7 +116,7 @@ pw_status rope(PyObject* const* a) {
   if (!some || some->dim() != 3 || (k && k->dim() != 3)) fail("q", "q or k must be [T, heads, head_dim]");
   const int64_t T = some->size(0), D = some->size(2);
   const pw_heads heads = {dtype_of(*some, "q"), (int)some->size(1), (int)(k ? k : q)->size(1), (int)D};
-  const pw_rotary* r = rotary(a[0], heads.dtype, D);
+  const pw_rotary* r = rotary(a[0], heads.dtype, D, *some);
   pw_rows rq = {}, rk = {}, rqo = {}, rko = {};
   if (q) rq = rows(*q, T, heads.n_heads, D, *some, "q"), rqo = rows(tensor(a[4], "q_out"), T, heads.n_heads, D, *some, "q_out");
   if (k) rk = rows(*k, T, heads.n_kv_heads, D, *some, "k"), rko = rows(tensor(a[5], "k_out"), T, heads.n_kv_heads, D, *some, "k_out");
@@ -133,7 +135,7 @@ pw_status append(PyObject* const* a) {
   const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
   const int64_t T = k.dim() == 3 ? k.size(0) : -1;
   const pw_rows rk = rows(k, T, hk, D, cache, "k"), rv = rows(v, T, hk, D, cache, "v");
-  const pw_rotary* r = rotary(a[6], dtype_of(cache, "cache"), D);
+  const pw_rotary* r = rotary(a[6], dtype_of(cache, "cache"), D, cache);
   const at::Tensor* q = maybe(a[8], "q");
   pw_rows rq = {}, rqo = {};
   if (!q && a[9] != Py_None) fail("q_out", "needs q");

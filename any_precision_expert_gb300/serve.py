@@ -32,10 +32,13 @@ class Rotary:
         for w in weights:
             if w.dim() != 1 or not w.is_contiguous() or w.shape != weights[0].shape or w.dtype != weights[0].dtype:
                 raise ValueError("norm weights must be contiguous [head_dim] tensors of one type")
+        given = [t for t in (cos_sin, q_weight, k_weight) if t is not None]
+        if any(t.device != given[0].device for t in given):
+            raise ValueError("cos_sin and the norm weights must be on one device")
         self._keep = (cos_sin, q_weight, k_weight)
         self.desc = RotaryDesc(_p(cos_sin), max_pos, rot, 1 if interleaved else 0, _p(q_weight), _p(k_weight), eps)
         self._key = (C.addressof(self.desc), _DTYPES.get(weights[0].dtype, len(_DTYPES)) if weights else -1,
-                     weights[0].shape[0] if weights else 0)
+                     weights[0].shape[0] if weights else 0, given[0] if given else None)
 
 
 def qk_norm_rope(rotary: Rotary, q, k, positions, q_out, k_out, err=None, stream=None):

@@ -119,3 +119,18 @@ def test_attend_workspace_is_memory_of_the_caches_device():
                torch.empty(2 * n + 512, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError):
             attend(c, ws=ws)
+
+
+def test_rotary_is_on_the_device_of_the_call():
+    w, pos = torch.zeros(D, dtype=F16), ints(3)
+    for kw in (dict(q_weight=w.to("meta")), dict(k_weight=w.to("meta")), dict(q_weight=w, k_weight=w.to("meta"))):
+        with pytest.raises(ValueError):
+            pw.Rotary(torch.zeros(8, D), **kw)
+    q = torch.zeros(3, HQ, D, dtype=F16)
+    for r in (pw.Rotary(torch.zeros(8, D, device="meta")), pw.Rotary(None, k_weight=w.to("meta"))):
+        with pytest.raises(ValueError):
+            append(cache(), rotary=r, positions=pos)
+        with pytest.raises(ValueError):
+            pw.qk_norm_rope(r, q, None, pos, torch.empty_like(q), None)
+    accepted(pw.qk_norm_rope, pw.Rotary(None, q_weight=w), q, None, None, torch.empty_like(q), None)
+    accepted(pw.qk_norm_rope, pw.Rotary(None), q, None, None, torch.empty_like(q), None)
