@@ -11,6 +11,10 @@
 
 #include "pw.h"
 
+namespace pw {
+bool host_sim();  // libpw.so: no kernel runs
+}
+
 namespace {
 
 struct Bad {};  // a Python error is set
@@ -43,6 +47,11 @@ int dtype_of(const at::Tensor& t, const char* what) {
   if (t.scalar_type() == at::kHalf) return PW_F16;
   if (t.scalar_type() == at::kBFloat16) return PW_BF16;
   fail(what, "heads are float16 or bfloat16");
+}
+
+// The tensor that a call's others are compared with is on a GPU (a host address would reach a kernel as it is).
+void on_gpu(const at::Tensor& t, const char* what) {
+  if (!t.is_cuda() && !pw::host_sim()) fail(what, "must be on a GPU");
 }
 
 // [T][H][D] head rows of the type and on the device of `like`.
@@ -109,11 +118,18 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, Py_ssize_t want) {
   }
 }
 
+// (cache k): whether a cache may be made of it.
+pw_status check_cache(PyObject* const* a) {
+  on_gpu(tensor(a[0], "k"), "k");
+  return PW_OK;
+}
+
 // (rotary, q, k, positions, q_out, k_out, err, stream)
 pw_status rope(PyObject* const* a) {
   const at::Tensor *q = maybe(a[1], "q"), *k = maybe(a[2], "k");
   const at::Tensor* some = q ? q : k;
   if (!some || some->dim() != 3 || (k && k->dim() != 3)) fail("q", "q or k must be [T, heads, head_dim]");
+  on_gpu(*some, q ? "q" : "k");
   const int64_t T = some->size(0), D = some->size(2);
   const pw_heads heads = {dtype_of(*some, "q"), (int)some->size(1), (int)(k ? k : q)->size(1), (int)D};
   const pw_rotary* r = rotary(a[0], heads.dtype, D, *some);
@@ -131,6 +147,7 @@ pw_status rope(PyObject* const* a) {
 pw_status append(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
   const int64_t hq = integer(a[2]), hk = cache.size(1), D = cache.size(3);
   const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
   const int64_t T = k.dim() == 3 ? k.size(0) : -1;
@@ -149,6 +166,7 @@ pw_status append(PyObject* const* a) {
 pw_status attend(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
   const int64_t hq = integer(a[2]), D = cache.size(3);
   const at::Tensor &q = tensor(a[3], "q"), &table = tensor(a[4], "table"), &out = tensor(a[6], "out");
   if (table.dim() != 2) fail("table", "must be [batch, pages]");
@@ -186,6 +204,7 @@ pw_status attend(PyObject* const* a) {
 pw_status verify(PyObject* const* a) {
   const at::Tensor& p = tensor(a[0], "target_p");
   if (p.dim() != 3) fail("target_p", "must be [B, K + 1, V]");
+  on_gpu(p, "target_p");
   const int64_t B = p.size(0), K = p.size(1) - 1, V = p.size(2);
   if (B > INT32_MAX || K > INT32_MAX || V > INT32_MAX) fail("target_p", "too large");
   return pw_verify_draft(vec<const float>(a[0], at::kFloat, p, "target_p", B, K + 1, V),
@@ -197,12 +216,14 @@ pw_status verify(PyObject* const* a) {
                          stream(a[9], p));
 }
 
+PyObject* py_check_cache(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<check_cache>(a, n, 1); }
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<rope>(a, n, 8); }
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<append>(a, n, 11); }
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<attend>(a, n, 15); }
 PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<verify>(a, n, 10); }
 
 PyMethodDef methods[] = {
+    {"check_cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_check_cache)), METH_FASTCALL, nullptr},
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_rope)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_append)), METH_FASTCALL, nullptr},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend)), METH_FASTCALL, nullptr},

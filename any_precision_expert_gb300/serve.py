@@ -60,6 +60,7 @@ class KvCache:
             raise ValueError("k and v must be [pages, kv heads, page tokens, head_dim] tensors of one layout")
         if k.dtype not in _DTYPES:
             raise ValueError(f"heads are float16 or bfloat16, not {k.dtype}")
+        _pw_torch.check_cache(k)
         self.k, self.v = k, v
         n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = k.shape
         self.n_heads, self.dtype = n_heads, k.dtype

@@ -134,3 +134,20 @@ def test_rotary_is_on_the_device_of_the_call():
             pw.qk_norm_rope(r, q, None, pos, torch.empty_like(q), None)
     accepted(pw.qk_norm_rope, pw.Rotary(None, q_weight=w), q, None, None, torch.empty_like(q), None)
     accepted(pw.qk_norm_rope, pw.Rotary(None), q, None, None, torch.empty_like(q), None)
+
+
+def test_tensors_are_on_a_gpu():
+    c, q = cache(), torch.zeros(3, HQ, D, dtype=F16)
+    lib.pw_testing_host_sim(0)      # the refusals below come before any launch
+    with pytest.raises(ValueError):
+        cache()
+    with pytest.raises(ValueError):
+        pw.qk_norm_rope(pw.Rotary(None), q, None, None, torch.empty_like(q), None)
+    with pytest.raises(ValueError):
+        pw.qk_norm_rope(pw.Rotary(None), None, q, None, None, torch.empty_like(q))
+    with pytest.raises(ValueError):
+        append(c)
+    with pytest.raises(ValueError):
+        attend(c)
+    with pytest.raises(ValueError):
+        pw.verify_draft(torch.zeros(1, 1, 8), None, None, None, None, torch.zeros(1, 8), ints(1, 1), ints(1))
