@@ -43,6 +43,12 @@ int small(PyObject* o, const char* what) {
   return (int)v;
 }
 
+// A size that the C ABI takes in 32 bits; larger ones would arrive as others.
+int size32(int64_t n, const char* what) {
+  if (n > INT32_MAX) fail(what, "too large");
+  return (int)n;
+}
+
 int dtype_of(const at::Tensor& t, const char* what) {
   if (t.scalar_type() == at::kHalf) return PW_F16;
   if (t.scalar_type() == at::kBFloat16) return PW_BF16;
@@ -131,12 +137,12 @@ pw_status rope(PyObject* const* a) {
   if (!some || some->dim() != 3 || (k && k->dim() != 3)) fail("q", "q or k must be [T, heads, head_dim]");
   on_gpu(*some, q ? "q" : "k");
   const int64_t T = some->size(0), D = some->size(2);
-  const pw_heads heads = {dtype_of(*some, "q"), (int)some->size(1), (int)(k ? k : q)->size(1), (int)D};
+  const pw_heads heads = {dtype_of(*some, "q"), size32(some->size(1), "q"), size32((k ? k : q)->size(1), "k"), size32(D, "q")};
   const pw_rotary* r = rotary(a[0], heads.dtype, D, *some);
   pw_rows rq = {}, rk = {}, rqo = {}, rko = {};
   if (q) rq = rows(*q, T, heads.n_heads, D, *some, "q"), rqo = rows(tensor(a[4], "q_out"), T, heads.n_heads, D, *some, "q_out");
   if (k) rk = rows(*k, T, heads.n_kv_heads, D, *some, "k"), rko = rows(tensor(a[5], "k_out"), T, heads.n_kv_heads, D, *some, "k_out");
-  return pw_qk_norm_rope(&heads, r, vec<const int32_t>(a[3], at::kInt, *some, "positions", T), (int)T, &rq, &rk, &rqo, &rko,
+  return pw_qk_norm_rope(&heads, r, vec<const int32_t>(a[3], at::kInt, *some, "positions", T), size32(T, "q"), &rq, &rk, &rqo, &rko,
                          vec<int32_t>(a[6], at::kInt, *some, "err", 1), stream(a[7], *some));
 }
 
@@ -158,7 +164,7 @@ pw_status append(PyObject* const* a) {
   if (!q && a[9] != Py_None) fail("q_out", "needs q");
   if (q) rq = rows(*q, T, hq, D, cache, "q"), rqo = rows(tensor(a[9], "q_out"), T, hq, D, cache, "q_out");
   return pw_kv_append(kv, r, vec<const int32_t>(a[7], at::kInt, cache, "positions", T),
-                      vec<const int32_t>(a[5], at::kInt, cache, "slots", T), (int)T, &rk, &rv, &rq, &rqo,
+                      vec<const int32_t>(a[5], at::kInt, cache, "slots", T), size32(T, "k"), &rk, &rv, &rq, &rqo,
                       stream(a[10], cache));
 }
 
@@ -172,14 +178,14 @@ pw_status attend(PyObject* const* a) {
   if (table.dim() != 2) fail("table", "must be [batch, pages]");
   pw_attend_desc d = {};
   const int64_t B = table.size(0);
-  d.batch = (int)B;
+  d.batch = size32(B, "table");
   d.q_len = small(a[8], "q_len");
   d.q = rows(q, B * d.q_len, hq, D, cache, "q");
   d.out = rows(out, B * d.q_len, hq, D, cache, "out");
   d.lse = vec<float>(a[13], at::kFloat, cache, "lse", B * d.q_len, hq);
   d.scale = (float)PyFloat_AsDouble(a[9]);
   if (PyErr_Occurred()) throw Bad();
-  d.table_stride = (int)table.size(1);
+  d.table_stride = size32(table.size(1), "table");
   d.table = vec<const int32_t>(a[4], at::kInt, cache, "table", B, d.table_stride);
   d.lens = vec<const int32_t>(a[5], at::kInt, cache, "lens", B);
   // a prefix left out by mistake would still give an answer, without it
@@ -188,8 +194,8 @@ pw_status attend(PyObject* const* a) {
   if (a[11] != Py_None) {
     const at::Tensor& pt = tensor(a[10], "prefix_table");
     if (pt.dim() != 2) fail("prefix_table", "must be [groups, pages]");
-    d.n_groups = (int)pt.size(0);
-    d.prefix_stride = (int)pt.size(1);
+    d.n_groups = size32(pt.size(0), "prefix_table");
+    d.prefix_stride = size32(pt.size(1), "prefix_table");
     d.prefix_table = vec<const int32_t>(a[10], at::kInt, cache, "prefix_table", d.n_groups, d.prefix_stride);
     d.prefix_lens = vec<const int32_t>(a[11], at::kInt, cache, "prefix_lens", d.n_groups);
     d.group_offsets = vec<const int32_t>(a[12], at::kInt, cache, "group_offsets", d.n_groups + 1);

@@ -151,3 +151,19 @@ def test_tensors_are_on_a_gpu():
         attend(c)
     with pytest.raises(ValueError):
         pw.verify_draft(torch.zeros(1, 1, 8), None, None, None, None, torch.zeros(1, 8), ints(1, 1), ints(1))
+
+
+def test_sizes_past_32_bits_are_refused():
+    c, n, one = cache(), (1 << 32) + 1, torch.zeros(1, HQ, D, dtype=F16)
+    with pytest.raises(ValueError):
+        pw.qk_norm_rope(pw.Rotary(None), one.expand(n, HQ, D), None, None, one.expand(n, HQ, D), None)
+    with pytest.raises(ValueError):
+        pw.qk_norm_rope(pw.Rotary(None), one[:, :1].expand(1, n, D), None, None, one[:, :1].expand(1, n, D), None)
+    empty = torch.zeros(1, 0, dtype=torch.int32)     # tables without pages
+    q = torch.zeros(3, HQ, D, dtype=F16)
+    with pytest.raises(ValueError):
+        attend(c, prefix_table=empty.expand(n, 0), prefix_lens=ints(1))
+    with pytest.raises(ValueError):
+        attend(c, q=q[:1], out=q[:1].clone(), table=torch.empty(n, 0, dtype=torch.int32), lens=ints(1))
+    with pytest.raises(ValueError):
+        attend(c, q=q[:0], out=q[:0], lens=ints(0), table=torch.empty(0, n, dtype=torch.int32))
