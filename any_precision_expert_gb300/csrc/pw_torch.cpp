@@ -87,11 +87,11 @@ T* vec(PyObject* o, at::ScalarType type, const at::Tensor& like, const char* wha
 // The stream argument: None (the tensors' device's current one), a raw handle, or an object with .cuda_stream.
 void* stream(PyObject* o, const at::Tensor& like) {
   if (o == Py_None) return like.is_cuda() ? c10::cuda::getCurrentCUDAStream(like.get_device()).stream() : nullptr;
-  if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-  PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
+  PyObject* a = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
   if (!a) throw Bad();
   void* p = PyLong_AsVoidPtr(a);
   Py_DECREF(a);
+  if (!p && PyErr_Occurred()) throw Bad();  // before the call, which would run on the null stream
   return p;
 }
 
