@@ -129,20 +129,18 @@ __global__ void __launch_bounds__(NT, 2048 / NT) verify_kernel(const VerifyParam
       kept = n;
       for (int i0 = 0; i0 < K; i0 += 32) {  // the drafts side by side; the first refusal ends the kept ones
         const int i = i0 + lane;
-        bool ok = true, bad = false;
+        bool ok = true;
         if (i < K) {  // read whether or not it counts: the count is on its way too
           const int x = P.tokens[(size_t)b * K + i];
-          bad = x < 0 || x >= V;
-          ok = !bad;
+          ok = x >= 0 && x < V;
           if (ok) {
             const float uq = P.u[(size_t)b * K + i] * P.q[((size_t)b * K + i) * V + x];
             ok = uq < P.p[((size_t)b * (K + 1) + i) * V + x];
           }
         }
-        const unsigned no = __ballot_sync(0xffffffffu, !ok && i < n), wrong = __ballot_sync(0xffffffffu, bad);
+        const unsigned no = __ballot_sync(0xffffffffu, !ok && i < n);
         if (no) {
           kept = i0 + __ffs(no) - 1;
-          if (lane == 0 && P.err && (wrong >> (kept - i0) & 1)) atomicExch(P.err, kErrToken);
           break;
         }
       }
@@ -188,8 +186,11 @@ __global__ void __launch_bounds__(NT, 2048 / NT) verify_kernel(const VerifyParam
     q = nullptr;
   }
   if (part != 0) return;
-  for (int i = tid; i <= K; i += NT)
-    P.out[(size_t)b * (K + 1) + i] = i < kept ? P.tokens[(size_t)b * K + i] : i == kept ? next : -1;
+  for (int i = tid; i <= K; i += NT) {
+    const int x = i < K ? P.tokens[(size_t)b * K + i] : 0;
+    P.out[(size_t)b * (K + 1) + i] = i < kept ? x : i == kept ? next : -1;
+    if ((x < 0 || x >= V) && i < s_n && P.err) atomicExch(P.err, kErrToken);  // behind a refusal too
+  }
   if (tid == 0) P.accepted[b] = kept;
 }
 

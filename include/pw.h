@@ -701,7 +701,8 @@ pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* desc, void* ws, size_t 
  *   u         device fp32 [B][K]          noise    device fp32 [B][V]
  *   out       device int32 [B][K+1]       accepted device int32 [B]
  *   err       device int32 or NULL: set when an n_draft is outside [0, K]
- *             (clamped) or a token outside [0, V) (not kept)
+ *             (clamped) or one of a sequence's n tokens outside [0, V) (not
+ *             kept), whether or not an earlier draft was refused
  * B in [0, 65535], K in [0, 64], V in [1, 2^24]; with K = 0 the arrays of drafts may be
  * NULL (plain sampling from target_p).
  */

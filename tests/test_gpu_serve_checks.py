@@ -16,3 +16,42 @@ def test_an_argument_that_is_no_stream_enqueues_nothing(stream, error):
         pw.qk_norm_rope(pw.Rotary(None), q, None, None, out, None, stream=stream)
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+def verify(B, K, V, n_draft, tokens, refused):
+    """Flat distributions; the drafts at places in `refused` are refused by their uniform numbers."""
+    p, q = (torch.full((B, k, V), 1.0 / V, device="cuda") for k in (K + 1, K))
+    u = torch.zeros(B, K, device="cuda")
+    for b, i in refused:
+        u[b, i] = 2.0
+    out, acc = torch.empty(B, K + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pw.verify_draft(p, q, tokens.cuda(), torch.tensor(n_draft, dtype=torch.int32, device="cuda"), u,
+                    torch.ones(B, V, device="cuda"), out, acc, err=err)
+    return out.tolist(), acc.tolist(), err.item()
+
+
+@pytest.mark.parametrize("K,at,bad", [(3, 1, 50), (3, 2, -1), (40, 35, 50), (64, 63, -7), (64, 1, 2 ** 31 - 1)])
+def test_verify_flags_a_bad_token_behind_a_refusal(K, at, bad):
+    tokens = torch.full((2, K), 5, dtype=torch.int32)
+    out, acc, err = verify(2, K, 50, [K, K], tokens, [(0, 0), (1, 0)])
+    assert acc == [0, 0] and err == 0
+    tokens[1, at] = bad
+    again, acc, err = verify(2, K, 50, [K, K], tokens, [(0, 0), (1, 0)])
+    assert again == out and acc == [0, 0] and err != 0
+    # past the sequence's count it is padding
+    again, acc, err = verify(2, K, 50, [K, at], tokens, [(0, 0), (1, 0)])
+    assert again == out and acc == [0, 0] and err == 0
+
+
+@pytest.mark.parametrize("K", [1, 33, 64])
+def test_verify_keeps_up_to_the_first_refusal_in_any_block_of_drafts(K):
+    tokens = torch.arange(K, dtype=torch.int32)[None].expand(3, K).contiguous()
+    last = K - 1
+    out, acc, err = verify(3, K, 100, [K, K, last], tokens, [(0, last)])
+    assert acc == [last, K, last] and err == 0
+    want = tokens[0].tolist()
+    assert [r[:a] for r, a in zip(out, acc)] == [want[:a] for a in acc]
+    assert all(r[a + 1:] == [-1] * (K - a) for r, a in zip(out, acc))
+    # two refusals: the first one ends them
+    assert verify(1, K, 100, [K], tokens[:1], [(0, last), (0, last // 2)])[1] == [last // 2]
