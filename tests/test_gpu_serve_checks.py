@@ -55,3 +55,23 @@ def test_verify_keeps_up_to_the_first_refusal_in_any_block_of_drafts(K):
     assert all(r[a + 1:] == [-1] * (K - a) for r, a in zip(out, acc))
     # two refusals: the first one ends them
     assert verify(1, K, 100, [K], tokens[:1], [(0, last), (0, last // 2)])[1] == [last // 2]
+
+
+def test_verify_ties_an_empty_distribution_and_infinite_quotients_each_by_itself():
+    V, K = 5000, 2
+    p, q = torch.full((3, K + 1, V), 1.0 / V, device="cuda"), torch.full((3, K, V), 1.0 / V, device="cuda")
+    u, e = torch.full((3, K), 2.0, device="cuda"), torch.ones(3, V, device="cuda")
+    p[0] = 0
+    for i in (4999, 1234, 77):
+        p[0, :, i] = 0.25               # equal quotients: the lowest index
+    q[0] = 0.5                          # more than the target anywhere: no residual, so from the target itself
+    p[1] = 0                            # nothing at all: index 0
+    e[2, 3:6] = 0.0                     # infinite quotients: the first of them
+    tokens = torch.full((3, K), 9, dtype=torch.int32, device="cuda")
+    n = torch.tensor([K, K, 0], dtype=torch.int32, device="cuda")
+    out, acc = torch.empty(3, K + 1, dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+    pw.verify_draft(p, q, tokens, n, u, e, out, acc)
+    assert acc.tolist() == [0, 0, 0]
+    assert out[0].tolist() == [77, -1, -1]
+    assert out[1].tolist() == [0, -1, -1]
+    assert out[2].tolist() == [3, -1, -1]
