@@ -26,6 +26,8 @@ import any_precision_expert_gb300 as pw  # noqa: E402
 from synth import bits_plan, get_config, make_expert, make_router  # noqa: E402
 
 HQ, HKV, D, PAGE, VOCAB, MAX_POS = 8, 2, 64, 16, 1000, 512
+BATCH, DRAFTS, PROMPT = 4, 3, 100
+MOST_STEPS = (MAX_POS - PROMPT) // (DRAFTS + 1)  # that the rotation table and the pages hold, every draft kept
 
 
 class Block:
@@ -132,10 +134,12 @@ class Block:
 
 
 def main(steps: int = 8):
-    block = Block(batch=4, drafts=3)
+    if not 0 <= steps <= MOST_STEPS:
+        raise SystemExit(f"0 to {MOST_STEPS} steps: {MAX_POS} positions hold the prompt's {PROMPT} and {DRAFTS + 1} a step")
+    block = Block(batch=BATCH, drafts=DRAFTS)
     try:
-        block.prompt(torch.randint(0, VOCAB, (100,), generator=block.gen, device="cuda"))
-        last = torch.randint(0, VOCAB, (4,), generator=block.gen, device="cuda")
+        block.prompt(torch.randint(0, VOCAB, (PROMPT,), generator=block.gen, device="cuda"))
+        last = torch.randint(0, VOCAB, (BATCH,), generator=block.gen, device="cuda")
         for i in range(steps):
             r = block.step(last)
             last = r["next"]
