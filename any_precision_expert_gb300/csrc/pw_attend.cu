@@ -73,6 +73,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
+// The same, and whether it holds in all of them.
+__device__ __forceinline__ bool compute_all(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)mine), "n"(kComputeWarps * 32)
+      : "memory");
+  return all != 0;
+}
 
 // Which keys of a tile each of a thread's two fragment words may hold: words
 // whose key is at or past `n` (relative to the fragment's first key) become 0.
@@ -201,6 +211,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   bool have = ring.take(pc);
   if (have) load_q();
+  // Warps that share keys meet at barriers in every piece.  Where the wait for a piece gives up it may do so in some of
+  // them only, so they go on together or not at all.
+  if constexpr (KS > 1) have = compute_all(have);
   while (have) {
     const Piece cur = pc;
     const int ra = cur.row0 + mt * 16 + g;
@@ -355,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 #pragma unroll
     for (int step = KS / 2; step > 0; step >>= 1) {
-      compute_sync();  // the buffer is free
+      if (step == KS / 2)
+        have = compute_all(have);
+      else
+        compute_sync();
+      // the buffer is free
       if (ks >= step && ks < 2 * step) {
         const int slot = ((ks - step) * HB + hb) * MT + mt;
 #pragma unroll
