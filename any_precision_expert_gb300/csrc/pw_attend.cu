@@ -179,12 +179,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (++stage == C::STAGES) stage = 0, phase ^= 1;
       }
     }
-    if (!ok)  // a wait gave up: let the copies in flight land before the shared memory goes away
-      for (int i = 0; i < C::STAGES; ++i)
-        for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
-        }
     let_next_start();  // the join may take its place beside the last pieces
     if (!W.behind) behind_the_stream();
+    // Copies in flight land before the shared memory goes away: the compute warps have waited for all of them, unless a
+    // wait has given up, in any warp and at any time.
+    for (int i = 0; i < C::STAGES; ++i)
+      for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
+      }
     return;
   }
 
