@@ -15,7 +15,7 @@
 // them the legacy tensor path keeps up with HBM, so the loads bound it.  Items
 // with more rows go to the tcgen05 kernel (pw_attend_tc.cu).  Measured: 64
 // sequences with suffixes of 2048 tokens on average, 8 key heads of 128, 537
-// MB in 86 us (6.2 TB/s); a call of one piece a CTA takes about 4 us from its
+// MB in 88 us (6.1 TB/s); a call of one piece a CTA takes about 4 us from its
 // first instruction (lengths, page, keys and products one after another).
 #include <math_constants.h>
 
@@ -440,14 +440,14 @@ struct JoinShape {
   int split;  // warps that share four rows
 };
 
-// Warps that share four rows' pieces, by the number of rows (query tokens x heads): a lone sequence on a long prefix has
-// a piece from every CTA (measured: 20 rows of 300 pieces, the call 41 us with 4 warps, 31 with 16), many rows fill the
-// GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).
+// Warps that share four rows' pieces, by the number of rows (query tokens x heads), 16 up to four rows an SM: a lone
+// sequence on a long prefix has a piece from every CTA (measured: 20 rows of 300 pieces, the call 41 us with 4 warps, 31
+// with 16), many rows fill the GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).
 constexpr int kJoinWarps = 4;         // a CTA's, but for
 constexpr int kJoinMost = 16;
 constexpr int kJoinFlight = 4;        // pieces of a row that a warp has in flight
 inline int join_split(long long rows, long long keys) {
-  return rows <= 608 && keys > 64 * 32 ? kJoinMost : rows <= 4096 ? kJoinWarps : 1;
+  return rows <= 4 * sm_count() && keys > 64 * 32 ? kJoinMost : rows <= 4096 ? kJoinWarps : 1;
 }
 
 // With fewer segments than this every one is split among many CTAs: stages of one head then, whose four warps join their
@@ -619,6 +619,10 @@ int stream_ctas() { return 2 * sm_count(); }
 // 1289 16.8 -> 11.7; 100 of 55 rows behind 320 48.8 -> 53.1 at 2.2e6, 70 of 25 behind 1116 24.9 -> 32.4 at 7.8e6).  Where
 // long suffixes keep that kernel waiting for HBM it takes eight times as much along (64 sequences of 4 rows, suffixes to
 // 1000: 35.5 -> 29.2 us at 2.1e6, to 4095: 95.2 -> 89.4 at 4.2e6; 32 of 4, to 4000: 62 -> 56 at 8.2e6).
+// The host knows the tables' widths, not the lengths: with tables much wider than their sequences the rule sees more work
+// than there is, and such a call costs up to what its other side measured (the first two calls above 12.1 -> 16.6 and 12.3 ->
+// 16.3 us with a table for 32768 prefix tokens; 64 sequences of 4 rows behind 2048 tokens, suffixes to 100, with a table for
+// 32768 suffix tokens 23.3 -> 26.5).
 constexpr double kLittlePrefix = 2e6, kLongSuffix = 262144;  // the latter in keys x key heads of the whole batch
 
 // Which kernel takes which items.  Up to 64 rows a key head the streaming
