@@ -20,7 +20,7 @@
 // take 2048, so 70% of their rate once it runs; what is left is the chain
 // scores -> softmax (1.2-1.4 k cycles) -> weights -> products of one row tile,
 // as P and S share their columns.  256 sequences of 4 rows a head on 32768
-// keys: 104 us, 1320 TFLOP/s, of which 6 us pass before a CTA's first scores
+// keys: 98-104 us, 1320-1400 TFLOP/s, of which 6 us pass before a CTA's first scores
 // and 3 after its last.  Tried: one MMA warp for both row tiles 3600 cycles,
 // half a row a softmax thread 3070-3250, weights in 4 parts 3190, in one part
 // 3010, the warpgroups not in turns 3450-4030, the first half's weights taken
@@ -45,7 +45,8 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kParts = 2;            // a tile's weights are handed over in halves: P V starts on the first
 constexpr int kSegmentCost = 2;      // a segment's fixed cost, in key tiles
 // Tiles a CTA takes at least: fewer CTAs leave SMs to the streaming kernel and write fewer partial sums, more share the
-// work (64 sequences on a 2048-token prefix, sent here: 96 / 94 / 97 / 101 us the call with 2 / 3 / 6 / 10).
+// work (the call with 2 / 3 / 6 / 10: 24 sequences of 20 rows behind 8191 tokens 52.2 / 52.1 / 52.1 / 59.7 us, four groups
+// of 132 rows behind up to 6000 25.7 / 25.7 / 28.0 / 33.0).
 constexpr int kLeastUnits = 3;
 constexpr float kGrow = 8.f;
 

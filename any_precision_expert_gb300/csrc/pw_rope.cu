@@ -15,7 +15,7 @@
 // are in flight together and its cosines, sines and weights are loaded once.
 // Measured: 16384 tokens of 40 heads of 128 in 55 us, 6.3 TB/s (one row a warp
 // in flight 100 us, eight 76; with partners exchanged by shuffles 169); one
-// token 2.2 us, the launch.
+// token 2.3 us, the launch.
 #include "pw_heads.cuh"
 #include "pw_serve.h"
 

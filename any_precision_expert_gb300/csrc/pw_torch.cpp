@@ -3,8 +3,8 @@
 //
 // These calls run for a few microseconds in a decode step; reading every
 // tensor's shape, strides and address from Python and converting each argument
-// took 8 to 11 us of host time a call, this takes about one.  Shape and type
-// errors become ValueError; the pw_status is returned.
+// took 8 to 11 us of host time a call, this takes 0.2 to 0.5 beside the launch.
+// Shape, type and device errors become ValueError; the pw_status is returned.
 #include <Python.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>

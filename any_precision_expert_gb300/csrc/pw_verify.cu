@@ -7,8 +7,8 @@
 // small one.  A cluster of CTAs shares a sequence's vocabulary and joins its
 // maxima through shared memory: one launch, no workspace, and the largest
 // (quotient, lowest index) does not depend on any order.  Measured: 256
-// sequences over 131072 tokens, half of them refused a draft, 336 MB in 52 us
-// (6.4 TB/s; 108 us when every index was divided); 4 over 32000 4.7 us.
+// sequences over 131072 tokens, half of them refused a draft, 336 MB in 54.5
+// us (6.2 TB/s; 108 us when every index was divided); 4 over 32000 4.9 us.
 #include <cooperative_groups.h>
 
 #include <utility>

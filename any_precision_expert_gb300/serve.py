@@ -4,8 +4,8 @@ the paged KV cache and its attention, draft verification (include/pw.h).
 Only argument marshalling and shape checks happen here and in the compiled
 module ``_pw_torch`` (csrc/pw_torch.cpp); every step runs in libpw.so's kernels
 on the given (or the tensors' device's current) stream, and no call
-synchronises.  A wrong shape or type raises ValueError, what the library
-refuses raises PwError.
+synchronises.  A wrong shape, type or device raises ValueError, what the
+library refuses raises PwError.
 """
 from __future__ import annotations
 
