@@ -620,7 +620,7 @@ int stream_ctas() { return 2 * sm_count(); }
 // long suffixes keep that kernel waiting for HBM it takes eight times as much along (64 sequences of 4 rows, suffixes to
 // 1000: 35.5 -> 29.2 us at 2.1e6, to 4095: 95.2 -> 89.4 at 4.2e6; 32 of 4, to 4000: 62 -> 56 at 8.2e6).
 // The host knows the tables' widths, not the lengths: with tables much wider than their sequences the rule sees more work
-// than there is, and such a call costs up to what its other side measured (the first two calls above 12.1 -> 16.6 and 12.3 ->
+// than there is, and such a call costs up to what its other side measured (calls like the first two 12.1 -> 16.6 and 12.3 ->
 // 16.3 us with a table for 32768 prefix tokens; 64 sequences of 4 rows behind 2048 tokens, suffixes to 100, with a table for
 // 32768 suffix tokens 23.3 -> 26.5).
 constexpr double kLittlePrefix = 2e6, kLongSuffix = 262144;  // the latter in keys x key heads of the whole batch
