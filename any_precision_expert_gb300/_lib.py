@@ -59,6 +59,31 @@ class AttendDesc(C.Structure):
                 ("prefix_table", vp), ("prefix_stride", i32), ("prefix_lens", vp)]
 
 
+class Kv4Desc(C.Structure):
+    _fields_ = [("heads", Heads), ("page_tokens", i32), ("n_pages", i32)]
+
+
+class PromptDesc(C.Structure):
+    _fields_ = [("q", Rows), ("k", Rows), ("v", Rows), ("out", Rows), ("lse", vp), ("tokens", i32), ("offsets", vp),
+                ("batch", i32), ("scale", C.c_float), ("err", vp)]
+
+
+class LogprobDesc(C.Structure):
+    _fields_ = [("logits", vp), ("dtype", i32), ("row_stride", C.c_longlong), ("T", i32), ("V", i32), ("tokens", vp),
+                ("logprobs", vp), ("entropy", vp), ("n_top", i32), ("top_ids", vp), ("top_logprobs", vp), ("err", vp)]
+
+
+class WeighDesc(C.Structure):
+    _fields_ = [("q", Rows), ("lse", vp), ("batch", i32), ("q_len", i32), ("scale", C.c_float), ("decay", C.c_float),
+                ("table", vp), ("table_stride", i32), ("lens", vp), ("mass", vp), ("out", vp), ("mass_stride", i32)]
+
+
+class EvictDesc(C.Structure):
+    _fields_ = [("batch", i32), ("budget", i32), ("recent", i32), ("table", vp), ("table_stride", i32), ("lens", vp),
+                ("mass", vp), ("mass_stride", i32), ("new_table", vp), ("new_stride", i32), ("new_lens", vp),
+                ("new_mass", vp), ("kept", vp)]
+
+
 U8P3 = C.c_void_p * 3          # const uint8_t* const [3]
 U16P3 = C.c_void_p * 3         # const uint16_t* const [3]
 LUTP = (C.c_void_p * 4) * 3    # const uint16_t* const [3][4]
@@ -110,6 +135,18 @@ _SIGS = {
     "pw_kv_attend_workspace_size": (i32, [vp, i32, i32, i32, C.POINTER(sz)]),
     "pw_kv_attend": (i32, [vp, vp, vp, sz, vp]),
     "pw_verify_draft": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
+    "pw_prompt_attend": (i32, [vp, vp, vp]),
+    "pw_token_logprobs": (i32, [vp, vp]),
+    "pw_kv4_create": (i32, [vp, vp, vp, vp, vp, vp, C.POINTER(vp)]),
+    "pw_kv4_destroy": (i32, [vp]),
+    "pw_kv4_check_device": (i32, [vp, vp]),
+    "pw_kv4_append": (i32, [vp, vp, i32, vp, vp, vp]),
+    "pw_kv4_load": (i32, [vp, vp, i32, vp, vp, vp]),
+    "pw_kv4_attend_workspace_size": (i32, [vp, i32, i32, C.POINTER(sz)]),
+    "pw_kv4_attend": (i32, [vp, vp, vp, sz, vp]),
+    "pw_kv_weigh": (i32, [vp, vp, vp]),
+    "pw_kv_evict_workspace_size": (i32, [vp, i32, i32, C.POINTER(sz)]),
+    "pw_kv_evict": (i32, [vp, vp, vp, sz, vp]),
     "pw_testing_host_sim": (i32, [i32]),
     "pw_testing_complete_events": (i32, []),
     "pw_testing_wait_limit": (i32, [vp, C.c_longlong, i32]),

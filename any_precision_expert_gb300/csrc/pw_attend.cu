@@ -58,20 +58,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-template <typename E>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (sizeof(E) == 2 && __is_same(E, __half))
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
 // The same, and whether it holds in all of them.
 __device__ __forceinline__ bool compute_all(bool mine) {
@@ -435,11 +421,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // How the prefix and the suffix kernel cut rows: rows and heads of a segment, CTAs, and whether it is the tcgen05 one.
-struct JoinShape {
-  int rows[2], heads[2], ctas[2], tc[2];
-  int split;  // warps that share four rows
-};
-
 // Warps that share four rows' pieces, by the number of rows (query tokens x heads), 16 up to four rows an SM: a lone
 // sequence on a long prefix has a piece from every CTA (measured: 20 rows of 300 pieces, the call 41 us with 4 warps, 31
 // with 16), many rows fill the GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).
@@ -728,15 +709,23 @@ cudaError_t launch_typed(const AttendParams& P, const KvMapSet& maps, void* ws, 
     shape.tc[i] = tc;
     shape.ctas[i] = tc ? attend_tc_ctas() : stream_ctas();
   }
+  return launch_join(P, W, shape, s);
+}
+
+}  // namespace
+
+cudaError_t launch_join(const AttendParams& P, const AttendWork& W, JoinShape shape, cudaStream_t s) {
   const int join_rows = P.B * P.ql * P.G;
   shape.split = join_split((long long)join_rows * P.kv.hkv,
                            (long long)(P.table_stride + (P.n_groups ? P.prefix_stride : 0)) << P.kv.page_shift);
   const int warps = shape.split > kJoinWarps ? shape.split : kJoinWarps, cta_rows = 4 * warps / shape.split;
   const Launch at(dim3((join_rows + cta_rows - 1) / cta_rows, P.kv.hkv), warps * 32, 0, s);
-  return cudaLaunchKernelEx(&at.cfg, join_kernel<E, D>, P, W, shape);
+  if (P.kv.dtype == PW_F16)
+    return P.kv.d == 128 ? cudaLaunchKernelEx(&at.cfg, join_kernel<__half, 128>, P, W, shape)
+                         : cudaLaunchKernelEx(&at.cfg, join_kernel<__half, 64>, P, W, shape);
+  return P.kv.d == 128 ? cudaLaunchKernelEx(&at.cfg, join_kernel<__nv_bfloat16, 128>, P, W, shape)
+                       : cudaLaunchKernelEx(&at.cfg, join_kernel<__nv_bfloat16, 64>, P, W, shape);
 }
-
-}  // namespace
 
 cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps) {
   using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -15,6 +15,7 @@
 
 #include <cuda.h>
 
+#include "pw_mma.cuh"
 #include "pw_serve.h"
 #include "pw_tc.cuh"
 
@@ -274,12 +275,6 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A query's weight for a key that it does not see is 0, but 0 times an infinity or NaN is NaN.  Values at keys that only
 // some rows of a sequence see (the last q_len - 1) are therefore looked at, and those that are no numbers kept from the
 // other rows.
@@ -298,6 +293,14 @@ template <typename E>
 __device__ __forceinline__ bool all_finite(const uint4& v) {
   return (finite_bits<E>(v.x) & finite_bits<E>(v.y) & finite_bits<E>(v.z) & finite_bits<E>(v.w)) == 0xffffffffu;
 }
+
+// Where the join finds the pieces of prefixes [0] and suffixes [1]: rows and key heads of the slots, CTAs that wrote them,
+// whether the tcgen05 kernel did.
+struct JoinShape {
+  int rows[2], heads[2], ctas[2], tc[2];
+  int split;  // warps that share four rows; the launch sets it
+};
+cudaError_t launch_join(const AttendParams& P, const AttendWork& W, JoinShape shape, cudaStream_t s);
 
 // The tensor-core kernel for prefix groups with many rows (pw_attend_tc.cu).
 constexpr int kTcRows = 256;

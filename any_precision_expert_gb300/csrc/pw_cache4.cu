@@ -1,0 +1,678 @@
+// The paged cache held in 4 bits: append, load and attention.
+//
+// A head row is cut into groups of 32 values.  A group keeps its least value
+// and a step of the heads' type and 32 codes c in 0..15; a value stands for
+// least + c step.  The order of a row's codes is that of the products:
+// * keys: word (t, i), i < D / 32, t < 4, at t D / 32 + i holds values
+//   32 i + 8 t .. + 7, value order 0 2 4 6 / 1 3 5 7 ... see key_nibble: what
+//   lane t of a group of four multiplies, so that a lane's share of a row is
+//   one aligned piece and a mask turns it into operands;
+// * values: plain, lowest first; lane g of eight takes D / 8 of them.
+#include <math_constants.h>
+
+#include "pw_attend.cuh"
+#include "pw_heads.cuh"
+#include "pw_mma.cuh"
+#include "pw_tc.cuh"
+
+namespace pw {
+
+namespace {
+
+// Nibble of a key word that holds value k of its eight: values (0, 1) and (2, 3) are the operand pairs of an even product
+// step, (4, 5) and (6, 7) of the odd one; a pair lies 16 bits apart.
+__device__ __forceinline__ constexpr int key_nibble(int k) { return (k & 1) * 4 + (k & 2) + (k >> 2); }
+
+template <typename E>
+__device__ __forceinline__ float to_f32(uint16_t bits) {
+  E e;
+  memcpy(&e, &bits, 2);
+  return (float)e;
+}
+template <typename E>
+__device__ __forceinline__ uint16_t from_f32(float x) {
+  E e;
+  if constexpr (__is_same(E, __half)) e = __float2half_rn(x);
+  else e = __float2bfloat16_rn(x);
+  uint16_t bits;
+  memcpy(&bits, &e, 2);
+  return bits;
+}
+
+// ---- append and load ------------------------------------------------------------
+//
+// Eight values a lane: a row is D / 8 lanes, a group four of them, a lane's
+// codes one word.  Bound by HBM for long prompts, by one chain of loads else.
+
+constexpr int kRowThreads = 128;
+
+struct Row4 {
+  uint32_t* codes;   // this lane's word
+  uint32_t* step;    // its group's least value and step
+};
+
+template <int D>
+__device__ __forceinline__ Row4 row4(const Kv4View& kv, int value, long long row, int l) {
+  uint32_t* codes = reinterpret_cast<uint32_t*>(value ? kv.v : kv.k) + row * (D / 8);
+  uint32_t* steps = reinterpret_cast<uint32_t*>(value ? kv.vs : kv.ks) + row * (D / 32);
+  return {codes + (value ? l : (l & 3) * (D / 32) + (l >> 2)), steps + (l >> 2)};
+}
+
+// The row of a slot and head; negative where nothing is written or read.
+__device__ __forceinline__ long long row_of(const Kv4View& kv, int slot, int head, bool flag) {
+  if (slot < 0) return -1;
+  const int page = slot >> kv.page_shift;
+  if (page >= kv.n_pages) {
+    if (flag) atomicExch(kv.err, kErrSlot);
+    return -1;
+  }
+  return (((long long)page * kv.hkv + head) << kv.page_shift) + (slot & ((1 << kv.page_shift) - 1));
+}
+
+template <typename E, int D, bool LOAD>
+__global__ void __launch_bounds__(kRowThreads) row4_kernel(const Row4Params P) {
+  behind_the_stream();
+  let_next_start();
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, l = lane % LPR;
+  const unsigned per = 2 * P.kv.hkv;  // rows a token: keys, then values
+  const unsigned unit = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;
+  const unsigned t = unit / per;
+  const bool live = t < (unsigned)P.T;
+  int h = unit - t * per;
+  const int value = h >= P.kv.hkv;
+  h -= value ? P.kv.hkv : 0;
+  const pw_rows& rows = value ? P.v : P.k;
+  E* at = static_cast<E*>(rows.ptr) + (live ? t * rows.token_stride + h * rows.head_stride : 0) + 8 * l;
+  const long long row = live ? row_of(P.kv, P.slots[t], h, l == 0) : -1;
+  if constexpr (LOAD) {
+    if (row < 0) return;
+    const Row4 to = row4<D>(P.kv, value, row, l);
+    const uint32_t w = *to.codes, st = *to.step;
+    const float least = to_f32<E>(st & 0xffff), step = to_f32<E>(st >> 16);
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = fmaf((float)(w >> 4 * (value ? k : key_nibble(k)) & 15), step, least);
+    *reinterpret_cast<uint4*>(at) = pack8<E>(x);
+  } else {
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (row >= 0) raw = __ldcs(reinterpret_cast<const uint4*>(at));
+    float x[8];
+    unpack8<E>(raw, x);
+    float lo = x[0], hi = x[0];
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) lo = fminf(lo, x[k]), hi = fmaxf(hi, x[k]), bad |= !isfinite(x[k]);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    if (row < 0) return;
+    uint16_t step_bits = from_f32<E>((hi - lo) / 15.f), least_bits = from_f32<E>(lo);  // the least is a value of the type
+    const float step = to_f32<E>(step_bits);
+    uint32_t w = 0;
+    if (bad || !isfinite(step)) {
+      step_bits = least_bits = 0x7fff;  // the group holds what is no number
+    } else if (step > 0.f) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = min(max(__float2int_rn((x[k] - lo) / step), 0), 15);
+        w |= (uint32_t)c << 4 * (value ? k : key_nibble(k));
+      }
+    }
+    const Row4 to = row4<D>(P.kv, value, row, l);
+    *to.codes = w;
+    if ((l & 3) == 0) *to.step = least_bits | (uint32_t)step_bits << 16;
+  }
+}
+
+template <typename E, int D>
+cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
+  constexpr int kRows = kRowThreads / 32 * (32 / (D / 8));
+  const long long blocks = ((long long)P.T * 2 * P.kv.hkv + kRows - 1) / kRows;
+  if (blocks > 0x7fffffffll || blocks * kRows > 0xffffffffll) return cudaErrorInvalidConfiguration;
+  const Launch at(dim3((unsigned)blocks), kRowThreads, 0, s);
+  return load ? cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, true>, P) : cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, false>, P);
+}
+
+// ---- attention ------------------------------------------------------------------
+//
+// The streaming kernel of pw_attend.cu on codes.  Scores take the keys exactly:
+//   q . k = sum over groups g of  step_g (q_g . c_g) + least_g sum(q_g),
+// the first from products of fp16 queries with codes as fp16 numbers (c 2^-24:
+// the bits of a code are a subnormal number; a code 4 bits up is 16 of it,
+// which the queries of odd steps make up for), the second from one more product
+// with sum(q_g) cut into three numbers of the heads' type.  For the range of
+// the codes' products the queries are brought to a largest value of 2^8 .. 2^9
+// a row by a power of two: that is exact but for values of less than 2^-18 of
+// the row's largest, which are off by at most 2^-29 of it.  Values are turned
+// into the heads' type, one rounding each.
+
+constexpr int kComputeWarps = 4;
+constexpr int kThreads = (kComputeWarps + 1) * 32;
+constexpr int kTile = 128;                                // keys a stage
+
+template <int D>
+struct Cfg {
+  // eight keys' steps take 128 bytes, where a copy lands, or 64 side by side (heads of 64 on pages of 16 tokens and more)
+  static constexpr int CODES = kTile * (D / 2), STEPS = kTile * 16;
+  static constexpr int K_AT = 0, V_AT = CODES, KS_AT = 2 * CODES, VS_AT = KS_AT + STEPS;
+  static constexpr int STAGE = 2 * (CODES + STEPS);
+  static constexpr int STAGES = 81920 / STAGE;
+  static constexpr int JOIN = 2 * (D / 8) * 512;          // accumulators of two warps
+  static constexpr int JOIN_AT = STAGES * STAGE;
+  static constexpr int ML_AT = JOIN_AT + JOIN;
+  static constexpr int PIECE_AT = ML_AT + 2 * 128;
+  static constexpr int BAR_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
+  static constexpr int SMEM = BAR_AT + 16 * STAGES + 16 * kPieces + 16;
+};
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
+__device__ __forceinline__ bool compute_all(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)mine), "n"(kComputeWarps * 32)
+      : "memory");
+  return all != 0;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+// Bytes of eight keys' steps in a stage.
+template <int D>
+__device__ __forceinline__ int step_group(int page_shift) {
+  return D == 128 || page_shift == 3 ? 128 : 64;
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 4) {
+    const uint4 v = shared16(at);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(at);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = lds32(at);
+  }
+}
+
+// The code pair at bits 4 n and 4 n + 16 of w as numbers, times step, plus least, rounded once.
+template <typename E>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int n, uint32_t step2, uint32_t least2) {
+  if constexpr (__is_same(E, __half)) {
+    const uint32_t bits = ((n & 2 ? w >> 8 : w) & (n & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;  // 1024 + c (or 16 c)
+    __half2 c = *reinterpret_cast<const __half2*>(&bits);
+    c = n & 1 ? __hfma2(c, __float2half2_rn(0.0625f), __float2half2_rn(-64.f)) : __hadd2(c, __float2half2_rn(-1024.f));
+    const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&step2), *reinterpret_cast<const __half2*>(&least2));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const uint32_t bits = ((w >> 4 * n) & 0x000f000fu) | 0x43004300u;  // 128 + c
+    __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&bits);
+    c = __hadd2(c, __float2bfloat162_rn(-128.f));
+    const __nv_bfloat162 r =
+        __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&step2), *reinterpret_cast<const __nv_bfloat162*>(&least2));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// MT row tiles of 16; KS warps share the keys of a row tile.
+template <typename E, int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    attend4_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ Kv4Maps maps) {
+  using C = Cfg<D>;
+  constexpr int ROWS = 16 * MT, KS = kComputeWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64;
+  using Walk = AttendWalk<ROWS, kTile, 1, 1, 1>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES + 16 * kPieces);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (base & 1023) {
+    if (tid == 0) atomicExch(P.kv.err, kErrLayout);
+    return;
+  }
+  behind_the_stream();
+  const typename Walk::Mine mine = Walk::mine(P, W);
+  PieceRing ring;
+  ring.full = empty + 8 * C::STAGES;
+  ring.empty = ring.full + 8 * kPieces;
+  ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
+  ring.abort_flag = abort_flag;
+  ring.err = P.kv.err;
+  if (tid < 2 * (C::STAGES + kPieces)) {
+    const bool one = tid < C::STAGES || (tid >= 2 * C::STAGES && tid < 2 * C::STAGES + kPieces);
+    mbar_init(full + 8 * tid, one ? 1 : kComputeWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 0) *abort_flag = 0;
+  Walk walk;
+  walk.start(P, W, mine, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
+  Piece pc;
+  int stage = 0, phase = 0;
+
+  if (warp == kComputeWarps) {
+    // ---- producer: one lane a box ----
+    const int shift = P.kv.page_shift, box = min(1 << shift, kBoxTokens), group = step_group<D>(shift);
+    const int* table;
+    bool ok = true;
+    uint64_t once;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    while (ok) {
+      const bool more = walk.next(P, pc, table);
+      ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
+      if (!more) break;
+      for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
+        const int kt = key_tile<kTile>(pc, t), keys = min(kTile, pc.len - kt * kTile), boxes = (keys + box - 1) / box;
+        const int at = kt * kTile + lane * box;
+        int page = 0;
+        if (lane < boxes) {
+          page = table[at >> shift];
+          if (page < 0 || page >= P.kv.n_pages) atomicExch(P.kv.err, kErrPage);  // reads as zeros
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, abort_flag, P.kv.err));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(boxes * box * (D + D / 4)));
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t to = base + stage * C::STAGE;
+          const int tok = at & ((1 << shift) - 1), off = lane * box;
+          tma_load_page(to + C::K_AT + off * (D / 2), &maps.k, 0, tok, pc.head, page, full + 8 * stage, once);
+          tma_load_page(to + C::V_AT + off * (D / 2), &maps.v, 0, tok, pc.head, page, full + 8 * stage, once);
+          tma_load_3d(to + C::KS_AT + off / 8 * group, &maps.ks, tok * (D / 32), pc.head, page, full + 8 * stage, once);
+          tma_load_3d(to + C::VS_AT + off / 8 * group, &maps.vs, tok * (D / 32), pc.head, page, full + 8 * stage, once);
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+    }
+    let_next_start();
+    // copies in flight land before the shared memory goes away (after a normal end all have)
+    for (int i = 0; i < C::STAGES; ++i)
+      for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
+      }
+    return;
+  }
+
+  // ---- compute warps ----
+  const int g = lane >> 2, t4 = lane & 3;
+  const int group = step_group<D>(P.kv.page_shift);
+  const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
+  const int turned = (g >> 1) + (g & 1) * 4;  // the key of eight that is column g of a score tile: columns 2 t, 2 t + 1 are keys t, t + 4
+  uint32_t qf[2 * NG][4], qs[4];
+  float rs[2];  // a row's score in log2 units is rs times its product
+  auto load_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = pc.row0 + mt * 16 + g + 8 * i;
+      const bool in = r < pc.nrows;
+      const int tok = in ? r / P.G : 0, hd = in ? pc.head * P.G + r - tok * P.G : 0;
+      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride + 8 * t4;
+      float x[NG][8], most = 0.f;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        unpack8<E>(in ? *reinterpret_cast<const uint4*>(src + 32 * n) : make_uint4(0, 0, 0, 0), x[n]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[n][k]));
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // a power of two that brings the largest to 2^8 .. 2^9, in two factors that are numbers
+      const int e = most > 0.f && most < CUDART_INF_F ? 8 - ilogbf(most) : 0, e1 = e / 2, e2 = e - e1;
+      const float f1 = ldexpf(1.f, e1), f2 = ldexpf(1.f, e2);
+      rs[i] = ldexpf(ldexpf(P.scale * 1.4426950408889634f, -e1), -e2);
+      float mine = 0.f;  // of the group t4
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[n][k] = x[n][k] * f1 * f2;
+          sum += x[n][k];
+        }
+        qf[2 * n][i] = pack2<__half>(x[n][0], x[n][1]);
+        qf[2 * n][2 + i] = pack2<__half>(x[n][2], x[n][3]);
+        qf[2 * n + 1][i] = pack2<__half>(x[n][4] * 0.0625f, x[n][5] * 0.0625f);
+        qf[2 * n + 1][2 + i] = pack2<__half>(x[n][6] * 0.0625f, x[n][7] * 0.0625f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (n == t4) mine = sum;
+      }
+      // three parts of the heads' type; their products with the least values are exact
+      const float a = to_f32<E>(from_f32<E>(mine)), b = to_f32<E>(from_f32<E>(mine - a)), c = mine - a - b;
+      qs[i] = pack2<E>(a, b);
+      qs[2 + i] = pack2<E>(c, 0.f);
+    }
+  };
+  bool have = ring.take(pc);
+  if (have) load_q();
+  if constexpr (KS > 1) have = compute_all(have);
+  while (have) {
+    const Piece cur = pc;
+    const int ra = cur.row0 + mt * 16 + g;
+    int vis[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vis[i] = ra + 8 * i < cur.nrows ? cur.len - P.ql + 1 + (ra + 8 * i) / P.G : cur.len;
+    const int sure = cur.len - P.ql + 1;  // keys below this are seen by every row
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    for (int t = cur.tile0; t < cur.tile1; ++t) {
+      const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
+      const int tile_first = key_tile<kTile>(cur, t) * kTile + k0;
+      const uint32_t at = base + stage * C::STAGE;
+#pragma unroll 1
+      for (int blk = 0; blk < KPW; blk += 32) {
+        const int first = tile_first + blk;  // this warp's next 32 keys
+        if (!landed || first >= cur.len) break;
+        const int row0 = k0 + blk;           // their rows in the stage
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int krow = row0 + 8 * n;
+          uint32_t kw[NG], sa[NG], sb[NG];
+          lds_words<NG>(at + C::K_AT + (krow + turned) * (D / 2) + t4 * (NG * 4), kw);
+          lds_words<NG>(at + C::KS_AT + krow / 8 * group + t4 * (D / 8), sa);
+          lds_words<NG>(at + C::KS_AT + krow / 8 * group + (t4 + 4) * (D / 8), sb);
+          float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t w = kw[i], w8 = w >> 8;
+            mma16816<__half>(acc, qf[2 * i], w & 0x000f000fu, w8 & 0x000f000fu);
+            mma16816<__half>(acc, qf[2 * i + 1], w & 0x00f000f0u, w8 & 0x00f000f0u);
+            const float fa = to_f32<E>(sa[i] >> 16), fb = to_f32<E>(sb[i] >> 16);
+            p[0] = fmaf(fa, acc[0], p[0]);
+            p[1] = fmaf(fb, acc[1], p[1]);
+            p[2] = fmaf(fa, acc[2], p[2]);
+            p[3] = fmaf(fb, acc[3], p[3]);
+          }
+          const uint32_t least = t4 < NG ? lds32(at + C::KS_AT + krow / 8 * group + turned * (D / 8) + t4 * 4) & 0xffffu : 0u;
+          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          mma16816<E>(s[n], qs, least | least << 16, least);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][i] = fmaf(p[i], 16777216.f, s[n][i]);
+        }
+        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        const bool edge = first + 32 > sure;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] *= rs[i >> 1];
+            if (edge && first + 8 * n + t4 + 4 * (i & 1) >= vis[i >> 1]) s[n][i] = -CUDART_INF_F;
+            top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+          }
+        }
+        float ref[2];
+        bool grew = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          top[i] = fmaxf(top[i] - kShift, m[i]);
+          ref[i] = top[i] == -CUDART_INF_F ? 0.f : top[i];
+          grew |= top[i] > m[i];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f[i] = ex2(m[i] - ref[i]);
+            l[i] *= f[i];
+            m[i] = top[i];
+          }
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][0] *= f[0], o[d][1] *= f[0];
+            o[d][2] *= f[1], o[d][3] *= f[1];
+          }
+        }
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][i] = ex2(s[n][i] - ref[i >> 1]);
+            l[i >> 1] += s[n][i];
+          }
+          pf[n / 2][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
+          pf[n / 2][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t vw[4][VW], vs[4];  // rows t, t + 4 (the first operand word), t + 8, t + 12
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int vrow = row0 + 16 * u + t4 + 4 * k;
+            lds_words<VW>(at + C::V_AT + vrow * (D / 2) + g * (VW * 4), vw[k]);
+            vs[k] = lds32(at + C::VS_AT + (row0 / 8 + 2 * u + k / 2) * group + (t4 + 4 * (k & 1)) * (D / 8) + (g * NG / 8) * 4);
+            // nothing past the length counts, nor (of what only some rows see) what is no number: those rows get it below
+            if (edge) {
+              const int key = first + 16 * u + t4 + 4 * k;
+              if (key >= cur.len || (key >= sure && finite_bits<E>(vs[k]) != 0xffffffffu)) vs[k] = 0;
+            }
+          }
+          const uint32_t least01 = __byte_perm(vs[0], vs[1], 0x5410), step01 = __byte_perm(vs[0], vs[1], 0x7632);
+          const uint32_t least23 = __byte_perm(vs[2], vs[3], 0x5410), step23 = __byte_perm(vs[2], vs[3], 0x7632);
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t pick = half ? 0x7632 : 0x5410;
+              const uint32_t x = __byte_perm(vw[0][w], vw[1][w], pick), y = __byte_perm(vw[2][w], vw[3][w], pick);
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                mma16816<E>(o[8 * w + 4 * half + n], pf[u], value_pair<E>(x, n, step01, least01),
+                            value_pair<E>(y, n, step23, least23));
+            }
+        }
+        if (edge && P.ql > 1) {
+#pragma unroll 1
+          for (int key = max(sure, first); key < min(cur.len, first + 32); ++key) {
+            // this thread's values of a row, 2 t4 D / 8 .. + D / 4, lie in one group
+            if (finite_bits<E>(lds32(at + C::VS_AT + (row0 + key - first) / 8 * group + ((key - first) & 7) * (D / 8) + (t4 * NG / 4) * 4)) == 0xffffffffu) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (key < vis[i]) {
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) o[d][2 * i] = o[d][2 * i + 1] = CUDART_NAN_F;
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * stage);
+      if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    }
+
+    have = ring.take(pc);
+    if (have) load_q();  // on their way while this piece's sums are stored
+
+    // ---- join the warps that share keys, in halving steps ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+#pragma unroll
+    for (int step = KS / 2; step > 0; step >>= 1) {
+      if (step == KS / 2)
+        have = compute_all(have);
+      else
+        compute_sync();
+      // the buffer is free
+      if (ks >= step && ks < 2 * step) {
+        const int slot = (ks - step) * MT + mt;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16) =
+              make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+        if (t4 == 0) *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 128 + g * 16) = make_float4(m[0], l[0], m[1], l[1]);
+      }
+      compute_sync();
+      if (ks < step) {
+        const int slot = ks * MT + mt;
+        const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 128 + g * 16);
+        const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
+        float fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mm = fmaxf(m[i], ym[i]), rr = mm == -CUDART_INF_F ? 0.f : mm;
+          fa[i] = ex2(m[i] - rr);
+          fb[i] = ex2(ym[i] - rr);
+          l[i] = l[i] * fa[i] + yl[i] * fb[i];
+          m[i] = mm;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          const float4 v = *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16);
+          o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
+          o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
+          o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
+          o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
+        }
+      }
+    }
+    if (ks == 0) {
+      const AttendPieces& to = W.suffix;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = ra + 8 * i;
+        if (r >= cur.nrows) continue;
+        float* dst;
+        if (cur.first) {
+          const int tok = r / P.G;
+          const long long row = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + r - tok * P.G;
+          dst = to.row_o + row * D;
+          if (t4 == 0) to.row_ml[row] = make_float4(m[i], l[i], __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
+        } else {
+          const int slot = blockIdx.x * ROWS + r - cur.row0;
+          dst = to.cta_o + (long long)slot * D;
+          if (t4 == 0) to.cta_ml[slot] = make_float2(m[i], l[i]);
+        }
+        // column 2 t of the sums' tile d is value 2 t D / 8 + d
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int d = 0; d < D / 8; d += 4)
+            *reinterpret_cast<float4*>(dst + (2 * t4 + k) * (D / 8) + d) =
+                make_float4(o[d][2 * i + k], o[d + 1][2 * i + k], o[d + 2][2 * i + k], o[d + 3][2 * i + k]);
+      }
+    }
+  }
+}
+
+int attend4_ctas() { return 2 * sm_count(); }
+
+// 16 rows a tile where a key head has no more, else 32 or 64.
+int attend4_rows(int G, int ql) { return G * ql <= 16 ? 16 : G * ql <= 32 ? 32 : 64; }
+
+struct Layout4 {
+  size_t row_o, row_ml, cta_o, cta_ml, total;
+  Layout4(const KvView& kv, int B, int ql) {
+    const size_t rows = (size_t)B * ql * kv.hq, slots = (size_t)attend4_ctas() * attend4_rows(kv.hq / kv.hkv, ql);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t was = at;
+      at += (n + 255) & ~(size_t)255;
+      return was;
+    };
+    row_o = take(rows * kv.d * 4);
+    row_ml = take(rows * 16);
+    cta_o = take(slots * kv.d * 4);
+    cta_ml = take(slots * 8);
+    total = at;
+  }
+};
+
+template <typename E, int D, int MT>
+cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const Kv4Maps& maps, cudaStream_t s) {
+  const void* fn = reinterpret_cast<const void*>(attend4_kernel<E, D, MT>);
+  const cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const Launch at(dim3(attend4_ctas()), kThreads, Cfg<D>::SMEM, s);
+  return cudaLaunchKernelEx(&at.cfg, attend4_kernel<E, D, MT>, P, W, maps);
+}
+
+template <typename E, int D>
+cudaError_t launch_typed(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s) {
+  const Layout4 L(P.kv, P.B, P.ql);
+  char* w = static_cast<char*>(ws);
+  AttendWork W = {};
+  W.first = 0;
+  W.count = P.B;
+  W.behind = true;
+  W.suffix.row_o = reinterpret_cast<float*>(w + L.row_o);
+  W.suffix.row_ml = reinterpret_cast<float4*>(w + L.row_ml);
+  W.suffix.cta_o = reinterpret_cast<float*>(w + L.cta_o);
+  W.suffix.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml);
+  const int rows = attend4_rows(P.G, P.ql);
+  const cudaError_t e = rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
+                        : rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
+                                     : launch_stream<E, D, 4>(P, W, maps, s);
+  if (e != cudaSuccess) return e;
+  JoinShape shape = {};
+  shape.rows[0] = shape.rows[1] = rows;
+  shape.heads[0] = shape.heads[1] = 1;
+  shape.ctas[0] = shape.ctas[1] = attend4_ctas();
+  return launch_join(P, W, shape, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rows4(const Row4Params& P, bool load, cudaStream_t s) {
+  if (P.kv.dtype == PW_F16) return P.kv.d == 128 ? launch_rows<__half, 128>(P, load, s) : launch_rows<__half, 64>(P, load, s);
+  return P.kv.d == 128 ? launch_rows<__nv_bfloat16, 128>(P, load, s) : launch_rows<__nv_bfloat16, 64>(P, load, s);
+}
+
+size_t attend4_ws_bytes(const KvView& kv, int B, int ql) { return B == 0 ? 0 : Layout4(kv, B, ql).total; }
+
+cudaError_t launch_attend4(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s) {
+  if (P.kv.dtype == PW_F16) return P.kv.d == 128 ? launch_typed<__half, 128>(P, maps, ws, s) : launch_typed<__half, 64>(P, maps, ws, s);
+  return P.kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, ws, s) : launch_typed<__nv_bfloat16, 64>(P, maps, ws, s);
+}
+
+cudaError_t encode_kv4_maps(const Kv4View& kv, Kv4Maps* maps) {
+  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const auto enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t pt = 1ull << kv.page_shift, row = kv.d / 2, words = kv.d / 32;
+  const cuuint32_t box = pt < (cuuint64_t)kBoxTokens ? (cuuint32_t)pt : kBoxTokens, one[4] = {1, 1, 1, 1};
+  // codes: (byte, token of a page, head, page); steps: (word of a page's tokens, head, page)
+  const cuuint64_t cdim[4] = {row, pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
+  const cuuint64_t cstride[3] = {row, row * pt, row * pt * kv.hkv};
+  const cuuint32_t cbox[4] = {(cuuint32_t)row, box, 1, 1};
+  const cuuint64_t sdim[3] = {words * pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
+  const cuuint64_t sstride[2] = {4 * words * pt, 4 * words * pt * kv.hkv};
+  const cuuint32_t sbox[3] = {(cuuint32_t)(words * box), 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    if (enc(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? kv.v : kv.k, cdim, cstride, cbox, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        enc(i ? &maps->vs : &maps->ks, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, i ? kv.vs : kv.ks, sdim, sstride, sbox, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace pw

@@ -1,0 +1,639 @@
+// Causal attention of packed prompts over their own keys: tcgen05 products.
+//
+// Row r of a sequence and key head is query token r / G, head r % G of the
+// group, so the G heads that share keys lie side by side and a tile of 256 rows
+// ends within 256 / G keys of its diagonal.  A CTA takes 256 rows (two 128-row
+// tiles) past the 128-key tiles that they see, as attend_tc_kernel does
+// (pw_attend_tc.cu, which explains the parts): S = Q K^T and O += P V with
+// accumulators in tensor memory, P in the place of S, a softmax warpgroup and
+// an MMA warp a row tile.  Nothing is split: a row's keys stay in one CTA, and
+// its sums are divided and rounded on their way out.
+//
+// Work grows with a tile's place in its sequence, so the CTAs take the tiles by
+// falling place (a counting sort over the sequences' lengths, which every CTA
+// does for itself), to and fro: CTA c takes c, 2 P - 1 - c, 2 P + c, ...
+#include <cuda.h>
+#include <math_constants.h>
+
+#include "pw_attend.cuh"
+#include "pw_heads.cuh"
+#include "pw_tc.cuh"
+
+namespace pw {
+
+namespace {
+
+constexpr int kTile = 128;           // keys a tile
+constexpr int kRows = 256;           // rows a CTA has at a time
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+// Registers: launched with 168 a thread; the softmax warps take what the other four give up (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kParts = 2;            // a tile's weights are handed over in halves
+constexpr float kGrow = 8.f;         // sums are rescaled when a row's maximum has grown by 2^kGrow
+constexpr int kBuckets = 512;
+
+template <int D>
+struct Cfg {
+  static constexpr int NH = D / 64;
+  static constexpr int HALF = kTile * 128;                 // 64-value column block of 128 rows
+  static constexpr int SLOT = NH * HALF;                   // keys or values of a tile
+  static constexpr int Q_AT = 0;                           // two row tiles
+  static constexpr int RING_AT = 2 * SLOT;
+  static constexpr int SORT = (3 * kBuckets + 4) * 4;
+  static constexpr int FIT = (226 * 1024 - RING_AT - SORT - 1024) / SLOT;
+  static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+  static constexpr int BAR_AT = RING_AT + SLOTS * SLOT;
+  static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 192;
+  static constexpr int SORT_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
+  static constexpr int SMEM = SORT_AT + SORT;
+  static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
+};
+
+struct PromptMaps {
+  CUtensorMap k, v;
+};
+
+__device__ int prompt_err;  // the error word of calls without one
+
+// Tokens of a sequence, inside the call's.
+struct Span {
+  int lo, n;
+};
+__device__ __forceinline__ Span span_of(const PromptParams& P, int b, int* err) {
+  const int lo = P.offsets[b], hi = P.offsets[b + 1];
+  const int l = min(max(lo, 0), P.T), h = min(max(hi, l), P.T);
+  if (err && (l != lo || h != hi)) atomicExch(err, kErrOffsets);
+  return {l, h - l};
+}
+__device__ __forceinline__ int row_tiles(const PromptParams& P, int n) { return (int)(((long long)n * P.G + kRows - 1) / kRows); }
+
+// Row tiles in falling order of their place in the sequence.  Places are sorted into buckets of 2^shift.
+struct PromptWalk {
+  int* full;    // [kBuckets] sequences whose last, partial bucket this is; then what they hold of it
+  int* rest;
+  int* start;   // [kBuckets] row tiles in the buckets above; [kBuckets]: all row tiles
+  int shift, turn, bucket, b0, before;
+
+  __device__ __forceinline__ void clear(int tid) {
+    for (int i = tid; i < kBuckets; i += kThreads) full[i] = rest[i] = 0;
+  }
+  __device__ __forceinline__ void count(const PromptParams& P, int tid, int* err) {
+    for (int b = tid; b < P.B; b += kThreads) {
+      const int tiles = row_tiles(P, span_of(P, b, blockIdx.x == 0 ? err : nullptr).n);
+      if (tiles > 0) {
+        atomicAdd(&full[tiles >> shift], 1);
+        atomicAdd(&rest[tiles >> shift], tiles & ((1 << shift) - 1));
+      }
+    }
+  }
+  // One warp; lane 0 holds the highest buckets.
+  __device__ __forceinline__ void sort(int lane) {
+    constexpr int PER = kBuckets / 32;
+    auto scan = [&](int sum) {  // what the lanes before this one hold
+      int x = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      return x - sum;
+    };
+    const int top = kBuckets - 1 - lane * PER;
+    int sum = 0;
+    for (int i = 0; i < PER; ++i) sum += full[top - i];
+    const int above = scan(sum);  // sequences that reach past this lane's buckets
+    int a = above;
+    sum = 0;
+    for (int i = 0; i < PER; ++i) {
+      sum += (a << shift) + rest[top - i];
+      a += full[top - i];
+    }
+    int at = scan(sum);
+    a = above;
+    for (int i = 0; i < PER; ++i) {
+      start[top - i] = at;
+      at += (a << shift) + rest[top - i];
+      a += full[top - i];
+    }
+    if (lane == 31) start[kBuckets] = at;
+  }
+  __device__ __forceinline__ void begin() { turn = 0, bucket = -1, b0 = before = 0; }
+
+  // One warp: the CTA's next row tile; false (and a piece without tiles) at the end.
+  __device__ __forceinline__ bool next(const PromptParams& P, Piece& p, int lane) {
+    p.tile1 = 0;
+    const unsigned grid = gridDim.x;
+    const unsigned rank = turn * grid + ((turn & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+    ++turn;
+    const int unit = rank / P.hkv;
+    if (unit >= start[kBuckets]) return false;
+    int lo = 0, hi = kBuckets - 1;  // the lowest bucket that does not begin behind the tile
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (start[mid] <= unit) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lo != bucket) bucket = lo, b0 = before = 0;
+    const int want = unit - start[bucket], first = bucket << shift;
+#pragma unroll 1
+    for (; b0 < P.B; b0 += 32) {
+      const int b = b0 + lane;
+      Span s = {0, 0};
+      if (b < P.B) s = span_of(P, b, nullptr);
+      const int mine = min(max(row_tiles(P, s.n) - first, 0), 1 << shift);
+      int scan = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + scan > want);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        const int tile = first + want - before - __shfl_sync(0xffffffffu, scan - mine, at);
+        p.tok0 = __shfl_sync(0xffffffffu, s.lo, at);
+        p.nrows = __shfl_sync(0xffffffffu, s.n, at) * P.G;
+        p.head = rank - unit * P.hkv;
+        p.row0 = tile * kRows;
+        // the keys that each of the two row tiles sees, in tiles
+        p.tile0 = min(p.row0 + 127, p.nrows - 1) / P.G / kTile + 1;
+        p.len = min(p.row0 + 255, p.nrows - 1) / P.G + 1;
+        p.tile1 = (p.len + kTile - 1) / kTile;
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ bool active(const Piece& pc, int i) { return i == 0 || pc.row0 + 128 < pc.nrows; }
+// Key tiles of row tile i.
+__device__ __forceinline__ int tiles_of(const Piece& pc, int i) { return i == 0 ? pc.tile0 : active(pc, 1) ? pc.tile1 : 0; }
+
+// The key tiles of a CTA's pieces as one sequence.
+struct Tiles {
+  Piece pc;
+  int t = 0;
+  __device__ __forceinline__ bool next(PieceRing& ring) {
+    if (++t < pc.tile1) return true;
+    if (!ring.take(pc)) return false;
+    t = 0;
+    return true;
+  }
+};
+
+// The MMA warp of row tile I: the whole warp walks, one lane issues.  PV(n) goes out behind QK(n + 1)'s keys have come and
+// before QK(n + 1), whose scores take the place of the weights.
+template <typename E, int D, int I>
+__device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t full, uint32_t empty, uint32_t bars,
+                                         uint32_t tmem, volatile int* abort_flag, int* err) {
+  using C = Cfg<D>;
+  constexpr uint32_t id_qk = idesc_of<E>(kTile, false), id_pv = idesc_of<E>(D, true);
+  const uint32_t q_full = bars + 8 * I, s_full = bars + 16 + 8 * I, o_done = bars + 32 + 8 * I,
+                 p_full = bars + 64 + 8 * kParts * I;
+  const uint32_t ts = tmem + C::S_COL + I * 128, to = tmem + C::O_COL + I * 128;
+  const uint64_t q = sw128_desc(base + C::Q_AT + I * C::SLOT), k0 = sw128_desc(base + C::RING_AT);
+  const uint64_t v0 = sw128_desc_outer(base + C::RING_AT, C::HALF);
+  const uint32_t q_lo = (uint32_t)q, k_hi = (uint32_t)(k0 >> 32), v_hi = (uint32_t)(v0 >> 32);
+  const bool leader = elect_one();
+  unsigned qn = 0, pn = 0;     // phases of q_full and p_full waited for so far
+  unsigned slot = 0, par = 0;  // ring slot of the next keys or values, and its phase
+  Tiles it;
+  it.pc.tile1 = 0;
+  auto wait = [&](uint32_t bar, unsigned parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, err)) != 0;
+  };
+  bool have = it.next(ring), act = false, first = false, last = false;
+  unsigned vs = 0, vp = 0;     // the current tile's values
+  bool run = false;            // a tile is waiting for its weights
+  while (have || run) {
+    const bool k_act = have && it.t < tiles_of(it.pc, I), k_last = k_act && it.t + 1 == tiles_of(it.pc, I);
+    const unsigned ks = slot, kp = par;
+    if (have) {
+      if (++slot == C::SLOTS) slot = 0, par ^= 1;
+      if (!wait(full + 8 * ks, kp)) return;   // also of keys that this tile has no use for: an arrival belongs to their phase
+    }
+    if (run) {
+      if (!wait(full + 8 * vs, vp)) return;
+      if (act) {  // O (+)= P V
+        const uint32_t v_lo = (uint32_t)v0 + vs * (C::SLOT >> 4);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {  // as the parts of P come
+          if (!wait(p_full + 8 * h, pn)) return;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int c = 8 / kParts * h; c < 8 / kParts * (h + 1); ++c)
+              umma_ts_lo(to, ts + 8 * c, v_lo + 128 * c, v_hi, id_pv, c > 0 || !first);
+          }
+          __syncwarp();
+        }
+        ++pn;
+      }
+    }
+    // a piece's queries come once the sums of the one before are out, so not before its last product is issued
+    if (run && last) {
+      if (leader) umma_commit(o_done);
+      __syncwarp();
+    }
+    const bool k_first = k_act && it.t == 0;
+    if (k_first && !wait(q_full, qn++)) return;
+    tc_fence_after();
+    if (leader) {
+      if (k_act) {  // S = Q K^T; in order behind the product that reads the weights in its place
+        const uint32_t k_lo = (uint32_t)k0 + ks * (C::SLOT >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t step = (c / 4) * (C::HALF >> 4) + 2 * (c % 4);
+          umma_f16_lo(ts, q_lo + step, k_hi, k_lo + step, k_hi, id_qk, c != 0);
+        }
+        umma_commit(s_full);
+      }
+      if (run) umma_commit(empty + 8 * vs);
+      if (have) umma_commit(empty + 8 * ks);
+    }
+    __syncwarp();
+    run = have;
+    act = k_act;
+    first = k_first;
+    last = k_last;
+    if (have) {
+      vs = slot, vp = par;
+      if (++slot == C::SLOTS) slot = 0, par ^= 1;
+      have = it.next(ring);
+    }
+  }
+}
+
+// Adds to 32 of a row's sums the values that are no numbers, of the keys lo .. vis - 1.
+template <typename E>
+__device__ __forceinline__ void add_odd(const PromptParams& P, const Piece& pc, int lo, int vis, int col, uint32_t (&o)[32]) {
+#pragma unroll 1
+  for (int key = lo; key < vis; ++key) {
+    const E* src = static_cast<const E*>(P.v.ptr) + (pc.tok0 + key) * P.v.token_stride + pc.head * P.v.head_stride + col;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+      float x[8];
+      unpack8<E>(*reinterpret_cast<const uint4*>(src + c), x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (!isfinite(x[k])) o[c + k] = __float_as_uint(__uint_as_float(o[c + k]) + x[k]);
+    }
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams P, int shift, const __grid_constant__ PromptMaps maps) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::SLOTS, bars = empty + 8 * C::SLOTS + 16 * kPieces;
+  const uint32_t q_full = bars, s_full = bars + 16, o_done = bars + 32, turn = bars + 48, p_full = bars + 64;  // p_full: [row tile][part]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 16);
+  volatile int* odd_seen = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 12);  // values that are no numbers were taken out
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::PIECE_AT - 8);
+  int* err = P.err ? P.err : &prompt_err;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (base & 1023) {
+    if (tid == 0) atomicExch(err, kErrLayout);
+    return;
+  }
+  PieceRing ring;
+  ring.full = empty + 8 * C::SLOTS;
+  ring.empty = ring.full + 8 * kPieces;
+  ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
+  ring.abort_flag = abort_flag;
+  ring.err = err;
+  {
+    // the barriers lie side by side, one thread each: ring slots (full, empty), pieces (full, empty), then by row tile
+    // queries, scores, sums, turns and the parts of the weights
+    constexpr int kNear = 2 * C::SLOTS + 2 * kPieces, kAll = kNear + 8 + 2 * kParts;
+    if (tid < kAll) {
+      const int k = tid - kNear;
+      const int count = tid < C::SLOTS ? 1 : tid < 2 * C::SLOTS ? 2 : tid < 2 * C::SLOTS + kPieces ? 1
+                        : k < 0 ? kSoftmaxWarps + 2 : k < 2 ? 128 : k < 6 ? 1 : 128;
+      mbar_init(full + 8 * tid, count);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) *abort_flag = *odd_seen = 0;
+  }
+  PromptWalk walk;
+  walk.full = reinterpret_cast<int*>(smem + C::SORT_AT);
+  walk.rest = walk.full + kBuckets;
+  walk.start = walk.rest + kBuckets;
+  walk.shift = shift;
+  walk.clear(tid);
+  if (warp == kSoftmaxWarps + 3) tmem_alloc((uint32_t)__cvta_generic_to_shared(tmem_at), 512);
+  __syncthreads();
+  behind_the_stream();
+  let_next_start();
+  walk.count(P, tid, err);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ---- softmax: warpgroup i holds row tile i, one row a thread ----
+    const int i = warp >> 2, w4 = warp & 3, r = tid & 127;
+    const uint32_t lanes = (uint32_t)w4 << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t ts = tmem + lanes + C::S_COL + i * 128, to = tmem + lanes + C::O_COL + i * 128;
+    const bool plain_q = P.scale > 0.f;  // a negative scale turns the queries around, a scale of 0 takes them away
+    const float scale2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
+    Piece pc = {};
+    // Queries: a warp brings its 32 rows, whole lines at a time.
+    constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 32 / RPS;  // lanes a row, rows a step, steps
+    const int q_row = 32 * w4, q_sub = lane / LPR, q_col = lane % LPR;
+    const uint32_t q_base = base + C::Q_AT + i * C::SLOT;
+    // The lane's rows, RPS apart: f(k, source or null past the rows).
+    auto each_row = [&](auto f) {
+      const int row0 = pc.row0 + 128 * i + q_row + q_sub, tok = row0 / P.G;
+      int hd = row0 - tok * P.G, left = pc.nrows - row0;
+      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
+                     (pc.head * P.G + hd) * P.q.head_stride + 8 * q_col;
+      const long long turn_over = P.q.token_stride - P.G * P.q.head_stride;
+#pragma unroll 4
+      for (int k = 0; k < STEPS; ++k) {
+        f(k, left > 0 ? src : nullptr);
+        left -= RPS;
+        hd += RPS;
+        src += RPS * P.q.head_stride;
+        while (hd >= P.G) hd -= P.G, src += turn_over;
+      }
+    };
+    auto place_q = [&]() {
+      each_row([&](int k, const E* src) {
+        const int at = q_row + k * RPS + q_sub;
+        const uint32_t dst = q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4);
+        if (src && plain_q) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        } else {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (src && P.scale < 0.f) {
+            v = *reinterpret_cast<const uint4*>(src);
+            v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+          }
+          sts128(dst, v);
+        }
+      });
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(q_full + 8 * i);
+    };
+    unsigned n = 0;     // tiles of this row tile so far
+    unsigned flat = 0;  // tiles of the CTA before the current piece
+    unsigned turns = 0, done = 0;  // turns taken, pieces finished
+    bool ok = true;
+    auto advance = [&]() {  // to the next piece with rows of this tile
+      while (ring.take(pc)) {
+        if (active(pc, i)) return true;
+        flat += pc.tile1;
+      }
+      return false;
+    };
+    bool have = advance();
+    if (have) place_q();
+    while (have && ok) {
+      const Piece cur = pc;
+      const int row = cur.row0 + 128 * i + r;
+      const int tok = min(row, cur.nrows - 1) / P.G;
+      const int vis = tok + 1;                        // keys this row sees
+      const int sure0 = cur.row0 / P.G + 1;           // keys that every row of the piece sees
+      const int sure = (cur.row0 + 128 * i) / P.G + 1;  // ... of the row tile
+      const int tiles = tiles_of(cur, i);
+      const bool two = active(cur, 1);
+      float m = -CUDART_INF_F;
+      float2 l = make_float2(0.f, 0.f);
+      for (int t = 0; t < tiles; ++t, ++n) {
+        const bool both = two && t < cur.tile0;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * i, n & 1, abort_flag, err));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_load128(ts, s);
+        if (both) {  // the warpgroups take turns, so that one's softmax meets the other's products
+          ok = __all_sync(0xffffffffu, mbar_wait(turn + 8 * i, (turns & 1) ^ (i ^ 1), abort_flag, err));
+          if (!ok) break;
+          ++turns;
+        }
+        const int see = vis - t * kTile;
+        float top = -CUDART_INF_F;
+        if ((t + 1) * kTile > sure) {
+          // what a row does not see counts as -infinity: a weight of 0
+#pragma unroll
+          for (int k = 0; k < 128; ++k) {
+            if (k >= see) s[k] = 0xff800000u;
+            top = fmaxf(top, __uint_as_float(s[k]));
+          }
+        } else {
+          float t1 = -CUDART_INF_F, t2 = t1, t3 = t1;
+#pragma unroll
+          for (int k = 0; k < 128; k += 8) {
+            top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+            t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+            t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+            t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+          }
+          top = fmaxf(max3(top, t1, t2), t3);
+        }
+        top = top == -CUDART_INF_F ? top : top * scale2 - kShift;
+        if (t == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+          const float mm = fmaxf(m, top), f = mm == -CUDART_INF_F ? 1.f : ex2(m - mm);
+          m = mm;
+          l.x *= f, l.y *= f;
+          // these scores were issued behind the last product into O: it is done
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_load16(to + c, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_store16(to + c, o);
+          }
+        }
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
+        if (i == (t < cur.tile0 ? 0 : 1) && (t + 1) * kTile > sure0) {
+          // values at keys that no row of the piece sees may be anything: 0 instead (one key a thread; the other row
+          // tile's turn comes after this); so for those that are no numbers and that some rows do not see, which the
+          // others get at the end
+          const unsigned slot = 2 * (flat + t) + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
+          if (!ok) break;
+          const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
+          const int key = t * kTile + r;
+          if (key >= sure0) {
+#pragma unroll 1
+            for (int c = 0; c < 8 * C::NH; ++c) {
+              const uint32_t to = at + (c >> 3) * C::HALF + 16 * ((c ^ r) & 7);
+              if (key >= cur.len) {
+                sts128(to, make_uint4(0, 0, 0, 0));
+                continue;
+              }
+              const uint4 v = shared16(to);
+              if (!all_finite<E>(v)) {
+                sts128(to, make_uint4(v.x & finite_bits<E>(v.x), v.y & finite_bits<E>(v.y), v.z & finite_bits<E>(v.z),
+                                      v.w & finite_bits<E>(v.w)));
+                *odd_seen = 1;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          constexpr int N = kTile / kParts;  // keys of a part, two a column
+          uint32_t p[N / 2];
+#pragma unroll
+          for (int k = 0; k < N; k += 2) {
+            const int at = N * h + k;
+            float2 a = fma2(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), sc, off);
+            a.x = ex2(a.x), a.y = ex2(a.y);
+            l = add2(l, a);
+            p[k / 2] = pack2<E>(a.x, a.y);
+          }
+#pragma unroll
+          for (int k = 0; k < N / 2; k += 16) tmem_store16(ts + N / 2 * h + k, p + k);
+          tmem_store_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + 8 * (kParts * i + h));
+          if (h == 0 && both) mbar_arrive(turn + 8 * (i ^ 1));
+        }
+      }
+      if (!ok) break;
+      flat += cur.tile1;
+      // the last S is out of the queries' way: the next piece's go in before this one's sums come out
+      have = advance();
+      if (have) place_q();
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
+      if (!ok) break;
+      tc_fence_after();
+      // the wait is over already: it makes what any thread of the row tile has seen known here, and what the first one's
+      // have was known at the turns
+      const bool odd = mbar_wait(p_full + 8 * (kParts * i + kParts - 1), (n - 1) & 1, abort_flag, err) && *odd_seen;
+      const bool in = row < cur.nrows;
+      const long long at = cur.tok0 + tok;
+      const int head = cur.head * P.G + min(row, cur.nrows - 1) - tok * P.G;
+      const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (in && P.lse) P.lse[at * P.hq + head] = sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.6931471805599453f;
+      E* out = static_cast<E*>(P.out.ptr) + at * P.out.token_stride + head * P.out.head_stride;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_load32(to + c, o);
+        if (odd && in) add_odd<E>(P, cur, sure0, vis, c, o);
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(o[k + j]) * inv;
+            *reinterpret_cast<uint4*>(out + c + k) = pack8<E>(x);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSoftmaxWarps) {
+      // ---- producer: keys and values of a tile take one ring slot each ----
+      walk.sort(lane);
+      __syncwarp();
+      walk.begin();
+      unsigned x = 0;  // slots filled so far
+      bool ok = true;
+      Piece pc = {};
+      while (ok) {
+        const bool more = walk.next(P, pc, lane);
+        ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
+        if (!more) break;
+        for (int t = 0; ok && t < pc.tile1; ++t) {
+          for (int v = 0; v < 2; ++v, ++x) {
+            const unsigned slot = x % C::SLOTS, round = x / C::SLOTS;
+            ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * slot, (round & 1) ^ 1, abort_flag, err));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(full + 8 * slot, C::SLOT);
+            __syncwarp();
+            if (lane < C::NH)
+              tma_load_3d(base + C::RING_AT + slot * C::SLOT + lane * C::HALF, v ? &maps.v : &maps.k, 64 * lane,
+                          pc.tok0 + t * kTile, pc.head, full + 8 * slot);
+            __syncwarp();
+          }
+        }
+      }
+      // copies in flight land before the shared memory goes away (after a normal end all have)
+      for (int i = 0; i < C::SLOTS; ++i) {
+        const unsigned fills = (x + C::SLOTS - 1 - i) / C::SLOTS;
+        for (int k = 0; fills > 0 && k < (1 << 16) && !mbar_try_wait(full + 8 * i, (fills - 1) & 1); ++k) {
+        }
+      }
+    } else if (warp == kSoftmaxWarps + 1) {
+      mma_role<E, D, 0>(ring, base, full, empty, bars, tmem, abort_flag, err);
+    } else if (warp == kSoftmaxWarps + 2) {
+      mma_role<E, D, 1>(ring, base, full, empty, bars, tmem, abort_flag, err);
+    }
+  }
+  // ---- teardown: every MMA has completed or the wait for it has run out ----
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0) {  // products issued before the wait ran out end well within this time
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1000000) {
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kSoftmaxWarps + 3) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+cudaError_t encode(const pw_rows& r, int T, int heads, int dtype, int d, CUtensorMap* map) {
+  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const auto enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  // the stride of a dimension of one does not matter to the caller, but has to be a stride
+  const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads};
+  const cuuint64_t stride[2] = {(cuuint64_t)(T > 1 ? r.token_stride : d) * 2, (cuuint64_t)(heads > 1 ? r.head_stride : d) * 2};
+  const cuuint32_t box[3] = {64, kTile, 1}, step[3] = {1, 1, 1};
+  return enc(map, dtype == PW_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.ptr, dim, stride, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <typename E, int D>
+cudaError_t launch_typed(const PromptParams& P, const PromptMaps& maps, cudaStream_t s) {
+  const void* fn = reinterpret_cast<const void*>(prompt_kernel<E, D>);
+  cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be row tiles
+  const long long most = ((long long)P.T * P.G / kRows + P.B) * P.hkv;
+  int shift = 0;
+  while ((((long long)P.T * P.G + kRows - 1) / kRows >> shift) >= kBuckets) ++shift;
+  const Launch at(dim3(most < sm_count() ? (unsigned)most : sm_count()), kThreads, Cfg<D>::SMEM, s);
+  return cudaLaunchKernelEx(&at.cfg, prompt_kernel<E, D>, P, shift, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s) {
+  PromptMaps maps;
+  cudaError_t e = encode(P.k, P.T, P.hkv, dtype, d, &maps.k);
+  if (e == cudaSuccess) e = encode(P.v, P.T, P.hkv, dtype, d, &maps.v);
+  if (e != cudaSuccess) return e;
+  if (dtype == PW_F16) return d == 128 ? launch_typed<__half, 128>(P, maps, s) : launch_typed<__half, 64>(P, maps, s);
+  return d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, s) : launch_typed<__nv_bfloat16, 64>(P, maps, s);
+}
+
+}  // namespace pw

@@ -1,43 +1,10 @@
 // Host entry points around the layer: argument checks of the head norm and
 // rotation, the paged KV cache, its attention and draft verification.
-#include "pw_serve.h"
-
-#include <cmath>
-#include <new>
+#include "pw_host.h"
 
 using namespace pw;
 
-struct pw_kv_s {
-  KvView view;
-  KvMapSet maps;
-};
-
 namespace {
-
-struct Range {
-  explicit Range(const char* name) { range_push(name); }
-  ~Range() { range_pop(); }
-};
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-inline pw_status launched(cudaError_t e) { return e == cudaSuccess ? PW_OK : record_cuda_error(e); }
-inline bool bad_tokens(int T) { return T < 0 || T > (1 << 20); }
-
-pw_status check_heads(const pw_heads& h) {
-  if (h.dtype != PW_F16 && h.dtype != PW_BF16) return PW_ERR_INVALID_ARG;
-  if (h.n_heads < 1 || h.n_kv_heads < 1 || h.n_heads > 16384 || h.n_heads % h.n_kv_heads != 0)
-    return PW_ERR_INVALID_ARG;
-  if (h.n_heads / h.n_kv_heads > kMaxGroup) return PW_ERR_UNSUPPORTED;
-  if (h.head_dim != 64 && h.head_dim != 128) return PW_ERR_UNSUPPORTED;
-  return PW_OK;
-}
-
-// A set of head rows that a call reads or writes: 16-byte aligned rows.
-bool bad_rows(const pw_rows* r) {
-  return !r || !r->ptr || !aligned16(r->ptr) || (r->token_stride & 7) || (r->head_stride & 7);
-}
 
 pw_status check_rotary(const pw_rotary& r, int d) {
   if (r.rot_dim < 0 || r.rot_dim > d || (r.rot_dim & 15)) return PW_ERR_INVALID_ARG;
@@ -61,6 +28,18 @@ void set_rotary(RopeParams& P, const pw_rotary* r, const int32_t* positions) {
 }
 
 }  // namespace
+
+pw_status pw::read_error(int* word, cudaStream_t s) {
+  int err = 0;
+  cudaError_t e = cudaMemcpyAsync(&err, word, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && err != 0) {
+    e = cudaMemsetAsync(word, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  if (e != cudaSuccess) return record_cuda_error(e);
+  return err == 0 ? PW_OK : err == kErrTimeout ? PW_ERR_TIMEOUT : PW_ERR_DEVICE_CHECK;
+}
 
 extern "C" pw_status pw_qk_norm_rope(const pw_heads* heads, const pw_rotary* rot, const int32_t* positions, int T,
                                      const pw_rows* q, const pw_rows* k, const pw_rows* q_out, const pw_rows* k_out,
@@ -135,16 +114,7 @@ extern "C" pw_status pw_kv_destroy(pw_kv_t kv) {
 extern "C" pw_status pw_kv_check_device(pw_kv_t kv, void* stream) {
   if (!kv) return PW_ERR_INVALID_ARG;
   if (host_sim()) return PW_ERR_UNSUPPORTED;
-  int err = 0;
-  cudaStream_t s = as_stream(stream);
-  cudaError_t e = cudaMemcpyAsync(&err, kv->view.err, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && err != 0) {
-    e = cudaMemsetAsync(kv->view.err, 0, sizeof(int), s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  }
-  if (e != cudaSuccess) return record_cuda_error(e);
-  return err == 0 ? PW_OK : err == kErrTimeout ? PW_ERR_TIMEOUT : PW_ERR_DEVICE_CHECK;
+  return read_error(kv->view.err, as_stream(stream));
 }
 
 extern "C" pw_status pw_kv_append(pw_kv_t kv, const pw_rotary* rot, const int32_t* positions, const int32_t* slots,
@@ -194,7 +164,6 @@ extern "C" pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* a, void* ws,
   const pw_status st = pw_kv_attend_workspace_size(kv, a->batch, a->q_len, a->n_groups, &need);
   if (st != PW_OK) return st;
   if (!std::isfinite(a->scale) || a->table_stride < 0 || a->prefix_stride < 0) return PW_ERR_INVALID_ARG;
-  constexpr long long kMostKeys = 0x7ffff000ll;  // whole tiles of them still count in 32 bits
   if (((long long)a->table_stride << w.page_shift) > kMostKeys || ((long long)a->prefix_stride << w.page_shift) > kMostKeys)
     return PW_ERR_INVALID_ARG;
   if (a->batch > 0) {

@@ -67,6 +67,77 @@ struct VerifyParams {
   int* err;
 };
 
+// The cache held in 4 bits (contiguous: [page][key head][token][...]).
+struct Kv4View {
+  char *k, *v;          // codes, head_dim / 2 bytes a row
+  char *ks, *vs;        // least value and step of every 32 values, head_dim / 8 bytes a row
+  int* err;
+  int dtype, hq, hkv, d;
+  int page_shift, n_pages;
+};
+
+struct Row4Params {
+  Kv4View kv;
+  pw_rows k, v;         // read by an append, written by a load
+  const int* slots;
+  int T;
+};
+
+struct WeighParams {
+  KvView kv;
+  pw_rows q;
+  const float* lse;
+  int B, ql, G;
+  float scale, decay;
+  const int* table;
+  int table_stride;
+  const int* lens;
+  const float* mass;
+  float* out;
+  int mass_stride;
+};
+
+struct EvictParams {
+  KvView kv;
+  int B, budget, recent;
+  const int* table;
+  int table_stride;
+  const int* lens;
+  const float* mass;
+  int mass_stride;
+  const int* new_table;
+  int new_stride;
+  int* new_lens;
+  float* new_mass;
+  int* kept;
+  int* ws_kept;         // [B][budget] tokens that stay
+  float* ws_mass;       // their masses
+  int* ws_left;         // [B]
+};
+
+struct PromptParams {
+  pw_rows q, k, v, out;
+  float* lse;
+  const int* offsets;
+  int* err;
+  int T, B, hq, hkv, G;
+  float scale;
+};
+
+constexpr int kMaxTop = 32;          // alternatives a token
+
+struct LogprobParams {
+  const void* logits;
+  long long row_stride;
+  int T, V, n_top;
+  const int* tokens;
+  float* logprob;
+  float* entropy;
+  int* top_ids;
+  float* top_logprobs;
+  int* err;
+};
+
 // These kernels start while the one before them in the stream still ends (programmatic dependent launch), which takes the
 // launch itself off a decode step's path (one token's norm and rotation 4.1 -> 2.3 us a call).  Each waits for the
 // completion of what came before (behind_the_stream) before it reads or writes global memory, so the order of the stream
@@ -108,5 +179,17 @@ constexpr int kBoxTokens = 64;
 cudaError_t encode_kv_maps(const KvView& kv, KvMapSet* maps);
 cudaError_t launch_attend(const AttendParams& P, const KvMapSet& maps, void* ws, cudaStream_t s);
 cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s);
+cudaError_t launch_weigh(const WeighParams& P, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams& P, cudaStream_t s);
+cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s);
+cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s);
+// Tensor maps of a 4-bit cache: codes (byte, token of a page, head, page), steps (word of a page's tokens, head, page).
+struct Kv4Maps {
+  CUtensorMap k, v, ks, vs;
+};
+cudaError_t encode_kv4_maps(const Kv4View& kv, Kv4Maps* maps);
+cudaError_t launch_rows4(const Row4Params& P, bool load, cudaStream_t s);
+size_t attend4_ws_bytes(const KvView& kv, int B, int ql);
+cudaError_t launch_attend4(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s);
 
 }  // namespace pw

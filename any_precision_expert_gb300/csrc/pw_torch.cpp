@@ -9,6 +9,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+
 #include "pw.h"
 
 namespace pw {
@@ -222,11 +224,181 @@ pw_status verify(PyObject* const* a) {
                          stream(a[9], p));
 }
 
+float number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Bad();
+  return (float)v;
+}
+
+struct Scratch {
+  void* ptr;
+  size_t bytes;
+};
+Scratch scratch(PyObject* o, const at::Tensor& like) {
+  const at::Tensor* ws = maybe(o, "ws");
+  if (!ws) return {nullptr, 0};
+  if (ws->device() != like.device()) fail("ws", "on another device");
+  if (!ws->is_contiguous()) fail("ws", "must be contiguous");  // else it has fewer bytes than its sizes say
+  return {ws->data_ptr(), ws->nbytes()};
+}
+
+// [B][pages] of a page table.
+const at::Tensor& page_table(PyObject* o, const char* what) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.dim() != 2) fail(what, "must be [batch, pages]");
+  return t;
+}
+
+// (q, k, v, offsets, out, scale, whether the scale is left to the heads, lse, err, stream)
+pw_status prompt(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &offsets = tensor(a[3], "offsets");
+  if (q.dim() != 3 || k.dim() != 3) fail("q", "q, k and v must be [T, heads, head_dim]");
+  on_gpu(q, "q");
+  const int64_t T = q.size(0), hq = q.size(1), hk = k.size(1), D = q.size(2);
+  const pw_heads heads = {dtype_of(q, "q"), size32(hq, "q"), size32(hk, "k"), size32(D, "q")};
+  pw_prompt_desc d = {};
+  d.q = rows(q, T, hq, D, q, "q");
+  d.k = rows(k, T, hk, D, q, "k");
+  d.v = rows(v, T, hk, D, q, "v");
+  d.out = rows(tensor(a[4], "out"), T, hq, D, q, "out");
+  if (offsets.dim() != 1 || offsets.size(0) < 1) fail("offsets", "must be [batch + 1]");
+  d.offsets = vec<const int32_t>(a[3], at::kInt, q, "offsets", offsets.size(0));
+  d.batch = size32(offsets.size(0) - 1, "offsets");
+  d.tokens = size32(T, "q");
+  d.scale = PyObject_IsTrue(a[6]) ? (float)std::pow((double)D, -0.5) : number(a[5]);
+  d.lse = vec<float>(a[7], at::kFloat, q, "lse", T, hq);
+  d.err = vec<int32_t>(a[8], at::kInt, q, "err", 1);
+  return pw_prompt_attend(&heads, &d, stream(a[9], q));
+}
+
+// (logits, tokens, logprobs, entropy, top_ids, top_logprobs, err, stream)
+pw_status logprobs(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "logits");
+  if (x.dim() != 2) fail("logits", "must be [T, V]");
+  on_gpu(x, "logits");
+  if (x.size(1) > 1 && x.stride(1) != 1) fail("logits", "a row's values must be contiguous");
+  pw_logprob_desc d = {};
+  d.dtype = x.scalar_type() == at::kFloat ? (int)PW_F32 : x.scalar_type() == at::kHalf ? (int)PW_F16 : (int)PW_BF16;
+  if (d.dtype == PW_BF16 && x.scalar_type() != at::kBFloat16) fail("logits", "must be float32, float16 or bfloat16");
+  const int64_t T = x.size(0);
+  d.logits = x.data_ptr();
+  d.row_stride = x.stride(0);
+  d.T = size32(T, "logits");
+  d.V = size32(x.size(1), "logits");
+  d.tokens = vec<const int32_t>(a[1], at::kInt, x, "tokens", T);
+  d.logprobs = vec<float>(a[2], at::kFloat, x, "logprobs", T);
+  d.entropy = vec<float>(a[3], at::kFloat, x, "entropy", T);
+  if ((a[4] == Py_None) != (a[5] == Py_None)) fail("top_ids, top_logprobs", "both or neither");
+  if (const at::Tensor* ids = maybe(a[4], "top_ids")) {
+    if (ids->dim() != 2) fail("top_ids", "must be [T, n]");
+    d.n_top = size32(ids->size(1), "top_ids");
+    d.top_ids = vec<int32_t>(a[4], at::kInt, x, "top_ids", T, ids->size(1));
+    d.top_logprobs = vec<float>(a[5], at::kFloat, x, "top_logprobs", T, ids->size(1));
+  }
+  d.err = vec<int32_t>(a[6], at::kInt, x, "err", 1);
+  return pw_token_logprobs(&d, stream(a[7], x));
+}
+
+// The 4-bit cache's key steps [pages][key heads][tokens][D / 32][2] come with its calls: they have the heads' type.
+
+// (handle, cache steps, k, v, slots, load, stream)
+pw_status rows4(PyObject* const* a) {
+  auto* kv = static_cast<pw_kv4_t>(PyLong_AsVoidPtr(a[0]));
+  const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
+  const int64_t hk = cache.size(1), D = cache.size(3) * 32;
+  const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const int64_t T = k.dim() == 3 ? k.size(0) : -1;
+  const pw_rows rk = rows(k, T, hk, D, cache, "k"), rv = rows(v, T, hk, D, cache, "v");
+  const auto* slots = vec<const int32_t>(a[4], at::kInt, cache, "slots", T);
+  void* s = stream(a[6], cache);
+  return PyObject_IsTrue(a[5]) ? pw_kv4_load(kv, slots, size32(T, "k"), &rk, &rv, s) : pw_kv4_append(kv, slots, size32(T, "k"), &rk, &rv, s);
+}
+
+// (handle, cache steps, n_heads, q, table, lens, out, ws, q_len, scale, lse, stream)
+pw_status attend4(PyObject* const* a) {
+  auto* kv = static_cast<pw_kv4_t>(PyLong_AsVoidPtr(a[0]));
+  const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
+  const int64_t hq = integer(a[2]), D = cache.size(3) * 32;
+  const at::Tensor &q = tensor(a[3], "q"), &table = page_table(a[4], "table"), &out = tensor(a[6], "out");
+  pw_attend_desc d = {};
+  const int64_t B = table.size(0);
+  d.batch = size32(B, "table");
+  d.q_len = small(a[8], "q_len");
+  d.q = rows(q, B * d.q_len, hq, D, cache, "q");
+  d.out = rows(out, B * d.q_len, hq, D, cache, "out");
+  d.lse = vec<float>(a[10], at::kFloat, cache, "lse", B * d.q_len, hq);
+  d.scale = number(a[9]);
+  d.table_stride = size32(table.size(1), "table");
+  d.table = vec<const int32_t>(a[4], at::kInt, cache, "table", B, d.table_stride);
+  d.lens = vec<const int32_t>(a[5], at::kInt, cache, "lens", B);
+  const Scratch ws = scratch(a[7], cache);
+  return pw_kv4_attend(kv, &d, ws.ptr, ws.bytes, stream(a[11], cache));
+}
+
+// (handle, cache k, n_heads, q, table, lens, lse, mass, out, q_len, scale, decay, stream)
+pw_status weigh(PyObject* const* a) {
+  auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
+  const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
+  const int64_t hq = integer(a[2]), D = cache.size(3);
+  const at::Tensor &q = tensor(a[3], "q"), &table = page_table(a[4], "table"), &mass = tensor(a[7], "mass");
+  if (mass.dim() != 2) fail("mass", "must be [batch, positions]");
+  pw_weigh_desc d = {};
+  const int64_t B = table.size(0), M = mass.size(1);
+  d.batch = size32(B, "table");
+  d.q_len = small(a[9], "q_len");
+  d.q = rows(q, B * d.q_len, hq, D, cache, "q");
+  d.scale = number(a[10]);
+  d.decay = number(a[11]);
+  d.table_stride = size32(table.size(1), "table");
+  d.table = vec<const int32_t>(a[4], at::kInt, cache, "table", B, d.table_stride);
+  d.lens = vec<const int32_t>(a[5], at::kInt, cache, "lens", B);
+  d.lse = vec<const float>(a[6], at::kFloat, cache, "lse", B * d.q_len, hq);
+  d.mass = vec<const float>(a[7], at::kFloat, cache, "mass", B, M);
+  d.out = vec<float>(a[8], at::kFloat, cache, "out", B, M);
+  d.mass_stride = size32(M, "mass");
+  return pw_kv_weigh(kv, &d, stream(a[12], cache));
+}
+
+// (handle, cache k, table, lens, mass, budget, ws, recent, new_table, new_lens, new_mass, kept, stream)
+pw_status evict(PyObject* const* a) {
+  auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
+  const at::Tensor& cache = tensor(a[1], "cache");
+  on_gpu(cache, "cache");
+  const at::Tensor &table = page_table(a[2], "table"), &mass = tensor(a[4], "mass"), &to = page_table(a[8], "new_table");
+  if (mass.dim() != 2) fail("mass", "must be [batch, positions]");
+  pw_evict_desc d = {};
+  const int64_t B = table.size(0), M = mass.size(1);
+  d.batch = size32(B, "table");
+  d.budget = small(a[5], "budget");
+  d.recent = small(a[7], "recent");
+  d.table_stride = size32(table.size(1), "table");
+  d.table = vec<const int32_t>(a[2], at::kInt, cache, "table", B, d.table_stride);
+  d.lens = vec<const int32_t>(a[3], at::kInt, cache, "lens", B);
+  d.mass = vec<const float>(a[4], at::kFloat, cache, "mass", B, M);
+  d.mass_stride = size32(M, "mass");
+  d.new_stride = size32(to.size(1), "new_table");
+  d.new_table = vec<const int32_t>(a[8], at::kInt, cache, "new_table", B, d.new_stride);
+  d.new_lens = vec<int32_t>(a[9], at::kInt, cache, "new_lens", B);
+  d.new_mass = vec<float>(a[10], at::kFloat, cache, "new_mass", B, M);
+  d.kept = vec<int32_t>(a[11], at::kInt, cache, "kept", B, d.budget);
+  const Scratch ws = scratch(a[6], cache);
+  return pw_kv_evict(kv, &d, ws.ptr, ws.bytes, stream(a[12], cache));
+}
+
 PyObject* py_check_cache(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<check_cache>(a, n, 1); }
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<rope>(a, n, 8); }
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<append>(a, n, 11); }
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<attend>(a, n, 15); }
 PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<verify>(a, n, 10); }
+PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<prompt>(a, n, 10); }
+PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<logprobs>(a, n, 8); }
+PyObject* py_rows4(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<rows4>(a, n, 7); }
+PyObject* py_attend4(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<attend4>(a, n, 12); }
+PyObject* py_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<weigh>(a, n, 13); }
+PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) { return call<evict>(a, n, 13); }
 
 PyMethodDef methods[] = {
     {"check_cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_check_cache)), METH_FASTCALL, nullptr},
@@ -234,6 +406,12 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_append)), METH_FASTCALL, nullptr},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend)), METH_FASTCALL, nullptr},
     {"verify_draft", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_verify)), METH_FASTCALL, nullptr},
+    {"prompt", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_prompt)), METH_FASTCALL, nullptr},
+    {"logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_logprobs)), METH_FASTCALL, nullptr},
+    {"rows4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_rows4)), METH_FASTCALL, nullptr},
+    {"attend4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend4)), METH_FASTCALL, nullptr},
+    {"weigh", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_weigh)), METH_FASTCALL, nullptr},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_evict)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pw_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

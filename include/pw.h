@@ -550,10 +550,10 @@ pw_status pw_debug_page_address(pw_layer_t layer, int e, int p, int vpage, uint6
  * documented buffers is touched, and the call's device error word becomes
  * nonzero (PW_ERR_DEVICE_CHECK at the next pw_kv_check_device).
  */
-typedef enum { PW_F16 = 0, PW_BF16 = 1 } pw_dtype;
+typedef enum { PW_F16 = 0, PW_BF16 = 1, PW_F32 = 2 /* logits only */ } pw_dtype;
 
 typedef struct {
-  int dtype;        /* pw_dtype of every head row */
+  int dtype;        /* PW_F16 or PW_BF16, of every head row */
   int n_heads;      /* query heads, 1..16384 */
   int n_kv_heads;   /* key / value heads, divides n_heads */
   int head_dim;     /* 64 or 128 (PW_ERR_UNSUPPORTED otherwise) */
@@ -709,6 +709,183 @@ pw_status pw_kv_attend(pw_kv_t kv, const pw_attend_desc* desc, void* ws, size_t 
 pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int32_t* tokens,
                           const int32_t* n_draft, const float* u, const float* noise, int B, int K, int V,
                           int32_t* out, int32_t* accepted, int32_t* err, void* stream);
+
+/*
+ * Causal attention of whole prompts over their own keys, before they need a
+ * cache: B sequences packed one behind the other into T rows.  Row i of
+ * sequence b (rows offsets[b] .. offsets[b + 1] - 1) sees the rows offsets[b] ..
+ * i.  With s = scale * (q . key) over what a row sees,
+ *   out = sum e^s value / sum e^s,   lse = ln(sum e^s)
+ * (out 0 and lse -infinity where every e^s is 0).  A row's results never depend
+ * on keys or values that it does not see, whatever they hold (NaN included).
+ * Scores, the softmax and the sums are fp32; the weights e^s are rounded to the
+ * heads' type for the products with the values.
+ *   offsets  device int32 [batch + 1], not descending, in [0, T]; others are
+ *            clamped to that and flagged (descending ones that put a row into
+ *            two sequences leave its results unspecified)
+ *   k, v     strides of at least a row where there is more than one row along
+ *            them (PW_ERR_INVALID_ARG otherwise)
+ *   err      device int32 or NULL: the call's error word
+ * Rows in front of the first sequence, behind the last and between two are left as they
+ * were.  out must not overlap q, k or v.  No workspace.
+ */
+typedef struct {
+  pw_rows q, k, v, out;     /* [tokens][n_heads] rows; k, v: [tokens][n_kv_heads] */
+  float* lse;               /* device fp32 [tokens][n_heads], or NULL */
+  int tokens;               /* T in [0, 2^20] */
+  const int32_t* offsets;
+  int batch;                /* sequences, 0..4096 (PW_ERR_UNSUPPORTED above) */
+  float scale;              /* finite */
+  int32_t* err;
+} pw_prompt_desc;
+pw_status pw_prompt_attend(const pw_heads* heads, const pw_prompt_desc* desc, void* stream);
+
+/*
+ * Log probabilities of given tokens under rows of logits x, ln p_i = x_i -
+ * ln(sum e^x), with the rows' entropies -sum p ln p and best alternatives.
+ *   logits        device [T] rows of V values of `dtype` (fp32, fp16 or bf16),
+ *                 row_stride elements apart, aligned to their elements
+ *   tokens        device int32 [T]: a negative token means none (its logprob
+ *                 is 0); one past V gets NaN and is flagged
+ *   logprobs      device fp32 [T]
+ *   entropy       device fp32 [T] or NULL
+ *   top_ids       device int32 [T][n_top], top_logprobs fp32 [T][n_top]: the
+ *                 n_top largest logits, largest first, the lowest index of equal
+ *                 ones; where fewer than n_top logits are numbers above -infinity
+ *                 (+infinity counts as one) the rest is -1 and -infinity
+ *   err           device int32 or NULL: error word for tokens past V
+ * Sums are fp32 and in a fixed order.  A logit of -infinity has probability 0;
+ * a row of nothing else has log probabilities of -infinity and an entropy of 0;
+ * a row with a NaN or +infinity has NaN log probabilities and entropy.
+ * T in [0, 2^20], V in [1, 2^24], n_top in [0, 32] (PW_ERR_UNSUPPORTED above)
+ * and at most V.  No workspace.
+ */
+typedef struct {
+  const void* logits;
+  int dtype;                /* pw_dtype */
+  long long row_stride;
+  int T, V;
+  const int32_t* tokens;
+  float* logprobs;
+  float* entropy;
+  int n_top;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int32_t* err;
+} pw_logprob_desc;
+pw_status pw_token_logprobs(const pw_logprob_desc* desc, void* stream);
+
+/*
+ * The paged cache held in 4 bits, in caller memory: 5 bits a value instead of
+ * 16.  A head row is cut into groups of 32 values; a group keeps
+ *   least = the least value,  step = (largest - least) / 15 rounded to the heads' type,
+ *   c = (value - least) / step rounded to a whole number (ties to even) in 0..15,
+ *       0 where the step is 0 (differences and quotients are single fp32 operations)
+ * and a value stands for least + c step.  A group with a value that is not a
+ * finite number, or whose step would not be one, stands for NaN.
+ *   k, v              device, 16-byte aligned, contiguous [n_pages][n_kv_heads]
+ *                     [page_tokens][head_dim / 2] bytes of codes (their order inside
+ *                     a row is the library's)
+ *   k_steps, v_steps  device, 16-byte aligned, contiguous [n_pages][n_kv_heads]
+ *                     [page_tokens][head_dim / 32][2] values of the heads' type: least, step
+ *   err               device int32, zeroed by the caller, the handle's error word
+ * All must outlive the handle, which is used like a pw_kv_t.  Zeroed memory
+ * stands for zeros.
+ */
+typedef struct pw_kv4_s* pw_kv4_t;
+typedef struct {
+  pw_heads heads;
+  int page_tokens;          /* a power of two, 8..1024 */
+  int n_pages;              /* n_pages * page_tokens < 2^31 */
+} pw_kv4_desc;
+pw_status pw_kv4_create(const pw_kv4_desc* desc, void* k, void* v, void* k_steps, void* v_steps, int32_t* err,
+                        pw_kv4_t* out);
+pw_status pw_kv4_destroy(pw_kv4_t kv);
+pw_status pw_kv4_check_device(pw_kv4_t kv, void* stream);
+
+/*
+ * Append T tokens' keys and values [T][n_kv_heads] (normed and rotated already,
+ * pw_qk_norm_rope), and read tokens back: least + c step rounded to the heads'
+ * type.  slots as in pw_kv_append; a negative slot writes nothing on either
+ * way, one past the cache neither and is flagged.  Slots of one append are
+ * distinct, those of a load need not be.  T in [0, 2^20].
+ */
+pw_status pw_kv4_append(pw_kv4_t kv, const int32_t* slots, int T, const pw_rows* k, const pw_rows* v, void* stream);
+pw_status pw_kv4_load(pw_kv4_t kv, const int32_t* slots, int T, const pw_rows* k, const pw_rows* v, void* stream);
+
+/*
+ * Attention of a decode batch over the 4-bit cache: as pw_kv_attend without
+ * prefixes (n_groups must be 0, PW_ERR_UNSUPPORTED otherwise; sequences may name
+ * the same pages).  Keys enter the scores exactly as they are held, values
+ * rounded to the heads' type.
+ */
+pw_status pw_kv4_attend_workspace_size(pw_kv4_t kv, int batch, int q_len, size_t* bytes);
+pw_status pw_kv4_attend(pw_kv4_t kv, const pw_attend_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention weights of a decode step added up by key, after pw_kv_attend: for
+ * the positions i < lens[b] of sequence b's own keys
+ *   out[b][i] = decay * mass[b][i] + sum over its q_len query tokens and all heads of e^(scale q . key_i - lse)
+ * over the queries that see key i (query j sees 0 .. lens[b] - q_len + j); lse is
+ * what pw_kv_attend gave (prefixes included); a query whose lse is -infinity
+ * weighs nothing.  Positions at and past the length are left as they were.
+ * Sums are fp32 and in a fixed order.
+ *   q         [batch * q_len][n_heads] rows;  lse  device fp32 [batch * q_len][n_heads]
+ *   mass,out  device fp32 [batch][mass_stride]; may be the same
+ * Lengths are clamped to [0, min(table_stride * page_tokens, mass_stride)], and
+ * a page outside the cache reads as zeros; both are flagged.
+ */
+typedef struct {
+  pw_rows q;
+  const float* lse;
+  int batch;                /* 0..4096 */
+  int q_len;                /* 1..64 */
+  float scale, decay;       /* finite */
+  const int32_t* table;     /* device [batch][table_stride] */
+  int table_stride;
+  const int32_t* lens;
+  const float* mass;
+  float* out;
+  int mass_stride;
+} pw_weigh_desc;
+pw_status pw_kv_weigh(pw_kv_t kv, const pw_weigh_desc* desc, void* stream);
+
+/*
+ * Eviction: of a sequence's n = lens[b] tokens the last `recent` and, of the
+ * others, those with the largest masses stay, `budget` tokens in all (every
+ * token where n <= budget; `recent` counts up to that).  Of equal masses the
+ * lower position stays; one that is not a number is the smallest.  The tokens
+ * that stay keep their order: the j-th goes to position j,
+ *   new_lens[b] = min(n, budget),  new_mass[b][j] = its mass, 0 from there to mass_stride,
+ * and its keys and values go to position j of new_table's pages.  new_table
+ * may name the pages of `table` in their order (then the pages past the new
+ * length are free), or pages that no sequence of the call uses; new_lens and
+ * new_mass may be lens and mass.
+ *   new_table  device int32 [batch][new_stride], room for min(budget, old room)
+ *              tokens (PW_ERR_INVALID_ARG otherwise)
+ *   kept       device int32 [batch][budget] or NULL: the old positions, then -1
+ * Sequences of a call do not share pages.  Lengths are clamped to [0,
+ * min(table_stride * page_tokens, mass_stride)]; a page outside the cache reads
+ * as zeros and is not written; both are flagged.
+ * ws: as for pw_kv_attend, of pw_kv_evict_workspace_size() bytes.
+ */
+typedef struct {
+  int batch;                /* 0..4096 */
+  int budget;               /* 1..2^24 */
+  int recent;               /* >= 0 */
+  const int32_t* table;
+  int table_stride;
+  const int32_t* lens;
+  const float* mass;        /* device fp32 [batch][mass_stride] */
+  int mass_stride;
+  const int32_t* new_table;
+  int new_stride;
+  int32_t* new_lens;
+  float* new_mass;
+  int32_t* kept;
+} pw_evict_desc;
+pw_status pw_kv_evict_workspace_size(pw_kv_t kv, int batch, int budget, size_t* bytes);
+pw_status pw_kv_evict(pw_kv_t kv, const pw_evict_desc* desc, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Testing hook: host-simulated device (call before creating any pool).  The
