@@ -2,12 +2,14 @@
 //
 // A head row is cut into groups of 32 values.  A group keeps its least value
 // and a step of the heads' type and 32 codes c in 0..15; a value stands for
-// least + c step.  The order of a row's codes is that of the products:
-// * keys: word (t, i), i < D / 32, t < 4, at t D / 32 + i holds values
-//   32 i + 8 t .. + 7, value order 0 2 4 6 / 1 3 5 7 ... see key_nibble: what
-//   lane t of a group of four multiplies, so that a lane's share of a row is
-//   one aligned piece and a mask turns it into operands;
-// * values: plain, lowest first; lane g of eight takes D / 8 of them.
+// least + c step.  The order of a row's codes is that of the products, so that
+// a lane's share of a row is one aligned piece and a mask turns it into
+// operands:
+// * keys: word t D / 32 + i (i < D / 32, t < 4) holds values 32 i + 8 t .. + 7 in
+//   the nibbles of key_nibble: what lane t of four multiplies;
+// * values: in order, D / 8 for each of eight lanes; heads of 128 with the
+//   row's halves exchanged where bit 2 of the token is set, so that the rows
+//   a warp reads at once lie in different banks (value_word).
 #include <math_constants.h>
 
 #include "pw_attend.cuh"
@@ -22,6 +24,11 @@ namespace {
 // Nibble of a key word that holds value k of its eight: values (0, 1) and (2, 3) are the operand pairs of an even product
 // step, (4, 5) and (6, 7) of the odd one; a pair lies 16 bits apart.
 __device__ __forceinline__ constexpr int key_nibble(int k) { return (k & 1) * 4 + (k & 2) + (k >> 2); }
+
+template <int D>
+__device__ __forceinline__ int value_word(int l, int token) {
+  return D == 128 ? l ^ ((token & 4) << 1) : l;
+}
 
 template <typename E>
 __device__ __forceinline__ float to_f32(uint16_t bits) {
@@ -55,7 +62,7 @@ template <int D>
 __device__ __forceinline__ Row4 row4(const Kv4View& kv, int value, long long row, int l) {
   uint32_t* codes = reinterpret_cast<uint32_t*>(value ? kv.v : kv.k) + row * (D / 8);
   uint32_t* steps = reinterpret_cast<uint32_t*>(value ? kv.vs : kv.ks) + row * (D / 32);
-  return {codes + (value ? l : (l & 3) * (D / 32) + (l >> 2)), steps + (l >> 2)};
+  return {codes + (value ? value_word<D>(l, (int)row) : (l & 3) * (D / 32) + (l >> 2)), steps + (l >> 2)};
 }
 
 // The row of a slot and head; negative where nothing is written or read.
@@ -149,24 +156,36 @@ cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
 // a row by a power of two: that is exact but for values of less than 2^-18 of
 // the row's largest, which are off by at most 2^-29 of it.  Values are turned
 // into the heads' type, one rounding each.
+//
+// Both products have the cache as their first operand, 16 keys (or 16 of a
+// head's values) by 8 query rows, so that up to eight rows a key head, which is
+// what decode steps have, leave nothing idle and take 32 sums a lane; scores
+// become the second product's operand by transposing 8 x 8 blocks of weights.
+// Bound by the instructions that turn codes into operands, about 250 for 16
+// keys and values (2.5 KB), ahead of the loads: three CTAs an SM then hide what
+// is left of their latency.
 
 constexpr int kComputeWarps = 4;
 constexpr int kThreads = (kComputeWarps + 1) * 32;
 constexpr int kTile = 128;                                // keys a stage
 
-template <int D>
+template <int D, int NT>
 struct Cfg {
+  static constexpr int CTAS = NT == 1 ? 3 : 2;            // an SM
   // eight keys' steps take 128 bytes, where a copy lands, or 64 side by side (heads of 64 on pages of 16 tokens and more)
   static constexpr int CODES = kTile * (D / 2), STEPS = kTile * 16;
   static constexpr int K_AT = 0, V_AT = CODES, KS_AT = 2 * CODES, VS_AT = KS_AT + STEPS;
   static constexpr int STAGE = 2 * (CODES + STEPS);
-  static constexpr int STAGES = 81920 / STAGE;
-  static constexpr int JOIN = 2 * (D / 8) * 512;          // accumulators of two warps
+  static constexpr int JOIN = 2 * NT * (D / 16) * 512;    // accumulators of two warps
+  static constexpr int REST = JOIN + 2 * NT * 64 + kPieces * (int)sizeof(Piece) + 16 * kPieces + 16 * 16 + 16;
+  static constexpr int FIT = (226 * 1024 / CTAS - 1024 - REST) / STAGE;
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
   static constexpr int JOIN_AT = STAGES * STAGE;
   static constexpr int ML_AT = JOIN_AT + JOIN;
-  static constexpr int PIECE_AT = ML_AT + 2 * 128;
+  static constexpr int PIECE_AT = ML_AT + 2 * NT * 64;
   static constexpr int BAR_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
   static constexpr int SMEM = BAR_AT + 16 * STAGES + 16 * kPieces + 16;
+  static_assert(STAGES >= 2, "");
 };
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
@@ -190,12 +209,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
 }
-// Bytes of eight keys' steps in a stage.
-template <int D>
-__device__ __forceinline__ int step_group(int page_shift) {
-  return D == 128 || page_shift == 3 ? 128 : 64;
-}
-
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "");
@@ -208,6 +221,13 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
   } else {
     w[0] = lds32(at);
   }
+}
+
+// Rows and columns of an 8 x 8 block of 16-bit values exchanged (a row a group of four lanes).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // The code pair at bits 4 n and 4 n + 16 of w as numbers, times step, plus least, rounded once.
@@ -229,19 +249,25 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, int n, uint32_t step2
   }
 }
 
-// MT row tiles of 16; KS warps share the keys of a row tile.
-template <typename E, int D, int MT>
-__global__ void __launch_bounds__(kThreads, 2)
+// Bytes of eight keys' steps in a stage.
+template <int D>
+__device__ __forceinline__ int step_group(int page_shift) {
+  return D == 128 || page_shift == 3 ? 128 : 64;
+}
+
+// NT row tiles of 8 a warp, MT such sets of rows; KS warps share the keys of a set.
+template <typename E, int D, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
     attend4_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ Kv4Maps maps) {
-  using C = Cfg<D>;
-  constexpr int ROWS = 16 * MT, KS = kComputeWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64;
+  using C = Cfg<D, NT>;
+  constexpr int SET = 8 * NT, ROWS = SET * MT, KS = kComputeWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64, MV = D / 16;
   using Walk = AttendWalk<ROWS, kTile, 1, 1, 1>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES + 16 * kPieces);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (base & 1023) {
+  if (base & 127) {
     if (tid == 0) atomicExch(P.kv.err, kErrLayout);
     return;
   }
@@ -291,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t to = base + stage * C::STAGE;
           const int tok = at & ((1 << shift) - 1), off = lane * box;
           tma_load_page(to + C::K_AT + off * (D / 2), &maps.k, 0, tok, pc.head, page, full + 8 * stage, once);
-          tma_load_page(to + C::V_AT + off * (D / 2), &maps.v, 0, tok, pc.head, page, full + 8 * stage, once);
           tma_load_3d(to + C::KS_AT + off / 8 * group, &maps.ks, tok * (D / 32), pc.head, page, full + 8 * stage, once);
+          tma_load_page(to + C::V_AT + off * (D / 2), &maps.v, 0, tok, pc.head, page, full + 8 * stage, once);
           tma_load_3d(to + C::VS_AT + off / 8 * group, &maps.vs, tok * (D / 32), pc.head, page, full + 8 * stage, once);
         }
         __syncwarp();
@@ -311,13 +337,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = lane >> 2, t4 = lane & 3;
   const int group = step_group<D>(P.kv.page_shift);
   const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
-  const int turned = (g >> 1) + (g & 1) * 4;  // the key of eight that is column g of a score tile: columns 2 t, 2 t + 1 are keys t, t + 4
-  uint32_t qf[2 * NG][4], qs[4];
-  float rs[2];  // a row's score in log2 units is rs times its product
+  // Row m of eight keys is key order(m): the rows 2 t (and 2 t + 1) of values, which lanes t read at once, then lie in
+  // different banks, and so do the keys that lanes g and g + 1 read.
+  auto order = [](int m) { return m ^ (m >> 1 & 1); };
+  const int key_g = order(g), val_a = order(2 * t4), val_b = order(2 * t4 + 1);
+  uint32_t qf[NT][2 * NG][2], qs[NT][2];
+  float rs[NT][2];  // the score of row 2 t4 + k in log2 units is rs times its product
   auto load_q = [&]() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = pc.row0 + mt * 16 + g + 8 * i;
+    for (int j = 0; j < NT; ++j) {
+      const int r = pc.row0 + mt * SET + 8 * j + g;
       const bool in = r < pc.nrows;
       const int tok = in ? r / P.G : 0, hd = in ? pc.head * P.G + r - tok * P.G : 0;
       const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride + hd * P.q.head_stride + 8 * t4;
@@ -333,7 +362,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       // a power of two that brings the largest to 2^8 .. 2^9, in two factors that are numbers
       const int e = most > 0.f && most < CUDART_INF_F ? 8 - ilogbf(most) : 0, e1 = e / 2, e2 = e - e1;
       const float f1 = ldexpf(1.f, e1), f2 = ldexpf(1.f, e2);
-      rs[i] = ldexpf(ldexpf(P.scale * 1.4426950408889634f, -e1), -e2);
+      const float mine_rs = ldexpf(ldexpf(P.scale * 1.4426950408889634f, -e1), -e2);
+      rs[j][0] = __shfl_sync(0xffffffffu, mine_rs, 8 * t4);
+      rs[j][1] = __shfl_sync(0xffffffffu, mine_rs, 8 * t4 + 4);
       float mine = 0.f;  // of the group t4
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
@@ -343,18 +374,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           x[n][k] = x[n][k] * f1 * f2;
           sum += x[n][k];
         }
-        qf[2 * n][i] = pack2<__half>(x[n][0], x[n][1]);
-        qf[2 * n][2 + i] = pack2<__half>(x[n][2], x[n][3]);
-        qf[2 * n + 1][i] = pack2<__half>(x[n][4] * 0.0625f, x[n][5] * 0.0625f);
-        qf[2 * n + 1][2 + i] = pack2<__half>(x[n][6] * 0.0625f, x[n][7] * 0.0625f);
+        qf[j][2 * n][0] = pack2<__half>(x[n][0], x[n][1]);
+        qf[j][2 * n][1] = pack2<__half>(x[n][2], x[n][3]);
+        qf[j][2 * n + 1][0] = pack2<__half>(x[n][4] * 0.0625f, x[n][5] * 0.0625f);
+        qf[j][2 * n + 1][1] = pack2<__half>(x[n][6] * 0.0625f, x[n][7] * 0.0625f);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (n == t4) mine = sum;
       }
       // three parts of the heads' type; their products with the least values are exact
       const float a = to_f32<E>(from_f32<E>(mine)), b = to_f32<E>(from_f32<E>(mine - a)), c = mine - a - b;
-      qs[i] = pack2<E>(a, b);
-      qs[2 + i] = pack2<E>(c, 0.f);
+      qs[j][0] = pack2<E>(a, b);
+      qs[j][1] = pack2<E>(c, 0.f);
     }
   };
   bool have = ring.take(pc);
@@ -362,15 +393,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   if constexpr (KS > 1) have = compute_all(have);
   while (have) {
     const Piece cur = pc;
-    const int ra = cur.row0 + mt * 16 + g;
-    int vis[2];
+    const int ra = cur.row0 + mt * SET + 2 * t4;  // this lane's first row of a tile
+    int vis[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) vis[i] = ra + 8 * i < cur.nrows ? cur.len - P.ql + 1 + (ra + 8 * i) / P.G : cur.len;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) vis[j][k] = ra + 8 * j + k < cur.nrows ? cur.len - P.ql + 1 + (ra + 8 * j + k) / P.G : cur.len;
     const int sure = cur.len - P.ql + 1;  // keys below this are seen by every row
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    float o[D / 8][4];
+    float m[NT][2], l[NT][2], o[NT][MV][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int j = 0; j < NT; ++j) {
+      m[j][0] = m[j][1] = -CUDART_INF_F, l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MV; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+    }
 
     for (int t = cur.tile0; t < cur.tile1; ++t) {
       const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
@@ -381,90 +417,105 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int first = tile_first + blk;  // this warp's next 32 keys
         if (!landed || first >= cur.len) break;
         const int row0 = k0 + blk;           // their rows in the stage
-        float s[4][4];
+        float s[NT][2][4];                   // [row tile][16 keys]: keys order(g), + 8; rows 2 t4, + 1
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int krow = row0 + 8 * n;
-          uint32_t kw[NG], sa[NG], sb[NG];
-          lds_words<NG>(at + C::K_AT + (krow + turned) * (D / 2) + t4 * (NG * 4), kw);
-          lds_words<NG>(at + C::KS_AT + krow / 8 * group + t4 * (D / 8), sa);
-          lds_words<NG>(at + C::KS_AT + krow / 8 * group + (t4 + 4) * (D / 8), sb);
-          float p[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int h = 0; h < 2; ++h) {
+          const int krow = row0 + 16 * h;
+          uint32_t ka[NG], kb[NG], sa[NG], sb[NG];
+          lds_words<NG>(at + C::K_AT + (krow + key_g) * (D / 2) + t4 * (NG * 4), ka);
+          lds_words<NG>(at + C::K_AT + (krow + 8 + key_g) * (D / 2) + t4 * (NG * 4), kb);
+          lds_words<NG>(at + C::KS_AT + krow / 8 * group + key_g * (D / 8), sa);
+          lds_words<NG>(at + C::KS_AT + (krow / 8 + 1) * group + key_g * (D / 8), sb);
+          float p[NT][4];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) p[j][0] = p[j][1] = p[j][2] = p[j][3] = 0.f;
+          uint32_t la = 0, lb = 0;           // least values of the group t4
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t w = kw[i], w8 = w >> 8;
-            mma16816<__half>(acc, qf[2 * i], w & 0x000f000fu, w8 & 0x000f000fu);
-            mma16816<__half>(acc, qf[2 * i + 1], w & 0x00f000f0u, w8 & 0x00f000f0u);
+            const uint32_t wa = ka[i], wb = kb[i], wa8 = wa >> 8, wb8 = wb >> 8;
+            const uint32_t even[4] = {wa & 0x000f000fu, wb & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu};
+            const uint32_t odd[4] = {wa & 0x00f000f0u, wb & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u};
             const float fa = to_f32<E>(sa[i] >> 16), fb = to_f32<E>(sb[i] >> 16);
-            p[0] = fmaf(fa, acc[0], p[0]);
-            p[1] = fmaf(fb, acc[1], p[1]);
-            p[2] = fmaf(fa, acc[2], p[2]);
-            p[3] = fmaf(fb, acc[3], p[3]);
-          }
-          const uint32_t least = t4 < NG ? lds32(at + C::KS_AT + krow / 8 * group + turned * (D / 8) + t4 * 4) & 0xffffu : 0u;
-          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-          mma16816<E>(s[n], qs, least | least << 16, least);
+            if (i == t4) la = sa[i], lb = sb[i];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][i] = fmaf(p[i], 16777216.f, s[n][i]);
+            for (int j = 0; j < NT; ++j) {
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<__half>(acc, even, qf[j][2 * i][0], qf[j][2 * i][1]);
+              mma16816<__half>(acc, odd, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+              p[j][0] = fmaf(fa, acc[0], p[j][0]);
+              p[j][1] = fmaf(fa, acc[1], p[j][1]);
+              p[j][2] = fmaf(fb, acc[2], p[j][2]);
+              p[j][3] = fmaf(fb, acc[3], p[j][3]);
+            }
+          }
+          const uint32_t least[4] = {__byte_perm(la, la, 0x1010), __byte_perm(lb, lb, 0x1010), la & 0xffffu, lb & 0xffffu};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            s[j][h][0] = s[j][h][1] = s[j][h][2] = s[j][h][3] = 0.f;
+            mma16816<E>(s[j][h], least, qs[j][0], qs[j][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][h][i] = fmaf(p[j][i], 16777216.f, s[j][h][i]);
+          }
         }
-        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
         const bool edge = first + 32 > sure;
+        uint32_t pf[NT][2][2];  // weights as the second operand: keys 2 t4, + 1 (and + 8) of 16, row g
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int j = 0; j < NT; ++j) {
+          float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[n][i] *= rs[i >> 1];
-            if (edge && first + 8 * n + t4 + 4 * (i & 1) >= vis[i >> 1]) s[n][i] = -CUDART_INF_F;
-            top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[j][h][i] *= rs[j][i & 1];
+              if (edge && first + 16 * h + 8 * (i >> 1) + key_g >= vis[j][i & 1]) s[j][h][i] = -CUDART_INF_F;
+              top[i & 1] = fmaxf(top[i & 1], s[j][h][i]);
+            }
+          float ref[2];
+          bool grew = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], x));
+            top[k] = fmaxf(top[k] - kShift, m[j][k]);
+            ref[k] = top[k] == -CUDART_INF_F ? 0.f : top[k];
+            grew |= top[k] > m[j][k];
+          }
+          if (__any_sync(0xffffffffu, grew)) {
+            float f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              f[k] = ex2(m[j][k] - ref[k]);
+              l[j][k] *= f[k];
+              m[j][k] = top[k];
+            }
+#pragma unroll
+            for (int i = 0; i < MV; ++i) {
+              o[j][i][0] *= f[0], o[j][i][1] *= f[1];
+              o[j][i][2] *= f[0], o[j][i][3] *= f[1];
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[j][h][i] = ex2(s[j][h][i] - ref[i & 1]);
+              l[j][i & 1] += s[j][h][i];
+            }
+            pf[j][h][0] = transpose8(pack2<E>(s[j][h][0], s[j][h][1]));
+            pf[j][h][1] = transpose8(pack2<E>(s[j][h][2], s[j][h][3]));
           }
         }
-        float ref[2];
-        bool grew = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-          top[i] = fmaxf(top[i] - kShift, m[i]);
-          ref[i] = top[i] == -CUDART_INF_F ? 0.f : top[i];
-          grew |= top[i] > m[i];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-          float f[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            f[i] = ex2(m[i] - ref[i]);
-            l[i] *= f[i];
-            m[i] = top[i];
-          }
-#pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[d][0] *= f[0], o[d][1] *= f[0];
-            o[d][2] *= f[1], o[d][3] *= f[1];
-          }
-        }
-        uint32_t pf[2][4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[n][i] = ex2(s[n][i] - ref[i >> 1]);
-            l[i >> 1] += s[n][i];
-          }
-          pf[n / 2][2 * (n & 1)] = pack2<E>(s[n][0], s[n][1]);
-          pf[n / 2][2 * (n & 1) + 1] = pack2<E>(s[n][2], s[n][3]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t vw[4][VW], vs[4];  // rows t, t + 4 (the first operand word), t + 8, t + 12
+        for (int h = 0; h < 2; ++h) {
+          uint32_t vw[4][VW], vs[4];  // keys order(2 t4), order(2 t4 + 1), and those + 8
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int vrow = row0 + 16 * u + t4 + 4 * k;
-            lds_words<VW>(at + C::V_AT + vrow * (D / 2) + g * (VW * 4), vw[k]);
-            vs[k] = lds32(at + C::VS_AT + (row0 / 8 + 2 * u + k / 2) * group + (t4 + 4 * (k & 1)) * (D / 8) + (g * NG / 8) * 4);
+            const int in8 = k & 1 ? val_b : val_a, row = row0 + 16 * h + 8 * (k >> 1) + in8;
+            lds_words<VW>(at + C::V_AT + row * (D / 2) + value_word<D>(g * VW, in8) * 4, vw[k]);
+            vs[k] = lds32(at + C::VS_AT + (row0 / 8 + 2 * h + (k >> 1)) * group + in8 * (D / 8) + (g * NG / 8) * 4);
             // nothing past the length counts, nor (of what only some rows see) what is no number: those rows get it below
             if (edge) {
-              const int key = first + 16 * u + t4 + 4 * k;
+              const int key = first + 16 * h + 8 * (k >> 1) + in8;
               if (key >= cur.len || (key >= sure && finite_bits<E>(vs[k]) != 0xffffffffu)) vs[k] = 0;
             }
           }
@@ -477,22 +528,29 @@ __global__ void __launch_bounds__(kThreads, 2)
               const uint32_t pick = half ? 0x7632 : 0x5410;
               const uint32_t x = __byte_perm(vw[0][w], vw[1][w], pick), y = __byte_perm(vw[2][w], vw[3][w], pick);
 #pragma unroll
-              for (int n = 0; n < 4; ++n)
-                mma16816<E>(o[8 * w + 4 * half + n], pf[u], value_pair<E>(x, n, step01, least01),
-                            value_pair<E>(y, n, step23, least23));
+              for (int n = 0; n < 4; n += 2) {
+                const uint32_t a[4] = {value_pair<E>(x, n, step01, least01), value_pair<E>(x, n + 1, step01, least01),
+                                       value_pair<E>(y, n, step23, least23), value_pair<E>(y, n + 1, step23, least23)};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma16816<E>(o[j][4 * w + 2 * half + n / 2], a, pf[j][h][0], pf[j][h][1]);
+              }
             }
         }
         if (edge && P.ql > 1) {
 #pragma unroll 1
           for (int key = max(sure, first); key < min(cur.len, first + 32); ++key) {
-            // this thread's values of a row, 2 t4 D / 8 .. + D / 4, lie in one group
-            if (finite_bits<E>(lds32(at + C::VS_AT + (row0 + key - first) / 8 * group + ((key - first) & 7) * (D / 8) + (t4 * NG / 4) * 4)) == 0xffffffffu) continue;
+            // this lane's values of a row lie in one group
+            if (finite_bits<E>(lds32(at + C::VS_AT + (row0 + key - first) / 8 * group + ((key - first) & 7) * (D / 8) +
+                                     (g * NG / 8) * 4)) == 0xffffffffu)
+              continue;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (key < vis[i]) {
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d) o[d][2 * i] = o[d][2 * i + 1] = CUDART_NAN_F;
-              }
+              for (int k = 0; k < 2; ++k)
+                if (key < vis[j][k]) {
+#pragma unroll
+                  for (int i = 0; i < MV; ++i) o[j][i][k] = o[j][i][2 + k] = CUDART_NAN_F;
+                }
           }
         }
       }
@@ -506,10 +564,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // ---- join the warps that share keys, in halving steps ----
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[j][k] += __shfl_xor_sync(0xffffffffu, l[j][k], x);
 #pragma unroll
     for (int step = KS / 2; step > 0; step >>= 1) {
       if (step == KS / 2)
@@ -518,75 +577,84 @@ __global__ void __launch_bounds__(kThreads, 2)
         compute_sync();
       // the buffer is free
       if (ks >= step && ks < 2 * step) {
-        const int slot = (ks - step) * MT + mt;
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d)
-          *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16) =
-              make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-        if (t4 == 0) *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 128 + g * 16) = make_float4(m[0], l[0], m[1], l[1]);
+        for (int j = 0; j < NT; ++j) {
+          const int slot = ((ks - step) * MT + mt) * NT + j;
+#pragma unroll
+          for (int i = 0; i < MV; ++i)
+            *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * MV + i) * 512 + lane * 16) =
+                make_float4(o[j][i][0], o[j][i][1], o[j][i][2], o[j][i][3]);
+          if (g == 0) *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 64 + t4 * 16) = make_float4(m[j][0], l[j][0], m[j][1], l[j][1]);
+        }
       }
       compute_sync();
       if (ks < step) {
-        const int slot = ks * MT + mt;
-        const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 128 + g * 16);
-        const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
-        float fa[2], fb[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mm = fmaxf(m[i], ym[i]), rr = mm == -CUDART_INF_F ? 0.f : mm;
-          fa[i] = ex2(m[i] - rr);
-          fb[i] = ex2(ym[i] - rr);
-          l[i] = l[i] * fa[i] + yl[i] * fb[i];
-          m[i] = mm;
-        }
+        for (int j = 0; j < NT; ++j) {
+          const int slot = (ks * MT + mt) * NT + j;
+          const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 64 + t4 * 16);
+          const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
+          float fa[2], fb[2];
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          const float4 v = *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * (D / 8) + d) * 512 + lane * 16);
-          o[d][0] = o[d][0] * fa[0] + v.x * fb[0];
-          o[d][1] = o[d][1] * fa[0] + v.y * fb[0];
-          o[d][2] = o[d][2] * fa[1] + v.z * fb[1];
-          o[d][3] = o[d][3] * fa[1] + v.w * fb[1];
+          for (int k = 0; k < 2; ++k) {
+            const float mm = fmaxf(m[j][k], ym[k]), rr = mm == -CUDART_INF_F ? 0.f : mm;
+            fa[k] = ex2(m[j][k] - rr);
+            fb[k] = ex2(ym[k] - rr);
+            l[j][k] = l[j][k] * fa[k] + yl[k] * fb[k];
+            m[j][k] = mm;
+          }
+#pragma unroll
+          for (int i = 0; i < MV; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * MV + i) * 512 + lane * 16);
+            o[j][i][0] = o[j][i][0] * fa[0] + v.x * fb[0];
+            o[j][i][1] = o[j][i][1] * fa[1] + v.y * fb[1];
+            o[j][i][2] = o[j][i][2] * fa[0] + v.z * fb[0];
+            o[j][i][3] = o[j][i][3] * fa[1] + v.w * fb[1];
+          }
         }
       }
     }
     if (ks == 0) {
       const AttendPieces& to = W.suffix;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = ra + 8 * i;
-        if (r >= cur.nrows) continue;
-        float* dst;
-        if (cur.first) {
-          const int tok = r / P.G;
-          const long long row = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + r - tok * P.G;
-          dst = to.row_o + row * D;
-          if (t4 == 0) to.row_ml[row] = make_float4(m[i], l[i], __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
-        } else {
-          const int slot = blockIdx.x * ROWS + r - cur.row0;
-          dst = to.cta_o + (long long)slot * D;
-          if (t4 == 0) to.cta_ml[slot] = make_float2(m[i], l[i]);
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = ra + 8 * j + k;
+          if (r >= cur.nrows) continue;
+          float* dst;
+          if (cur.first) {
+            const int tok = r / P.G;
+            const long long row = (long long)(cur.tok0 + tok) * P.kv.hq + cur.head * P.G + r - tok * P.G;
+            dst = to.row_o + row * D;
+            if (g == 0) to.row_ml[row] = make_float4(m[j][k], l[j][k], __int_as_float((int)blockIdx.x), __int_as_float(cur.last_cta));
+          } else {
+            const int slot = blockIdx.x * ROWS + r - cur.row0;
+            dst = to.cta_o + (long long)slot * D;
+            if (g == 0) to.cta_ml[slot] = make_float2(m[j][k], l[j][k]);
+          }
+          // rows g and g + 8 of the sums' tile i are values g D / 8 + 2 i and + 1
+#pragma unroll
+          for (int i = 0; i < MV; i += 2)
+            *reinterpret_cast<float4*>(dst + g * (D / 8) + 2 * i) =
+                make_float4(o[j][i][k], o[j][i][2 + k], o[j][i + 1][k], o[j][i + 1][2 + k]);
         }
-        // column 2 t of the sums' tile d is value 2 t D / 8 + d
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int d = 0; d < D / 8; d += 4)
-            *reinterpret_cast<float4*>(dst + (2 * t4 + k) * (D / 8) + d) =
-                make_float4(o[d][2 * i + k], o[d + 1][2 * i + k], o[d + 2][2 * i + k], o[d + 3][2 * i + k]);
-      }
     }
   }
 }
 
-int attend4_ctas() { return 2 * sm_count(); }
-
-// 16 rows a tile where a key head has no more, else 32 or 64.
-int attend4_rows(int G, int ql) { return G * ql <= 16 ? 16 : G * ql <= 32 ? 32 : 64; }
+// Rows of a tile: 8 or 16 where a key head has no more, else 32 or 64.
+int attend4_rows(int G, int ql) {
+  const long long rows = (long long)G * ql;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+int attend4_ctas(int rows) { return (rows == 8 ? 3 : 2) * sm_count(); }
 
 struct Layout4 {
   size_t row_o, row_ml, cta_o, cta_ml, total;
   Layout4(const KvView& kv, int B, int ql) {
-    const size_t rows = (size_t)B * ql * kv.hq, slots = (size_t)attend4_ctas() * attend4_rows(kv.hq / kv.hkv, ql);
+    const int tile = attend4_rows(kv.hq / kv.hkv, ql);
+    const size_t rows = (size_t)B * ql * kv.hq, slots = (size_t)attend4_ctas(tile) * tile;
     size_t at = 0;
     auto take = [&](size_t n) {
       const size_t was = at;
@@ -601,13 +669,14 @@ struct Layout4 {
   }
 };
 
-template <typename E, int D, int MT>
+template <typename E, int D, int NT, int MT>
 cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const Kv4Maps& maps, cudaStream_t s) {
-  const void* fn = reinterpret_cast<const void*>(attend4_kernel<E, D, MT>);
-  const cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
+  using C = Cfg<D, NT>;
+  const void* fn = reinterpret_cast<const void*>(attend4_kernel<E, D, NT, MT>);
+  const cudaError_t e = ensure_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
-  const Launch at(dim3(attend4_ctas()), kThreads, Cfg<D>::SMEM, s);
-  return cudaLaunchKernelEx(&at.cfg, attend4_kernel<E, D, MT>, P, W, maps);
+  const Launch at(dim3(attend4_ctas(8 * NT * MT)), kThreads, C::SMEM, s);
+  return cudaLaunchKernelEx(&at.cfg, attend4_kernel<E, D, NT, MT>, P, W, maps);
 }
 
 template <typename E, int D>
@@ -623,14 +692,15 @@ cudaError_t launch_typed(const AttendParams& P, const Kv4Maps& maps, void* ws, c
   W.suffix.cta_o = reinterpret_cast<float*>(w + L.cta_o);
   W.suffix.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml);
   const int rows = attend4_rows(P.G, P.ql);
-  const cudaError_t e = rows == 16   ? launch_stream<E, D, 1>(P, W, maps, s)
-                        : rows == 32 ? launch_stream<E, D, 2>(P, W, maps, s)
-                                     : launch_stream<E, D, 4>(P, W, maps, s);
+  const cudaError_t e = rows == 8    ? launch_stream<E, D, 1, 1>(P, W, maps, s)
+                        : rows == 16 ? launch_stream<E, D, 2, 1>(P, W, maps, s)
+                        : rows == 32 ? launch_stream<E, D, 2, 2>(P, W, maps, s)
+                                     : launch_stream<E, D, 2, 4>(P, W, maps, s);
   if (e != cudaSuccess) return e;
   JoinShape shape = {};
   shape.rows[0] = shape.rows[1] = rows;
   shape.heads[0] = shape.heads[1] = 1;
-  shape.ctas[0] = shape.ctas[1] = attend4_ctas();
+  shape.ctas[0] = shape.ctas[1] = attend4_ctas(rows);
   return launch_join(P, W, shape, s);
 }
 

@@ -1,20 +1,24 @@
 // Log probabilities of given tokens, entropies and the best alternatives of
-// rows of logits x, in one pass:
-//   m = max x,  l = sum e^(x - m),  t = sum e^(x - m) (x - m),
-//   ln p_i = (x_i - m) - ln l,  H = ln l - t / l.
+// rows of logits x, in one pass.  With a_i = (x_i - m) log2 e about a maximum m,
+//   l = sum 2^a,  t = sum 2^a a,
+//   ln p_i = (x_i - m) - ln l,  H = ln l - ln 2 t / l.
 // Partial (m, l, t) join like the sums of a softmax; H's two terms have the
 // same sign, so nothing cancels.
 //
 // Bound: every logit is read once, HBM for long prompts, the chain of loads,
-// maxima and joins for a few rows.  A thread holds kVecs 16-byte vectors of a
-// round in registers, so that all its loads are in flight together and the
-// alternatives are picked without a second read; a cluster of CTAs shares a row.
+// maxima and joins for a few rows.  Measured: 2047 rows of 131072 bf16 logits
+// with 8 alternatives, 537 MB, in 106 us (5.1 TB/s; 95 without alternatives),
+// where it issues 79 million instructions, 77 us of issue slots; 8 rows of 32000
+// in 7.5 us.  A thread holds kVecs 16-byte vectors of a round in registers, so
+// that their loads are in flight together (with 2 / 4 / 6 / 8: 138 / 109 / 111 /
+// 106 us); a cluster of CTAs shares a row only where rows are few.
 //
-// Alternatives: a round's threads fall into 32 sets (by lane); the n-th largest
-// of the sets' maxima is a bound that n logits reach, and hardly more than n
-// do.  Those go to a list, whose best n by (value, lowest index) are found by
-// counting.  Where too many reach the bound (rows of equal logits), the n are
-// searched one after another instead.
+// Alternatives: a thread notes its vectors' maxima.  After kEpoch rounds the n-th
+// largest of 32 sets' maxima so far (the threads of a lane number) is a bound
+// that n logits reach, and hardly more than n do: the few vectors that reach it
+// are read again, from the L2, and their logits that do go to a list, whose
+// best n by (value, lowest index) are found by counting.  Where too many reach
+// it (rows of equal logits), the n are searched one after another instead.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -32,27 +36,93 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxCluster = 8;
 constexpr int kVecs = 8;       // 16-byte vectors a thread and round
-constexpr int kThreads = 256;
-constexpr int kList = 1024;    // alternatives a CTA lists
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 128;
+constexpr int kCtas = 6;       // an SM
+constexpr int kEpoch = 4;      // rounds between two looks for alternatives: 32 vectors a thread, one a lane that looks at them
+constexpr int kList = 512;    // alternatives a CTA lists
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A vector's values as fp32.
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays one
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// A vector's values as fp32, and the larger of two vectors, value by value (what is no number gives way).
 template <typename E>
 struct Vec {
   static constexpr int N = 8;
+  static constexpr uint32_t kNone = __is_same(E, __half) ? 0xfc00fc00u : 0xff80ff80u;
   static __device__ __forceinline__ void up(const uint4& r, float (&x)[N]) { unpack8<E>(r, x); }
   static __device__ __forceinline__ float one(const E* p) { return (float)*p; }
-  static __device__ __forceinline__ uint32_t none() { return sizeof(E) == 2 && __is_same(E, __half) ? 0xfc00fc00u : 0xff80ff80u; }
+  // Values from a low number up, so that a weight of 0 meets no infinity; what is no number stays that.  About a maximum
+  // of at most kSafe that number weighs 0.
+  static constexpr float kSafe = __is_same(E, __half) ? 6e4f : 1e6f;
+  static __device__ __forceinline__ uint4 finite_below(const uint4& r) {
+    constexpr uint32_t kLow = __is_same(E, __half) ? 0xfbfffbffu : 0xfe96fe96u;  // -65504, -1e38
+    const uint32_t low = kLow;
+    auto f = [&](uint32_t a) {
+      using V = typename Pair<E>::V;
+      const V m = __hmax2_nan(*reinterpret_cast<const V*>(&a), *reinterpret_cast<const V*>(&low));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    return make_uint4(f(r.x), f(r.y), f(r.z), f(r.w));
+  }
+  static __device__ __forceinline__ uint32_t more(uint32_t a, uint32_t b) {
+    using V = typename Pair<E>::V;
+    const V m = __hmax2(*reinterpret_cast<const V*>(&a), *reinterpret_cast<const V*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float top(uint32_t a) {
+    const float2 f = Pair<E>::up(*reinterpret_cast<const typename Pair<E>::V*>(&a));
+    return fmaxf(fmaxf(f.x, f.y), -CUDART_INF_F);
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void up(const uint4& r, float (&x)[N]) {
     x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
-  static __device__ __forceinline__ uint32_t none() { return 0xff800000u; }
+  static constexpr float kSafe = 1e6f;
+  static __device__ __forceinline__ uint4 finite_below(const uint4& r) {
+    auto f = [](uint32_t a) { return __float_as_uint(max_nan(__uint_as_float(a), -1e38f)); };
+    return make_uint4(f(r.x), f(r.y), f(r.z), f(r.w));
+  }
+  static __device__ __forceinline__ uint32_t more(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ float top(uint32_t a) { return fmaxf(__uint_as_float(a), -CUDART_INF_F); }
 };
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 struct Sums {
   float m, l, t;
@@ -62,8 +132,8 @@ struct Sums {
       l += ol, t += ot;
       return;
     }
-    const float da = fmaxf(m - mm, -1e30f), db = fmaxf(om - mm, -1e30f);  // of an empty side: a weight of 0
-    const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+    const float da = max_nan((m - mm) * kLog2e, -1e30f), db = max_nan((om - mm) * kLog2e, -1e30f);  // an empty side weighs 0
+    const float fa = ex2(da), fb = ex2(db);
     t = fa * fmaf(da, l, t) + fb * fmaf(db, ol, ot);
     l = fa * l + fb * ol;
     m = mm;
@@ -89,17 +159,17 @@ struct Handed {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const LogprobParams P) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprob_kernel(const LogprobParams P) {
   using V = Vec<E>;
   constexpr int N = V::N, WARPS = kThreads / 32;
   __shared__ Handed handed;
   __shared__ Alt list[kList];
+  __shared__ uint32_t vec_max[kEpoch * kVecs][kThreads + 1];
   __shared__ Sums warp_sums[WARPS];
-  __shared__ float set_max[WARPS][32];
+  __shared__ float set_max[2][WARPS][32];
   __shared__ Alt best[kMaxTop];
   __shared__ Alt warp_best[WARPS];
   __shared__ int s_count;
-  __shared__ float s_bar;
   behind_the_stream();
   let_next_start();
   const cg::cluster_group cluster = cg::this_cluster();
@@ -116,86 +186,128 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const LogprobParam
   if (part == 0 && tid < head) odd_at = tid;
   if (part == parts - 1 && tid >= 32 && tid - 32 < tail) odd_at = head + vecs * N + tid - 32;
   const float odd = odd_at >= 0 ? V::one(x + odd_at) : -CUDART_INF_F;
-  if (tid == 0) s_count = 0, s_bar = -CUDART_INF_F;
-  Sums sums = {-CUDART_INF_F, 0.f, 0.f};
+  if (tid == 0) s_count = 0;
+  Sums sums;
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
-  bool first = true;
+  constexpr int STEP = kVecs * kThreads;
+  uint4 raw[kVecs];
+  const uint4* mine = body + lo + tid;
+  auto load = [&](int v0) {
+    if (v0 + STEP <= hi) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) raw[u] = __ldcs(mine + v0 - lo + u * kThreads);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) {
+        raw[u] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+        if (v0 + u * kThreads + tid < hi) raw[u] = __ldcs(mine + v0 - lo + u * kThreads);
+      }
+    }
+  };
+  load(lo);
+  float seen = odd, epoch_top = -CUDART_INF_F;  // the largest so far, and since the last look
+  uint64_t l2 = 0, t2 = 0;
+  // a = (x - m) log2 e in one operation: x log2 e - rn(m log2 e), off by the rounding of the latter in all of a thread's
+  // terms alike, which the sums make good when m changes and at the end.  Not for an m beyond kSafe.
+  auto large = [](float m) { return !(fabsf(m) <= V::kSafe); };
+  auto rounded = [&](float m) {  // the power of two that makes it good
+    return large(m) ? 0.f : -fmaf(m, kLog2e, -(m * kLog2e));
+  };
 #pragma unroll 1
-  for (int v0 = lo; v0 < hi || first; v0 += kVecs * kThreads) {
-    uint4 raw[kVecs];
-    int most = 0;  // vectors of this thread
+  for (int v0 = lo, round = 0; v0 < hi || round == 0; v0 += STEP, ++round) {
+    uint32_t w = V::kNone;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const int v = v0 + u * kThreads + tid;
-      raw[u] = make_uint4(V::none(), V::none(), V::none(), V::none());
-      if (v < hi) raw[u] = __ldcs(body + v), most = u + 1;
+      const uint32_t y = V::more(V::more(raw[u].x, raw[u].y), V::more(raw[u].z, raw[u].w));
+      if (n > 0) vec_max[(round % kEpoch) * kVecs + u][tid] = y;
+      w = V::more(w, y);
     }
-    float top = first ? fmaxf(odd, -CUDART_INF_F) : -CUDART_INF_F;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      float f[N];
-      V::up(raw[u], f);
-#pragma unroll
-      for (int k = 0; k < N; ++k) top = fmaxf(top, f[k]);
+    const float was = seen, top = V::top(w);
+    seen = fmaxf(seen, top);
+    epoch_top = fmaxf(round % kEpoch == 0 ? -CUDART_INF_F : epoch_top, top);
+    // this round's sums, about the largest so far
+    const float ref = seen == -CUDART_INF_F ? 0.f : seen;
+    if (round > 0 && was != -CUDART_INF_F && seen > was) {
+      const float d = max_nan((was - seen) * kLog2e, -1e30f) + rounded(was) - rounded(seen), f = ex2(d);
+      t2 = mul2(pack(f, f), fma2(pack(d, d), l2, t2));
+      l2 = mul2(pack(f, f), l2);
     }
-    if (n > 0) {
-      set_max[warp][lane] = top;
-      __syncthreads();
-      if (warp == 0) {
-        float mine = set_max[0][lane];
+    if (!large(ref)) {
+      const float off = -(ref * kLog2e);
+      const uint64_t off2 = pack(off, off), unit = pack(kLog2e, kLog2e);
+      auto add = [&](float x, float y) {
+        const uint64_t a = fma2(pack(x, y), unit, off2);
+        const float2 f = unpack(a);
+        const uint64_t e = pack(ex2(f.x), ex2(f.y));
+        l2 = add2(l2, e);
+        t2 = fma2(e, a, t2);
+      };
+      if (round == 0 && odd_at >= 0) add(max_nan(odd, -1e38f), -1e38f);  // and one of no weight
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) mine = fmaxf(mine, set_max[w][lane]);
-        int rank = 0;
-#pragma unroll
-        for (int o = 0; o < 32; ++o) {
-          const float other = __shfl_sync(0xffffffffu, mine, o);
-          rank += other > mine || (other == mine && o < lane);
-        }
-        if (rank == n - 1) s_bar = fmaxf(s_bar, mine);
-      }
-      __syncthreads();
-      const float bar = s_bar;
-      if (top >= bar && top > -CUDART_INF_F) {
-        auto put = [&](float v, int i) {
-          if (v >= bar && v > -CUDART_INF_F) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kList) list[at] = {v, i};
-          }
-        };
-        if (first && odd_at >= 0) put(odd, odd_at);
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-          float f[N];
-          V::up(raw[u], f);
-#pragma unroll
-          for (int k = 0; k < N; ++k) put(f[k], head + (v0 + u * kThreads + tid) * N + k);
-        }
-      }
-    }
-    // this round's sums, about the larger of its own and the earlier maximum
-    const float mm = fmaxf(sums.m, top), ref = mm == -CUDART_INF_F ? 0.f : mm;
-    if (sums.m != -CUDART_INF_F && mm > sums.m) {
-      const float d = fmaxf(sums.m - mm, -1e30f), f = ex2(d * kLog2e);
-      sums.t = f * fmaf(d, sums.l, sums.t);
-      sums.l *= f;
-    }
-    sums.m = mm;
-    auto add = [&](float v) {
-      const float d = v - ref, e = ex2(d * kLog2e);
-      sums.l += e;
-      sums.t = fmaf(e, fmaxf(d, -1e30f), sums.t);  // 0 for a logit of -infinity
-    };
-    if (first && odd_at >= 0) add(odd);
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      if (u < most) {
+      for (int u = 0; u < kVecs; ++u) {
         float f[N];
-        V::up(raw[u], f);
+        V::up(V::finite_below(raw[u]), f);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) add(f[k], f[k + 1]);
+      }
+    } else {
+      auto add = [&](float x) {
+        const float a = max_nan((x - ref) * kLog2e, -1e30f), e = ex2(a);
+        l2 = add2(l2, pack(e, 0.f));
+        t2 = fma2(pack(e, 0.f), pack(a, 0.f), t2);
+      };
+      if (round == 0 && odd_at >= 0) add(odd);
+#pragma unroll 1
+      for (int v = v0 + tid; v < min(v0 + STEP, hi); v += kThreads) {
+        float f[N];
+        V::up(body[v], f);
 #pragma unroll
         for (int k = 0; k < N; ++k) add(f[k]);
       }
     }
-    first = false;
+    if (v0 + STEP < hi) load(v0 + STEP);
+    if (n > 0 && (round % kEpoch == kEpoch - 1 || v0 + kVecs * kThreads >= hi)) {
+      // every warp finds the bound for itself; a set's places are written again two looks later
+      float (&sets)[WARPS][32] = set_max[round / kEpoch & 1];
+      sets[warp][lane] = seen;
+      __syncthreads();
+      float top_set = sets[0][lane];
+#pragma unroll
+      for (int k = 1; k < WARPS; ++k) top_set = fmaxf(top_set, sets[k][lane]);
+      int rank = 0;
+#pragma unroll
+      for (int o = 0; o < 32; ++o) {
+        const float other = __shfl_sync(0xffffffffu, top_set, o);
+        rank += other > top_set || (other == top_set && o < lane);
+      }
+      const float bar = __shfl_sync(0xffffffffu, top_set, __ffs(__ballot_sync(0xffffffffu, rank == n - 1)) - 1);
+      auto put = [&](float v, int i) {
+        if (v >= bar && v > -CUDART_INF_F) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kList) list[at] = {v, i};
+        }
+      };
+      if (round < kEpoch && odd_at >= 0) put(odd, odd_at);
+      // the threads with a vector that reaches it, one after another: a lane a vector, then a lane a logit
+      unsigned threads = __ballot_sync(0xffffffffu, epoch_top >= bar && epoch_top > -CUDART_INF_F);
+#pragma unroll 1
+      for (; threads; threads &= threads - 1) {
+        const int who = warp * 32 + __ffs(threads) - 1;
+        const bool noted = lane / kVecs <= round % kEpoch;
+        const float most = noted ? V::top(vec_max[lane][who]) : -CUDART_INF_F;
+        unsigned vectors = __ballot_sync(0xffffffffu, most >= bar && most > -CUDART_INF_F);
+#pragma unroll 1
+        for (; vectors; vectors &= vectors - 1) {
+          const int v = lo + ((round - round % kEpoch) * kVecs + __ffs(vectors) - 1) * kThreads + who;
+          if (lane < N) put(V::one(x + head + (long long)v * N + lane), head + v * N + lane);
+        }
+      }
+    }
+  }
+  {
+    const float2 l = unpack(l2), t = unpack(t2);
+    const float c = seen == -CUDART_INF_F ? 0.f : rounded(seen), f = ex2(c);
+    sums = {seen, f * (l.x + l.y), f * fmaf(c, l.x + l.y, t.x + t.y)};
   }
   sums.warp();
   if (lane == 0) warp_sums[warp] = sums;
@@ -273,14 +385,14 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const LogprobParam
       lp = log_p(V::one(x + tok));
     }
     P.logprob[row] = lp;
-    if (P.entropy) P.entropy[row] = none ? 0.f : log_l - all.t / all.l;
+    if (P.entropy) P.entropy[row] = none ? 0.f : log_l - all.t / all.l * kLn2;
   }
-  if (tid < parts * n) {
-    const Alt mine = handed.best[tid / n][tid % n];
+  for (int i = tid; i < parts * n; i += kThreads) {
+    const Alt mine = handed.best[i / n][i % n];
     int rank = 0;
     for (int j = 0; j < parts * n; ++j) {
       const Alt o = handed.best[j / n][j % n];
-      rank += o.before(mine) || (o.v == mine.v && o.i == mine.i && j < tid);  // places without a token count in order
+      rank += o.before(mine) || (o.v == mine.v && o.i == mine.i && j < i);  // places without a token count in order
     }
     if (rank < n) {
       const bool some = mine.i != kNoToken;
@@ -292,12 +404,10 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(const LogprobParam
 
 template <typename E>
 cudaError_t launch_typed(const LogprobParams& P, cudaStream_t s) {
-  constexpr int kRound = kVecs * kThreads * Vec<E>::N;
-  // CTAs a row: as many as hold it in one round, more while the rows alone leave SMs idle and every thread has a vector
+  // CTAs a row: more than one only while the rows leave places for CTAs idle and every thread keeps a vector.  A CTA's
+  // fixed times weigh more than uneven ends: 2047 rows of 131072 take 110 / 119 / 136 / 194 us with 1 / 2 / 4 / 8.
   int parts = 1;
-  while (parts < kMaxCluster && ((long long)parts * kRound < P.V ||
-                                 ((long long)P.T * parts < 2 * sm_count() && P.V > parts * kThreads * Vec<E>::N)))
-    parts *= 2;
+  while (parts < kMaxCluster && (long long)P.T * parts < kCtas * sm_count() && P.V > parts * kThreads * Vec<E>::N) parts *= 2;
   const Launch at(dim3(P.T * parts), kThreads, 0, s, parts);
   return cudaLaunchKernelEx(&at.cfg, logprob_kernel<E>, P);
 }

@@ -301,6 +301,21 @@ def test_logprobs_masked_and_extreme_rows():
     check_logprobs(x.to(torch.bfloat16), [8, 4992, 0, 50, 9, 4999, 1, 2, int(x[8].argmax()), 4998, -7, 70000], 10)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_logprobs_maxima_at_the_ends_of_a_type(dt):
+    lo, hi = torch.finfo(TYPES[dt]).min, torch.finfo(TYPES[dt]).max
+    x = torch.full((8, 700), -INF)
+    x[0, 5:600:7] = lo
+    x[1, 3:500] = lo * 0.9375
+    x[2] = hi
+    x[3, 9] = hi
+    x[4, ::3], x[4, 1::3] = hi * 0.875, lo
+    x[5, :300], x[5, 300:] = lo, lo * 0.5
+    x[6] = torch.linspace(0.1, 0.2, 700) * lo
+    x[7] = torch.linspace(-1, 1, 700) * hi * 2.0 ** -100
+    check_logprobs(x.to(TYPES[dt]).cuda(), [5, 4, 0, 9, 3, 299, 0, 699], 6)
+
+
 def test_logprobs_bounds_over_rounds():
     # rows of several rounds whose best lie in the last, in ascending and in equal runs
     V = 150001
