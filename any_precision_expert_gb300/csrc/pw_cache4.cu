@@ -49,7 +49,10 @@ __device__ __forceinline__ uint16_t from_f32(float x) {
 // ---- append and load ------------------------------------------------------------
 //
 // Eight values a lane: a row is D / 8 lanes, a group four of them, a lane's
-// codes one word.  Bound by HBM for long prompts, by one chain of loads else.
+// codes one word.  Bound by HBM for long prompts, by one chain of loads else; a
+// warp has U steps of rows in flight (one while there are few).  Quotients are
+// products with the step's reciprocal, off by less than 2^-18, and exact
+// divisions where one falls that near to a half.
 
 constexpr int kRowThreads = 128;
 
@@ -76,72 +79,129 @@ __device__ __forceinline__ long long row_of(const Kv4View& kv, int slot, int hea
   return (((long long)page * kv.hkv + head) << kv.page_shift) + (slot & ((1 << kv.page_shift) - 1));
 }
 
-template <typename E, int D, bool LOAD>
+template <typename E>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // of two values each; what is no number stays
+  using V = typename Pair<E>::V;
+  const V m = __hmin2_nan(*reinterpret_cast<const V*>(&a), *reinterpret_cast<const V*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The codes of eight values of a group as a word, and its least value and step, given the values of its other lanes.
+template <typename E>
+__device__ __forceinline__ uint2 quantise8(const uint4& raw, bool value) {
+  // the group's least value and largest, the latter as the least of the negatives
+  constexpr uint32_t kSign = 0x80008000u;
+  const uint32_t lo2 = min2<E>(min2<E>(raw.x, raw.y), min2<E>(raw.z, raw.w));
+  const uint32_t hi2 = min2<E>(min2<E>(raw.x ^ kSign, raw.y ^ kSign), min2<E>(raw.z ^ kSign, raw.w ^ kSign));
+  uint32_t ends = min2<E>(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
+  ends = min2<E>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+  ends = min2<E>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+  const float lo = to_f32<E>(ends & 0xffff), hi = -to_f32<E>(ends >> 16);
+  const uint32_t step_bits = from_f32<E>((hi - lo) / 15.f);
+  const float step = to_f32<E>(step_bits);
+  if (!isfinite(lo) || !isfinite(hi) || !isfinite(step)) return make_uint2(0, 0x7fff7fff);  // the group holds what is no number
+  uint32_t w = 0;
+  if (step > 0.f) {
+    float x[8];
+    unpack8<E>(raw, x);
+    const float inv = 1.f / step;
+    constexpr float kRound = 12582912.f;  // 1.5 2^23: a sum with it is rounded to a whole number, in its low bits
+    float far = 0.f;                      // the largest distance from a whole number
+    uint32_t c[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float q = fminf((x[k] - lo) * inv, 15.f), r = q + kRound;
+      far = fmaxf(far, fabsf(q - (r - kRound)));
+      c[k] = __float_as_uint(r);
+    }
+    if (far > 0.5f - 3.814697265625e-6f || !(inv < CUDART_INF_F)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = __float_as_uint(fminf((x[k] - lo) / step, 15.f) + kRound);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w += (c[k] - __float_as_uint(kRound)) << 4 * (value ? k : key_nibble(k));
+  }
+  return make_uint2(w, (ends & 0xffff) | step_bits << 16);
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 values8(uint32_t w, uint32_t st, bool value) {
+  const float least = to_f32<E>(st & 0xffff), step = to_f32<E>(st >> 16);
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    // 2^23 + c, less 2^23
+    const float c = __uint_as_float((w >> 4 * (value ? k : key_nibble(k)) & 15) | 0x4b000000u) - 8388608.f;
+    x[k] = fmaf(c, step, least);
+  }
+  return pack8<E>(x);
+}
+
+template <typename E, int D, bool LOAD, int U>
 __global__ void __launch_bounds__(kRowThreads) row4_kernel(const Row4Params P) {
   behind_the_stream();
   let_next_start();
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, l = lane % LPR;
   const unsigned per = 2 * P.kv.hkv;  // rows a token: keys, then values
-  const unsigned unit = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  const unsigned t = unit / per;
-  const bool live = t < (unsigned)P.T;
-  int h = unit - t * per;
-  const int value = h >= P.kv.hkv;
-  h -= value ? P.kv.hkv : 0;
-  const pw_rows& rows = value ? P.v : P.k;
-  E* at = static_cast<E*>(rows.ptr) + (live ? t * rows.token_stride + h * rows.head_stride : 0) + 8 * l;
-  const long long row = live ? row_of(P.kv, P.slots[t], h, l == 0) : -1;
-  if constexpr (LOAD) {
-    if (row < 0) return;
-    const Row4 to = row4<D>(P.kv, value, row, l);
-    const uint32_t w = *to.codes, st = *to.step;
-    const float least = to_f32<E>(st & 0xffff), step = to_f32<E>(st >> 16);
-    float x[8];
+  const unsigned unit = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * (RPW * U) + lane / LPR;
+  unsigned t = unit / per, h = unit - t * per;
+  E* at[U];
+  int slot[U], head[U];
+  uint4 raw[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = fmaf((float)(w >> 4 * (value ? k : key_nibble(k)) & 15), step, least);
-    *reinterpret_cast<uint4*>(at) = pack8<E>(x);
-  } else {
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (row >= 0) raw = __ldcs(reinterpret_cast<const uint4*>(at));
-    float x[8];
-    unpack8<E>(raw, x);
-    float lo = x[0], hi = x[0];
-    int bad = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) lo = fminf(lo, x[k]), hi = fmaxf(hi, x[k]), bad |= !isfinite(x[k]);
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+  for (int i = 0; i < U; ++i) {
+    head[i] = h;
+    slot[i] = -1;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (t < (unsigned)P.T) {
+      slot[i] = P.slots[t];
+      const bool value = h >= (unsigned)P.kv.hkv;
+      const long long ts = value ? P.v.token_stride : P.k.token_stride, hs = value ? P.v.head_stride : P.k.head_stride;
+      at[i] = static_cast<E*>(value ? P.v.ptr : P.k.ptr) + t * ts + (value ? h - P.kv.hkv : h) * hs + 8 * l;
+      if (!LOAD) raw[i] = __ldcs(reinterpret_cast<const uint4*>(at[i]));
     }
-    if (row < 0) return;
-    uint16_t step_bits = from_f32<E>((hi - lo) / 15.f), least_bits = from_f32<E>(lo);  // the least is a value of the type
-    const float step = to_f32<E>(step_bits);
-    uint32_t w = 0;
-    if (bad || !isfinite(step)) {
-      step_bits = least_bits = 0x7fff;  // the group holds what is no number
-    } else if (step > 0.f) {
+    h += RPW;
+    while (h >= per) h -= per, ++t;
+  }
+  uint32_t w[U], st[U];
+  Row4 place[U];
+  bool live[U];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = min(max(__float2int_rn((x[k] - lo) / step), 0), 15);
-        w |= (uint32_t)c << 4 * (value ? k : key_nibble(k));
+  for (int i = 0; i < U; ++i) {
+    const int value = head[i] >= P.kv.hkv;
+    const long long row = row_of(P.kv, slot[i], value ? head[i] - P.kv.hkv : head[i], l == 0);
+    live[i] = row >= 0;
+    place[i] = row4<D>(P.kv, value, live[i] ? row : 0, l);
+    if (LOAD && live[i]) w[i] = *place[i].codes, st[i] = *place[i].step;
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const bool value = head[i] >= P.kv.hkv;
+    if constexpr (LOAD) {
+      if (live[i]) __stcs(reinterpret_cast<uint4*>(at[i]), values8<E>(w[i], st[i], value));
+    } else {
+      const uint2 r = quantise8<E>(raw[i], value);
+      if (live[i]) {
+        *place[i].codes = r.x;
+        if ((l & 3) == 0) *place[i].step = r.y;
       }
     }
-    const Row4 to = row4<D>(P.kv, value, row, l);
-    *to.codes = w;
-    if ((l & 3) == 0) *to.step = least_bits | (uint32_t)step_bits << 16;
   }
 }
 
+template <typename E, int D, int U>
+cudaError_t launch_unrolled(const Row4Params& P, bool load, cudaStream_t s) {
+  constexpr int kRows = kRowThreads / 32 * (32 / (D / 8)) * U;
+  const long long blocks = ((long long)P.T * 2 * P.kv.hkv + kRows - 1) / kRows;
+  if (blocks > 0x7fffffffll || blocks * kRows > 0xffffff00ll) return cudaErrorInvalidConfiguration;
+  const Launch at(dim3((unsigned)blocks), kRowThreads, 0, s);
+  return load ? cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, true, U>, P) : cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, false, U>, P);
+}
 template <typename E, int D>
 cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
-  constexpr int kRows = kRowThreads / 32 * (32 / (D / 8));
-  const long long blocks = ((long long)P.T * 2 * P.kv.hkv + kRows - 1) / kRows;
-  if (blocks > 0x7fffffffll || blocks * kRows > 0xffffffffll) return cudaErrorInvalidConfiguration;
-  const Launch at(dim3((unsigned)blocks), kRowThreads, 0, s);
-  return load ? cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, true>, P) : cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, false>, P);
+  const bool few = (long long)P.T * 2 * P.kv.hkv * D < (1 << 20);
+  return few ? launch_unrolled<E, D, 1>(P, load, s) : launch_unrolled<E, D, 4>(P, load, s);
 }
 
 // ---- attention ------------------------------------------------------------------

@@ -38,6 +38,7 @@ extern "C" pw_status pw_prompt_attend(const pw_heads* heads, const pw_prompt_des
   if (a->tokens > 0 && a->batch > 0) {
     for (const pw_rows* r : {&a->q, &a->k, &a->v, &a->out})
       if (bad_rows(r)) return PW_ERR_INVALID_ARG;
+    if (bad_strides(a->q, a->tokens, heads->n_heads, heads->head_dim)) return PW_ERR_INVALID_ARG;
     for (const pw_rows* r : {&a->k, &a->v})
       if (bad_strides(*r, a->tokens, heads->n_kv_heads, heads->head_dim)) return PW_ERR_INVALID_ARG;
     if (!a->offsets || !aligned4(a->offsets)) return PW_ERR_INVALID_ARG;
@@ -238,7 +239,7 @@ extern "C" pw_status pw_kv_weigh(pw_kv_t kv, const pw_weigh_desc* a, void* strea
 extern "C" pw_status pw_kv_evict_workspace_size(pw_kv_t kv, int batch, int budget, size_t* bytes) {
   if (!kv || !bytes || batch < 0 || budget < 1 || budget > (1 << 24)) return PW_ERR_INVALID_ARG;
   if (batch > kMaxBatch) return PW_ERR_UNSUPPORTED;
-  *bytes = 2 * up256((size_t)batch * budget * 4) + up256((size_t)batch * 4);
+  *bytes = up256((size_t)batch * budget * 8) + up256((size_t)batch * budget * 4) + up256((size_t)batch * 4);
   return PW_OK;
 }
 
@@ -283,8 +284,9 @@ extern "C" pw_status pw_kv_evict(pw_kv_t kv, const pw_evict_desc* a, void* ws, s
   P.new_mass = a->new_mass;
   P.kept = a->kept;
   char* at = static_cast<char*>(ws);
-  P.ws_kept = reinterpret_cast<int*>(at);
-  P.ws_mass = reinterpret_cast<float*>(at + up256((size_t)a->batch * a->budget * 4));
-  P.ws_left = reinterpret_cast<int*>(at + 2 * up256((size_t)a->batch * a->budget * 4));
+  const size_t tokens = (size_t)a->batch * a->budget;
+  P.ws_moves = reinterpret_cast<int2*>(at);
+  P.ws_mass = reinterpret_cast<float*>(at + up256(tokens * 8));
+  P.ws_left = reinterpret_cast<int*>(at + up256(tokens * 8) + up256(tokens * 4));
   return launched(launch_evict(P, as_stream(stream)));
 }

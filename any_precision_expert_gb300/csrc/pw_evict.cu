@@ -6,6 +6,7 @@
 #include "pw_heads.cuh"
 #include "pw_mma.cuh"
 #include "pw_serve.h"
+#include "pw_tc.cuh"
 
 namespace pw {
 
@@ -26,7 +27,7 @@ constexpr int kWeighWarps = 8;
 constexpr int kKeys = 64;            // keys a CTA
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const WeighParams P) {
+__global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const WeighParams P) {
   __shared__ float part[kWeighWarps][kKeys];
   behind_the_stream();
   let_next_start();
@@ -50,10 +51,27 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const WeighPara
     uint32_t qf[D / 16][4];
     float ref[2];
     int vis[2];
-#pragma unroll 1
-    for (int u = warp * per; u < min(units, (warp + 1) * per); ++u) {
+    const int u1 = min(units, (warp + 1) * per);
+    auto next = [&](int u) {  // the next unit with keys
+      while (u < u1 && key0 + (u % GROUPS) * 16 >= len) ++u;
+      return u;
+    };
+    auto load = [&](int u, uint4 (&kr)[2][D / 32]) {
       const int h = u / GROUPS, first = key0 + (u % GROUPS) * 16;
-      if (first >= len) continue;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int key = first + 8 * n;  // eight keys lie in one page
+        const int page = u < u1 && key < len ? table[key >> P.kv.page_shift] : -1;
+        const bool in = page >= 0 && page < P.kv.n_pages;
+        if (u < u1 && key < len && !in && lane == 0) atomicExch(P.kv.err, kErrPage);
+        const E* src = reinterpret_cast<const E*>(P.kv.k) + page * P.kv.page_stride + h * P.kv.head_stride +
+                       ((key & ((1 << P.kv.page_shift) - 1)) + g) * P.kv.token_stride + 8 * t4;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) kr[n][s] = in ? __ldcs(reinterpret_cast<const uint4*>(src + 32 * s)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto weigh = [&](int u, const uint4 (&kr)[2][D / 32]) {
+      const int h = u / GROUPS, first = key0 + (u % GROUPS) * 16;
       if (h != head) {
         head = h;
 #pragma unroll
@@ -73,18 +91,6 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const WeighPara
           vis[i] = !in || lse == -CUDART_INF_F ? 0 : sure + tok;  // a row that saw nothing weighs nothing
           ref[i] = lse * kLog2e;
         }
-      }
-      uint4 kr[2][D / 32];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int key = first + 8 * n;  // eight keys lie in one page
-        const int page = key < len ? table[key >> P.kv.page_shift] : -1;
-        const bool in = key < len && page >= 0 && page < P.kv.n_pages;
-        if (key < len && !in && lane == 0) atomicExch(P.kv.err, kErrPage);
-        const E* src = reinterpret_cast<const E*>(P.kv.k) + page * P.kv.page_stride + h * P.kv.head_stride +
-                       ((key & ((1 << P.kv.page_shift) - 1)) + g) * P.kv.token_stride + 8 * t4;
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) kr[n][s] = in ? __ldcs(reinterpret_cast<const uint4*>(src + 32 * s)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -106,6 +112,20 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const WeighPara
           if (g == 0) part[warp][key - key0] += w[k];
         }
       }
+    };
+    // two units' keys in registers: one on its way while the other is weighed
+    uint4 ka[2][D / 32], kb[2][D / 32];
+    int u = next(warp * per);
+    load(u, ka);
+#pragma unroll 1
+    while (u < u1) {
+      const int v = next(u + 1);
+      load(v, kb);
+      weigh(u, ka);
+      if (v >= u1) break;
+      u = next(v + 1);
+      load(u, ka);
+      weigh(v, kb);
     }
   }
   __syncthreads();
@@ -121,11 +141,14 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const WeighPara
 // ---- select -------------------------------------------------------------------
 //
 // A CTA a sequence.  Of the n - recent older tokens the budget - recent of the
-// largest masses stay: a radix search over the masses as ordered integers
-// finds the smallest that stays and how many of its equals do (the first
-// ones), and a scan in token order numbers them.
+// largest masses stay: a radix search over the masses as ordered integers finds
+// the smallest that stays and how many of its equals do (the first ones), and a
+// scan in token order numbers them.  Latency bounds it; masses of up to
+// kSpan tokens stay in registers over its passes.
 
 constexpr int kSelectThreads = 1024;
+constexpr int kOwn = 8;                          // masses a thread holds
+constexpr int kSpan = kOwn * kSelectThreads;
 
 // Order of masses as unsigned integers: larger is heavier; -0 is 0, what is no number is lightest.
 __device__ __forceinline__ unsigned mass_key(float x) {
@@ -134,10 +157,17 @@ __device__ __forceinline__ unsigned mass_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// The cache slot of position i of a page table's row; -1 outside the cache.
+__device__ __forceinline__ int slot_of(const KvView& kv, const int* table, int i) {
+  const int page = table[i >> kv.page_shift];
+  return page < 0 || page >= kv.n_pages ? -1 : (page << kv.page_shift) + (i & ((1 << kv.page_shift) - 1));
+}
+
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams P) {
   __shared__ unsigned hist[256];
   __shared__ unsigned s_prefix, s_left;
-  __shared__ int2 warp_sum[kSelectThreads / 32];
+  __shared__ unsigned count[kOwn * 32];            // of 1024 tokens by warp: heavier ones, and equal ones << 16; then their sums
+  __shared__ unsigned s_all;
   behind_the_stream();
   let_next_start();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -147,22 +177,46 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   const int left = (int)min((long long)min(n, P.budget), new_cap);  // tokens that stay
   const int recent = min(P.recent, left), older = n - recent, need = left - recent;
   const float* mass = P.mass + (long long)b * P.mass_stride;
-  int* kept = P.ws_kept + (long long)b * P.budget;
-  float* held = P.ws_mass + (long long)b * P.budget;
+  const int *from = P.table + (long long)b * P.table_stride, *to = P.new_table + (long long)b * P.new_stride;
+  const long long row = (long long)b * P.budget;
+  int2* moves = P.ws_moves + row;
+  float* held = P.ws_mass + row;
+  float own[kOwn];
+  auto load = [&](int first) {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int i = first + k * kSelectThreads + tid;
+      own[k] = i < older ? mass[i] : 0.f;
+    }
+  };
+  auto keep = [&](int at, int i, float x) {
+    const int src = slot_of(P.kv, from, i), dst = slot_of(P.kv, to, at);
+    if (src < 0 || dst < 0) atomicExch(P.kv.err, kErrPage);
+    moves[at] = make_int2(src, src == dst ? -1 : dst);
+    held[at] = x;
+    if (P.kept) P.kept[row + at] = i;
+  };
+  load(0);
+  for (int i = tid; i < recent; i += kSelectThreads) keep(need + i, older + i, mass[older + i]);
+  const bool all = need >= older;
   // the smallest key that stays (`bar`), and how many tokens of it
-  unsigned bar = 0;
-  int equal = older;
-  if (need < older) {
+  unsigned bar = 0, equal = 0;
+  if (!all) {
     if (tid == 0) s_prefix = 0, s_left = need;
-    __syncthreads();
 #pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
       __syncthreads();
       const unsigned prefix = s_prefix;
-      for (int i = tid; i < older; i += kSelectThreads) {
-        const unsigned k = mass_key(mass[i]);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[k >> shift & 255], 1u);
+#pragma unroll 1
+      for (int first = 0; first < older; first += kSpan) {
+        if (older > kSpan) load(first);
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+          if (first + k * kSelectThreads + tid >= older) break;
+          const unsigned key = mass_key(own[k]);
+          if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[key >> shift & 255], 1u);
+        }
       }
       __syncthreads();
       if (warp == 0) {  // the digit that holds the s_left-th largest
@@ -191,109 +245,161 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
     bar = s_prefix;
     equal = s_left;
   }
-  // a run of tokens a thread, numbered in order
-  const int per = (older + kSelectThreads - 1) / kSelectThreads, i0 = min(tid * per, older), i1 = min(i0 + per, older);
-  const bool all = need >= older;
-  int more = 0, same = 0;
-  for (int i = i0; i < i1; ++i) {
-    const unsigned k = all ? 1u : mass_key(mass[i]);
-    more += k > bar;
-    same += k == bar;
-  }
-  int2 scan = make_int2(more, same);
+  unsigned more_before = 0, same_before = 0;  // in the spans before
+#pragma unroll 1
+  for (int first = 0; first < older; first += kSpan) {
+    if (older > kSpan) load(first);
+    unsigned at[kOwn];  // heavier and equal tokens of the warp's 32 in front of this thread's, with its own flags
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, scan.x, o), y = __shfl_up_sync(0xffffffffu, scan.y, o);
-    if (lane >= o) scan.x += x, scan.y += y;
-  }
-  if (lane == 31) warp_sum[warp] = scan;
-  __syncthreads();
-  int at_more = scan.x - more, at_same = scan.y - same;
-  for (int w = 0; w < warp; ++w) at_more += warp_sum[w].x, at_same += warp_sum[w].y;
-  int at = at_more + min(at_same, equal);
-  for (int i = i0; i < i1; ++i) {
-    const float x = mass[i];
-    const unsigned k = all ? 1u : mass_key(x);
-    const bool stays = k > bar || (k == bar && at_same < equal);
-    at_same += k == bar;
-    if (stays) {
-      kept[at] = i;
-      held[at++] = x;
+    for (int k = 0; k < kOwn; ++k) {
+      const int i = first + k * kSelectThreads + tid;
+      const unsigned key = mass_key(own[k]);
+      const unsigned more = __ballot_sync(0xffffffffu, i < older && (all || key > bar));
+      const unsigned same = __ballot_sync(0xffffffffu, i < older && !all && key == bar);
+      const unsigned front = (1u << lane) - 1;
+      at[k] = __popc(more & front) | __popc(same & front) << 8 | (more >> lane & 1) << 16 | (same >> lane & 1) << 17;
+      if (lane == 0) count[k * 32 + warp] = __popc(more) | __popc(same) << 16;
     }
-  }
-  for (int i = tid; i < recent; i += kSelectThreads) {
-    kept[need + i] = older + i;
-    held[need + i] = mass[older + i];
+    __syncthreads();
+    if (warp == 0) {  // sums in front of every group of 32: of at most kSpan tokens, so both fit 16 bits
+      unsigned mine[kOwn], sum = 0;
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) sum += mine[k] = count[lane * kOwn + k];
+      unsigned scan = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+      }
+      if (lane == 31) s_all = scan;
+      scan -= sum;
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k) {
+        count[lane * kOwn + k] = scan;
+        scan += mine[k];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const unsigned sums = count[k * 32 + warp];
+      const unsigned more = more_before + (sums & 0xffff) + (at[k] & 255), same = same_before + (sums >> 16) + (at[k] >> 8 & 255);
+      const bool stays = (at[k] >> 16 & 1) || ((at[k] >> 17 & 1) && same < equal);
+      if (stays) keep(more + min(same, equal), first + k * kSelectThreads + tid, own[k]);
+    }
+    more_before += s_all & 0xffff, same_before += s_all >> 16;
+    __syncthreads();
   }
   __syncthreads();  // the new masses may lie in the old ones' place
   float* out = P.new_mass + (long long)b * P.mass_stride;
   for (int i = tid; i < P.mass_stride; i += kSelectThreads) out[i] = i < left ? held[i] : 0.f;
   if (P.kept)
-    for (int i = tid; i < P.budget; i += kSelectThreads) P.kept[(long long)b * P.budget + i] = i < left ? kept[i] : -1;
+    for (int i = left + tid; i < P.budget; i += kSelectThreads) P.kept[row + i] = -1;
   if (tid == 0) P.new_lens[b] = left, P.ws_left[b] = left;
 }
 
 // ---- move ---------------------------------------------------------------------
 //
 // Kept token j goes to slot j.  j is never above the token's old place, so a
-// CTA that goes through a row of places in order, and reads each step's rows
-// before any of the step is written, may move them inside the same pages.  The
-// rows of the next step are on their way meanwhile.  A CTA takes the keys or
-// the values of one head (or a 64-byte column of them, where the rows alone
-// would leave SMs idle).
+// CTA that goes through a row of places in order, and has each step's rows in
+// shared memory before any of the step is written, may move them inside the
+// same pages.  A CTA is one warp with the keys or the values of one head (or a
+// 64-byte column of them, where the rows alone would leave SMs idle); bulk
+// copies bring a step's 8 KB while the steps before go out, so that few
+// registers and no instructions in the data's way let seven CTAs an SM keep
+// HBM busy.
 
-constexpr int kMoveThreads = 256;
+constexpr int kStep = 8192;          // bytes of a step
+constexpr int kSteps = 3;            // in shared memory
+constexpr int kMoveSmem = kSteps * kStep + 8 * kSteps;
 
-template <int LPR>  // lanes a row: 16 bytes each
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams P, int columns) {
-  constexpr int U = 4, RPS = kMoveThreads / LPR, STEP = U * RPS;
+template <int R>  // rows a lane and step, of 256 / R bytes
+__global__ void __launch_bounds__(32) move_kernel(const EvictParams P, int columns) {
+  constexpr int BYTES = kStep / 32 / R, ROWS = 32 * R;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), bars = base + kSteps * kStep;
+  const int lane = threadIdx.x;
+  if (lane < kSteps) {
+    mbar_init(bars + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
   behind_the_stream();
   let_next_start();
-  const int b = blockIdx.y, tid = threadIdx.x, sub = tid / LPR;
-  int c = blockIdx.x;
-  const int col = c % columns;
-  c /= columns;
-  char* cache = (c & 1) ? P.kv.v : P.kv.k;
-  const long long base = (c >> 1) * P.kv.head_stride + (col * LPR + tid % LPR) * 8;
+  const int b = blockIdx.y, c = blockIdx.x / columns, col = blockIdx.x % columns;
+  char* cache = ((c & 1) ? P.kv.v : P.kv.k) + 2 * (c >> 1) * P.kv.head_stride + col * BYTES;
   const int left = P.ws_left[b], shift = P.kv.page_shift, mask = (1 << shift) - 1;
-  const int* kept = P.ws_kept + (long long)b * P.budget;
-  const int* from = P.table + (long long)b * P.table_stride;
-  const int* to = P.new_table + (long long)b * P.new_stride;
-  auto place = [&](const int* table, int i) -> uint4* {  // null outside the cache
-    const int page = table[i >> shift];
-    if (page < 0 || page >= P.kv.n_pages) return nullptr;
-    return reinterpret_cast<uint4*>(cache + 2 * (page * P.kv.page_stride + (i & mask) * P.kv.token_stride + base));
-  };
-  uint4 row[U], next[U];
-  uint4 *src[U], *dst[U], *next_dst[U];
-  auto load = [&](int j0, uint4 (&r)[U], uint4* (&d)[U]) {
+  const int2* moves = P.ws_moves + (long long)b * P.budget;
+  auto place = [&](int slot) { return cache + 2 * ((slot >> shift) * P.kv.page_stride + (slot & mask) * P.kv.token_stride); };
+  int dst[kSteps][R];
+  // rows of step s into shared memory; those of a page outside the cache are zeros
+  auto load = [&](int s, int (&to)[R]) {
+    int2 m[R];
+    unsigned rows = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * RPS + sub;
-      src[u] = d[u] = nullptr;
-      if (j < left) {
-        src[u] = place(from, kept[j]);
-        d[u] = place(to, j);
-        if (!src[u] || !d[u]) atomicExch(P.kv.err, kErrPage);
-        if (src[u] == d[u]) d[u] = nullptr;  // there already
+    for (int r = 0; r < R; ++r) {
+      const int j = s * ROWS + r * 32 + lane;
+      m[r] = j < left ? moves[j] : make_int2(-1, -1);
+      to[r] = m[r].y;
+      rows += __popc(__ballot_sync(0xffffffffu, m[r].x >= 0 && m[r].y >= 0));
+    }
+    const uint32_t bar = bars + 8 * (s % kSteps), at = base + (s % kSteps) * kStep + lane * BYTES;
+    if (lane == 0) mbar_arrive_expect_tx(bar, rows * BYTES);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (m[r].y < 0) continue;
+      if (m[r].x >= 0) {
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         at + r * 32 * BYTES),
+                     "l"(place(m[r].x)), "n"(BYTES), "r"(bar)
+                     : "memory");
+      } else {
+        for (int k = 0; k < BYTES; k += 16) sts128(at + r * 32 * BYTES + k, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r[u] = make_uint4(0, 0, 0, 0);  // a page outside the cache reads as zeros
-      if (src[u] && d[u]) r[u] = *src[u];
-    }
   };
-  load(0, row, dst);
+  const int steps = (left + ROWS - 1) / ROWS;
+  // a wait that gives up flags the error word and ends the moves; what is on its way lands first
+  auto wait = [&](int s) {
+    bool ok = false;
+    const long long t0 = clock64();
+    while (!(ok = mbar_try_wait(bars + 8 * (s % kSteps), (s / kSteps) & 1)) && clock64() - t0 < kWaitCycles) {
+    }
+    return __all_sync(0xffffffffu, ok);
+  };
+  bool ok = true;
+  load(0, dst[0]);
+  load(1, dst[1]);
+  int s0 = 0;
 #pragma unroll 1
-  for (int j0 = 0; j0 < left; j0 += STEP) {
-    load(j0 + STEP, next, next_dst);
-    __syncthreads();
+  for (; ok && s0 < steps; s0 += kSteps) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (dst[u]) *dst[u] = row[u];
-      row[u] = next[u];
-      dst[u] = next_dst[u];
+    for (int k = 0; k < kSteps; ++k) {  // the places in registers by their number
+      const int s = s0 + k;
+      if (!ok || s >= steps) break;
+      ok = wait(s);
+      if (!ok) break;
+      const uint32_t at = base + k * kStep + lane * BYTES;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (dst[k][r] >= 0)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(place(dst[k][r])),
+                       "r"(at + r * 32 * BYTES), "n"(BYTES)
+                       : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      // the step two ahead goes where the last one's rows have left
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+      load(s + 2, dst[(k + 2) % kSteps]);
+    }
+  }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (!ok) {
+    if (lane == 0) atomicExch(P.kv.err, kErrTimeout);
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1000000) {
     }
   }
 }
@@ -314,15 +420,15 @@ cudaError_t launch_weigh(const WeighParams& P, cudaStream_t s) {
 cudaError_t launch_evict(const EvictParams& P, cudaStream_t s) {
   const Launch sel(dim3(P.B), kSelectThreads, 0, s);
   const cudaError_t e = cudaLaunchKernelEx(&sel.cfg, select_kernel, P);
-  if (e != cudaSuccess || P.budget == 0) return e;
-  const long long ctas = (long long)P.B * P.kv.hkv * 2;
-  const bool split = ctas < 2 * sm_count();
-  const int lpr = split ? 4 : P.kv.d / 8, columns = P.kv.d / 8 / lpr;
-  const Launch at(dim3(P.kv.hkv * 2 * columns, P.B), kMoveThreads, 0, s);
-  switch (lpr) {
-    case 4: return cudaLaunchKernelEx(&at.cfg, move_kernel<4>, P, columns);
-    case 8: return cudaLaunchKernelEx(&at.cfg, move_kernel<8>, P, columns);
-    default: return cudaLaunchKernelEx(&at.cfg, move_kernel<16>, P, columns);
+  if (e != cudaSuccess) return e;
+  // 64-byte columns where whole rows leave SMs idle (see move_kernel)
+  const bool split = (long long)P.B * P.kv.hkv * 2 < 2 * sm_count();
+  const int row = 2 * P.kv.d, columns = split ? row / 64 : 1;
+  const Launch at(dim3(P.kv.hkv * 2 * columns, P.B), 32, kMoveSmem, s);
+  switch (row / columns) {
+    case 64: return cudaLaunchKernelEx(&at.cfg, move_kernel<4>, P, columns);
+    case 128: return cudaLaunchKernelEx(&at.cfg, move_kernel<2>, P, columns);
+    default: return cudaLaunchKernelEx(&at.cfg, move_kernel<1>, P, columns);
   }
 }
 

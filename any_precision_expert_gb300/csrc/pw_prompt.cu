@@ -1,13 +1,14 @@
 // Causal attention of packed prompts over their own keys: tcgen05 products.
 //
-// Row r of a sequence and key head is query token r / G, head r % G of the
-// group, so the G heads that share keys lie side by side and a tile of 256 rows
-// ends within 256 / G keys of its diagonal.  A CTA takes 256 rows (two 128-row
-// tiles) past the 128-key tiles that they see, as attend_tc_kernel does
-// (pw_attend_tc.cu, which explains the parts): S = Q K^T and O += P V with
-// accumulators in tensor memory, P in the place of S, a softmax warpgroup and
-// an MMA warp a row tile.  Nothing is split: a row's keys stay in one CTA, and
-// its sums are divided and rounded on their way out.
+// The G heads that share keys lie side by side: row r of a row tile is token r /
+// G, head r % G, and a row tile holds the floor(128 / G) whole tokens that fit
+// its 128 rows, so that one tensor copy brings its queries and it ends within
+// 128 / G keys of its diagonal.  A CTA takes two row tiles past the 128-key
+// tiles that they see, as attend_tc_kernel does (pw_attend_tc.cu, which explains
+// the parts): S = Q K^T and O += P V with accumulators in tensor memory, P in
+// the place of S, a softmax warpgroup and an MMA warp a row tile.  Nothing is
+// split: a row's keys stay in one CTA, and its sums are divided and rounded on
+// their way out.
 //
 // Work grows with a tile's place in its sequence, so the CTAs take the tiles by
 // falling place (a counting sort over the sequences' lengths, which every CTA
@@ -24,14 +25,20 @@ namespace pw {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile
-constexpr int kRows = 256;           // rows a CTA has at a time
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
-// Registers: launched with 168 a thread; the softmax warps take what the other four give up (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kParts = 2;            // a tile's weights are handed over in halves
+// Registers: launched with 168 a thread; the softmax warps take what the other four give up (256 * 216 + 128 * 72 = 384 * 168;
+// with 208 and 88 a document of 8191 tokens takes 390 us instead of 385).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// Parts in which a tile's weights are handed over: with 1 / 2 / 4 the document takes 385 / 401 / 450 us, 24 prompts 157 / 167 / 187.
+constexpr int kParts = 1;
 constexpr float kGrow = 8.f;         // sums are rescaled when a row's maximum has grown by 2^kGrow
 constexpr int kBuckets = 512;
+// The softmax of heads of 128 meets the other row tile's products if the warpgroups take turns; with heads of 64, whose
+// products are half as long, the two do better side by side (24 prompts of up to 1111 tokens 180 -> 157 us; a document with
+// heads of 128 and no turns 479 us, with turns 401).
+template <int D>
+constexpr bool kTurns = D == 128;
 
 template <int D>
 struct Cfg {
@@ -41,17 +48,18 @@ struct Cfg {
   static constexpr int Q_AT = 0;                           // two row tiles
   static constexpr int RING_AT = 2 * SLOT;
   static constexpr int SORT = (3 * kBuckets + 4) * 4;
-  static constexpr int FIT = (226 * 1024 - RING_AT - SORT - 1024) / SLOT;
-  static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+  static constexpr int FIT = (226 * 1024 - RING_AT - SORT - 1024 - kSoftmaxWarps * 2048) / SLOT;
+  static constexpr int SLOTS = FIT < 8 ? FIT / 2 * 2 : 8;  // even: keys, then values
   static constexpr int BAR_AT = RING_AT + SLOTS * SLOT;
   static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 192;
   static constexpr int SORT_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
-  static constexpr int SMEM = SORT_AT + SORT;
+  static constexpr int STAGE_AT = (SORT_AT + SORT + 127) / 128 * 128;  // 32 rows of 32 values a softmax warp, on their way out
+  static constexpr int SMEM = STAGE_AT + kSoftmaxWarps * 2048;
   static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
 };
 
 struct PromptMaps {
-  CUtensorMap k, v;
+  CUtensorMap q, k, v;
 };
 
 __device__ int prompt_err;  // the error word of calls without one
@@ -66,7 +74,11 @@ __device__ __forceinline__ Span span_of(const PromptParams& P, int b, int* err) 
   if (err && (l != lo || h != hi)) atomicExch(err, kErrOffsets);
   return {l, h - l};
 }
-__device__ __forceinline__ int row_tiles(const PromptParams& P, int n) { return (int)(((long long)n * P.G + kRows - 1) / kRows); }
+// Tokens of a row tile, and a sequence's tiles of two of them.
+__host__ __device__ __forceinline__ int tile_tokens(const PromptParams& P) { return 128 / P.G; }
+__host__ __device__ __forceinline__ int row_tiles(const PromptParams& P, int n) {
+  return (n + 2 * tile_tokens(P) - 1) / (2 * tile_tokens(P));
+}
 
 // Row tiles in falling order of their place in the sequence.  Places are sorted into buckets of 2^shift.
 struct PromptWalk {
@@ -153,12 +165,13 @@ struct PromptWalk {
         const int at = __ffs(hit) - 1;
         const int tile = first + want - before - __shfl_sync(0xffffffffu, scan - mine, at);
         p.tok0 = __shfl_sync(0xffffffffu, s.lo, at);
-        p.nrows = __shfl_sync(0xffffffffu, s.n, at) * P.G;
+        p.nrows = __shfl_sync(0xffffffffu, s.n, at);         // tokens here
         p.head = rank - unit * P.hkv;
-        p.row0 = tile * kRows;
+        const int tokens = tile_tokens(P);
+        p.row0 = tile * 2 * tokens;                          // the first row tile's first token
         // the keys that each of the two row tiles sees, in tiles
-        p.tile0 = min(p.row0 + 127, p.nrows - 1) / P.G / kTile + 1;
-        p.len = min(p.row0 + 255, p.nrows - 1) / P.G + 1;
+        p.tile0 = (min(p.row0 + tokens, p.nrows) + kTile - 1) / kTile;
+        p.len = min(p.row0 + 2 * tokens, p.nrows);
         p.tile1 = (p.len + kTile - 1) / kTile;
         return true;
       }
@@ -168,9 +181,11 @@ struct PromptWalk {
   }
 };
 
-__device__ __forceinline__ bool active(const Piece& pc, int i) { return i == 0 || pc.row0 + 128 < pc.nrows; }
+__device__ __forceinline__ bool active(const Piece& pc, int i, int tokens) { return i == 0 || pc.row0 + tokens < pc.nrows; }
 // Key tiles of row tile i.
-__device__ __forceinline__ int tiles_of(const Piece& pc, int i) { return i == 0 ? pc.tile0 : active(pc, 1) ? pc.tile1 : 0; }
+__device__ __forceinline__ int tiles_of(const Piece& pc, int i, int tokens) {
+  return i == 0 ? pc.tile0 : active(pc, 1, tokens) ? pc.tile1 : 0;
+}
 
 // The key tiles of a CTA's pieces as one sequence.
 struct Tiles {
@@ -188,9 +203,10 @@ struct Tiles {
 // before QK(n + 1), whose scores take the place of the weights.
 template <typename E, int D, int I>
 __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t full, uint32_t empty, uint32_t bars,
-                                         uint32_t tmem, volatile int* abort_flag, int* err) {
+                                         uint32_t clean, uint32_t tmem, int tokens, bool negative, volatile int* abort_flag, int* err) {
   using C = Cfg<D>;
-  constexpr uint32_t id_qk = idesc_of<E>(kTile, false), id_pv = idesc_of<E>(D, true);
+  const uint32_t id_qk = idesc_of<E>(kTile, false) | (negative ? 1u << 13 : 0u);  // -Q K^T
+  constexpr uint32_t id_pv = idesc_of<E>(D, true);
   const uint32_t q_full = bars + 8 * I, s_full = bars + 16 + 8 * I, o_done = bars + 32 + 8 * I,
                  p_full = bars + 64 + 8 * kParts * I;
   const uint32_t ts = tmem + C::S_COL + I * 128, to = tmem + C::O_COL + I * 128;
@@ -209,14 +225,14 @@ __device__ __forceinline__ void mma_role(PieceRing ring, uint32_t base, uint32_t
   unsigned vs = 0, vp = 0;     // the current tile's values
   bool run = false;            // a tile is waiting for its weights
   while (have || run) {
-    const bool k_act = have && it.t < tiles_of(it.pc, I), k_last = k_act && it.t + 1 == tiles_of(it.pc, I);
+    const bool k_act = have && it.t < tiles_of(it.pc, I, tokens), k_last = k_act && it.t + 1 == tiles_of(it.pc, I, tokens);
     const unsigned ks = slot, kp = par;
     if (have) {
       if (++slot == C::SLOTS) slot = 0, par ^= 1;
       if (!wait(full + 8 * ks, kp)) return;   // also of keys that this tile has no use for: an arrival belongs to their phase
     }
     if (run) {
-      if (!wait(full + 8 * vs, vp)) return;
+      if (!wait(clean + 8 * vs, vp)) return;
       if (act) {  // O (+)= P V
         const uint32_t v_lo = (uint32_t)v0 + vs * (C::SLOT >> 4);
 #pragma unroll
@@ -291,11 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::SLOTS, bars = empty + 8 * C::SLOTS + 16 * kPieces;
   const uint32_t q_full = bars, s_full = bars + 16, o_done = bars + 32, turn = bars + 48, p_full = bars + 64;  // p_full: [row tile][part]
+  const uint32_t clean = p_full + 16 * kParts;  // [ring slot], of values: looked through
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 16);
   volatile int* odd_seen = reinterpret_cast<volatile int*>(smem + C::PIECE_AT - 12);  // values that are no numbers were taken out
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::PIECE_AT - 8);
   int* err = P.err ? P.err : &prompt_err;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tokens = tile_tokens(P);
   if (base & 1023) {
     if (tid == 0) atomicExch(err, kErrLayout);
     return;
@@ -308,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
   ring.err = err;
   {
     // the barriers lie side by side, one thread each: ring slots (full, empty), pieces (full, empty), then by row tile
-    // queries, scores, sums, turns and the parts of the weights
-    constexpr int kNear = 2 * C::SLOTS + 2 * kPieces, kAll = kNear + 8 + 2 * kParts;
+    // queries, scores, sums, turns and the parts of the weights, then by slot values looked through
+    constexpr int kNear = 2 * C::SLOTS + 2 * kPieces, kAll = kNear + 8 + 2 * kParts + C::SLOTS;
     if (tid < kAll) {
       const int k = tid - kNear;
       const int count = tid < C::SLOTS ? 1 : tid < 2 * C::SLOTS ? 2 : tid < 2 * C::SLOTS + kPieces ? 1
-                        : k < 0 ? kSoftmaxWarps + 2 : k < 2 ? 128 : k < 6 ? 1 : 128;
+                        : k < 0 ? kSoftmaxWarps + 3 : k < 6 ? 1 : k < 8 + 2 * kParts ? 128 : 1;
       mbar_init(full + 8 * tid, count);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -341,74 +358,57 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
     const int i = warp >> 2, w4 = warp & 3, r = tid & 127;
     const uint32_t lanes = (uint32_t)w4 << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + C::S_COL + i * 128, to = tmem + lanes + C::O_COL + i * 128;
-    const bool plain_q = P.scale > 0.f;  // a negative scale turns the queries around, a scale of 0 takes them away
-    const float scale2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
+    // a negative scale turns the products around; for one of 0 a number that leaves -infinity what it is
+    const float scale2 = P.scale == 0.f ? 1.17549435e-38f : fabsf(P.scale) * 1.4426950408889634f;
     Piece pc = {};
-    // Queries: a warp brings its 32 rows, whole lines at a time.
-    constexpr int LPR = D / 8, RPS = 32 / LPR, STEPS = 32 / RPS;  // lanes a row, rows a step, steps
-    const int q_row = 32 * w4, q_sub = lane / LPR, q_col = lane % LPR;
-    const uint32_t q_base = base + C::Q_AT + i * C::SLOT;
-    // The lane's rows, RPS apart: f(k, source or null past the rows).
-    auto each_row = [&](auto f) {
-      const int row0 = pc.row0 + 128 * i + q_row + q_sub, tok = row0 / P.G;
-      int hd = row0 - tok * P.G, left = pc.nrows - row0;
-      const E* src = static_cast<const E*>(P.q.ptr) + (pc.tok0 + tok) * P.q.token_stride +
-                     (pc.head * P.G + hd) * P.q.head_stride + 8 * q_col;
-      const long long turn_over = P.q.token_stride - P.G * P.q.head_stride;
-#pragma unroll 4
-      for (int k = 0; k < STEPS; ++k) {
-        f(k, left > 0 ? src : nullptr);
-        left -= RPS;
-        hd += RPS;
-        src += RPS * P.q.head_stride;
-        while (hd >= P.G) hd -= P.G, src += turn_over;
+    // Queries: a box of whole tokens, called by one thread once the last product with the ones before is done.
+    auto call_q = [&]() {
+      if (r == 0) {
+        mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(tokens * P.G * D * 2));
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h)
+          tma_load_3d(base + C::Q_AT + i * C::SLOT + h * C::HALF, &maps.q, 64 * h, pc.head * P.G, pc.tok0 + pc.row0 + i * tokens,
+                      q_full + 8 * i);
       }
     };
-    auto place_q = [&]() {
-      each_row([&](int k, const E* src) {
-        const int at = q_row + k * RPS + q_sub;
-        const uint32_t dst = q_base + (q_col / 8) * C::HALF + at * 128 + (((q_col & 7) ^ (at & 7)) << 4);
-        if (src && plain_q) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        } else {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (src && P.scale < 0.f) {
-            v = *reinterpret_cast<const uint4*>(src);
-            v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
-          }
-          sts128(dst, v);
-        }
-      });
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(q_full + 8 * i);
-    };
+    // A row's token in the tile and head of its group; rows past the whole tokens are nobody's.
+    const int row_tok = r / P.G, row_head = r - row_tok * P.G;
+    // The rows that this lane stores: 8 k + lane / 4 of the warp's 32.
+    int out_tok[4], out_head[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = 32 * w4 + 8 * k + lane / 4;
+      out_tok[k] = x / P.G;
+      out_head[k] = x - out_tok[k] * P.G;
+    }
+    const uint32_t stage = base + C::STAGE_AT + warp * 2048;
     unsigned n = 0;     // tiles of this row tile so far
     unsigned flat = 0;  // tiles of the CTA before the current piece
     unsigned turns = 0, done = 0;  // turns taken, pieces finished
     bool ok = true;
     auto advance = [&]() {  // to the next piece with rows of this tile
       while (ring.take(pc)) {
-        if (active(pc, i)) return true;
+        if (active(pc, i, tokens)) return true;
         flat += pc.tile1;
       }
       return false;
     };
     bool have = advance();
-    if (have) place_q();
+    if (have) call_q();
     while (have && ok) {
       const Piece cur = pc;
-      const int row = cur.row0 + 128 * i + r;
-      const int tok = min(row, cur.nrows - 1) / P.G;
+      const int first = cur.row0 + i * tokens;        // the row tile's first token
+      const int tok = min(first + row_tok, cur.nrows - 1);
       const int vis = tok + 1;                        // keys this row sees
-      const int sure0 = cur.row0 / P.G + 1;           // keys that every row of the piece sees
-      const int sure = (cur.row0 + 128 * i) / P.G + 1;  // ... of the row tile
-      const int tiles = tiles_of(cur, i);
-      const bool two = active(cur, 1);
+      const int sure0 = cur.row0 + 1;                 // keys that every row of the piece sees
+      const int sure = first + 1;                     // ... of the row tile
+      const int tiles = tiles_of(cur, i, tokens);
+      const bool two = active(cur, 1, tokens);
+      bool odd = false;
       float m = -CUDART_INF_F;
       float2 l = make_float2(0.f, 0.f);
       for (int t = 0; t < tiles; ++t, ++n) {
-        const bool both = two && t < cur.tile0;
+        const bool both = kTurns<D> && two && t < cur.tile0;
         ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * i, n & 1, abort_flag, err));
         if (!ok) break;
         tc_fence_after();
@@ -420,25 +420,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
           ++turns;
         }
         const int see = vis - t * kTile;
-        float top = -CUDART_INF_F;
         if ((t + 1) * kTile > sure) {
           // what a row does not see counts as -infinity: a weight of 0
 #pragma unroll
-          for (int k = 0; k < 128; ++k) {
+          for (int k = 0; k < 128; ++k)
             if (k >= see) s[k] = 0xff800000u;
-            top = fmaxf(top, __uint_as_float(s[k]));
-          }
-        } else {
-          float t1 = -CUDART_INF_F, t2 = t1, t3 = t1;
-#pragma unroll
-          for (int k = 0; k < 128; k += 8) {
-            top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-            t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-            t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
-            t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
-          }
-          top = fmaxf(max3(top, t1, t2), t3);
         }
+        float top = -CUDART_INF_F, t1 = top, t2 = top, t3 = top;
+#pragma unroll
+        for (int k = 0; k < 128; k += 8) {
+          top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+          t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+          t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+          t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+        }
+        top = fmaxf(max3(top, t1, t2), t3);
         top = top == -CUDART_INF_F ? top : top * scale2 - kShift;
         if (t == 0) {
           m = top;
@@ -458,32 +454,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         }
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
-        if (i == (t < cur.tile0 ? 0 : 1) && (t + 1) * kTile > sure0) {
-          // values at keys that no row of the piece sees may be anything: 0 instead (one key a thread; the other row
-          // tile's turn comes after this); so for those that are no numbers and that some rows do not see, which the
-          // others get at the end
+        if (t + 1 == tiles) {
+          // The last S is out of the queries' way: the next piece's are called in.  Whether values that are no numbers were
+          // taken out of this piece's is known once its last ones have been looked through.
           const unsigned slot = 2 * (flat + t) + 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
+          flat += cur.tile1;
+          have = advance();
+          if (have) call_q();
+          ok = __all_sync(0xffffffffu, mbar_wait(clean + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
           if (!ok) break;
-          const uint32_t at = base + C::RING_AT + (slot % C::SLOTS) * C::SLOT + r * 128;
-          const int key = t * kTile + r;
-          if (key >= sure0) {
-#pragma unroll 1
-            for (int c = 0; c < 8 * C::NH; ++c) {
-              const uint32_t to = at + (c >> 3) * C::HALF + 16 * ((c ^ r) & 7);
-              if (key >= cur.len) {
-                sts128(to, make_uint4(0, 0, 0, 0));
-                continue;
-              }
-              const uint4 v = shared16(to);
-              if (!all_finite<E>(v)) {
-                sts128(to, make_uint4(v.x & finite_bits<E>(v.x), v.y & finite_bits<E>(v.y), v.z & finite_bits<E>(v.z),
-                                      v.w & finite_bits<E>(v.w)));
-                *odd_seen = 1;
-              }
-            }
-          }
-          fence_proxy_async_smem();
+          odd = *odd_seen;
         }
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
@@ -506,37 +486,46 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         }
       }
       if (!ok) break;
-      flat += cur.tile1;
-      // the last S is out of the queries' way: the next piece's go in before this one's sums come out
-      have = advance();
-      if (have) place_q();
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
-      // the wait is over already: it makes what any thread of the row tile has seen known here, and what the first one's
-      // have was known at the turns
-      const bool odd = mbar_wait(p_full + 8 * (kParts * i + kParts - 1), (n - 1) & 1, abort_flag, err) && *odd_seen;
-      const bool in = row < cur.nrows;
-      const long long at = cur.tok0 + tok;
-      const int head = cur.head * P.G + min(row, cur.nrows - 1) - tok * P.G;
-      const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (in && P.lse) P.lse[at * P.hq + head] = sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.6931471805599453f;
-      E* out = static_cast<E*>(P.out.ptr) + at * P.out.token_stride + head * P.out.head_stride;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_load32(to + c, o);
-        if (odd && in) add_odd<E>(P, cur, sure0, vis, c, o);
-        if (in) {
+      const bool in = row_tok < tokens && first + row_tok < cur.nrows;
+      const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+      // 32 values a row at a time through shared memory, so that four lanes store 64 bytes of a row
+      const int rest = min(tokens, cur.nrows - first);  // whole tokens of this sequence
+      E* out = static_cast<E*>(P.out.ptr) + (long long)(cur.tok0 + first) * P.out.token_stride + cur.head * P.G * P.out.head_stride +
+               8 * (lane & 3);
+      E* row[4];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
+      for (int k = 0; k < 4; ++k) row[k] = out + out_tok[k] * P.out.token_stride + out_head[k] * P.out.head_stride;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t all[2][32];
+        tmem_load64(to + c0, all[0], all[1]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t (&o)[32] = all[b];
+          if (odd && in) add_odd<E>(P, cur, sure0, vis, c0 + 32 * b, o);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(o[k + j]) * inv;
-            *reinterpret_cast<uint4*>(out + c + k) = pack8<E>(x);
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(o[8 * k + j]) * inv;
+            sts128(stage + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4), pack8<E>(x));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int x = 8 * k + lane / 4;
+            const uint4 v = shared16(stage + x * 64 + (((lane & 3) ^ (x >> 1 & 3)) << 4));
+            if (out_tok[k] < rest) *reinterpret_cast<uint4*>(row[k] + c0 + 32 * b) = v;
           }
         }
       }
+      if (in && P.lse)
+        P.lse[(long long)(cur.tok0 + tok) * P.hq + cur.head * P.G + row_head] =
+            sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.6931471805599453f;
       tc_fence_before();
     }
   } else {
@@ -547,12 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
       __syncwarp();
       walk.begin();
       unsigned x = 0;  // slots filled so far
-      bool ok = true;
-      Piece pc = {};
-      while (ok) {
-        const bool more = walk.next(P, pc, lane);
-        ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
-        if (!more) break;
+      // pieces are announced before the loads of the one in front of them
+      Piece pc = {}, ahead = {};
+      bool more = walk.next(P, ahead, lane);
+      bool ok = __all_sync(0xffffffffu, lane != 0 || ring.put(ahead));
+      while (ok && more) {
+        pc = ahead;
+        more = walk.next(P, ahead, lane);
+        ok = __all_sync(0xffffffffu, lane != 0 || ring.put(ahead));
         for (int t = 0; ok && t < pc.tile1; ++t) {
           for (int v = 0; v < 2; ++v, ++x) {
             const unsigned slot = x % C::SLOTS, round = x / C::SLOTS;
@@ -561,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
             if (lane == 0) mbar_arrive_expect_tx(full + 8 * slot, C::SLOT);
             __syncwarp();
             if (lane < C::NH)
-              tma_load_3d(base + C::RING_AT + slot * C::SLOT + lane * C::HALF, v ? &maps.v : &maps.k, 64 * lane,
-                          pc.tok0 + t * kTile, pc.head, full + 8 * slot);
+              tma_load_3d(base + C::RING_AT + slot * C::SLOT + lane * C::HALF, v ? &maps.v : &maps.k, 64 * lane, pc.head,
+                          pc.tok0 + t * kTile, full + 8 * slot);
             __syncwarp();
           }
         }
@@ -574,9 +565,52 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         }
       }
     } else if (warp == kSoftmaxWarps + 1) {
-      mma_role<E, D, 0>(ring, base, full, empty, bars, tmem, abort_flag, err);
+      mma_role<E, D, 0>(ring, base, full, empty, bars, clean, tmem, tokens, P.scale < 0.f, abort_flag, err);
     } else if (warp == kSoftmaxWarps + 2) {
-      mma_role<E, D, 1>(ring, base, full, empty, bars, tmem, abort_flag, err);
+      mma_role<E, D, 1>(ring, base, full, empty, bars, clean, tmem, tokens, P.scale < 0.f, abort_flag, err);
+    } else {
+      // ---- values are looked through on their way to the products: those at keys that no row of the piece sees may be
+      // anything, and those that are no numbers, at keys that only some rows see, come back to these rows at the end ----
+      unsigned slot = 1, par = 0;
+      Tiles it;
+      it.pc.tile1 = 0;
+      while (it.next(ring)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * slot, par, abort_flag, err))) break;
+        const int sure = it.pc.row0 + 1, key0 = it.t * kTile;
+        const uint32_t at = base + C::RING_AT + slot * C::SLOT;
+        const int c0 = max(sure - key0, 0) * 8 * C::NH + lane, c1 = kTile * 8 * C::NH;  // 16 bytes each
+        auto place = [&](int c) { return at + (c / 8 % C::NH) * C::HALF + c / (8 * C::NH) * 128 + 16 * (c & 7); };
+        // 0 times a value adds up to what is no number as soon as one is none
+        using V = typename Pair<E>::V;
+        uint32_t sum[4] = {0, 0, 0, 0};
+        const uint32_t zero = 0;
+        auto add = [&](uint32_t& to, uint32_t x) {
+          const V y = __hfma2(*reinterpret_cast<const V*>(&x), *reinterpret_cast<const V*>(&zero), *reinterpret_cast<const V*>(&to));
+          to = *reinterpret_cast<const uint32_t*>(&y);
+        };
+#pragma unroll 8
+        for (int c = c0; c < c1; c += 32) {
+          const uint4 v = shared16(place(c));
+          add(sum[0], v.x), add(sum[1], v.y), add(sum[2], v.z), add(sum[3], v.w);
+        }
+        if (!all_finite<E>(make_uint4(sum[0], sum[1], sum[2], sum[3]))) {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 32) {
+            const uint4 v = shared16(place(c));
+            if (all_finite<E>(v)) continue;
+            const bool seen = key0 + c / (8 * C::NH) < it.pc.len;
+            sts128(place(c), seen ? make_uint4(v.x & finite_bits<E>(v.x), v.y & finite_bits<E>(v.y), v.z & finite_bits<E>(v.z),
+                                               v.w & finite_bits<E>(v.w))
+                                  : make_uint4(0, 0, 0, 0));
+            if (seen) *odd_seen = 1;
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(clean + 8 * slot);
+        slot += 2;
+        if (slot > C::SLOTS) slot = 1, par ^= 1;
+      }
     }
   }
   // ---- teardown: every MMA has completed or the wait for it has run out ----
@@ -595,16 +629,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
   }
 }
 
-cudaError_t encode(const pw_rows& r, int T, int heads, int dtype, int d, CUtensorMap* map) {
+// Boxes of 64 values x `heads_in` heads x `tokens_in` tokens, a row tile's queries, or of kTile tokens of one head.
+cudaError_t encode(const pw_rows& r, int T, int heads, int dtype, int d, int heads_in, int tokens_in, CUtensorMap* map) {
   using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                    const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   const auto enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
   if (!enc) return cudaErrorNotSupported;
   // the stride of a dimension of one does not matter to the caller, but has to be a stride
-  const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads};
-  const cuuint64_t stride[2] = {(cuuint64_t)(T > 1 ? r.token_stride : d) * 2, (cuuint64_t)(heads > 1 ? r.head_stride : d) * 2};
-  const cuuint32_t box[3] = {64, kTile, 1}, step[3] = {1, 1, 1};
+  const cuuint64_t dim[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t stride[2] = {(cuuint64_t)(heads > 1 ? r.head_stride : d) * 2, (cuuint64_t)(T > 1 ? r.token_stride : d) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_in, (cuuint32_t)tokens_in}, step[3] = {1, 1, 1};
   return enc(map, dtype == PW_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.ptr, dim, stride, box,
              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -618,9 +653,9 @@ cudaError_t launch_typed(const PromptParams& P, const PromptMaps& maps, cudaStre
   cudaError_t e = ensure_smem(fn, Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be row tiles
-  const long long most = ((long long)P.T * P.G / kRows + P.B) * P.hkv;
+  const long long most = ((long long)P.T / (2 * tile_tokens(P)) + P.B) * P.hkv;
   int shift = 0;
-  while ((((long long)P.T * P.G + kRows - 1) / kRows >> shift) >= kBuckets) ++shift;
+  while ((row_tiles(P, P.T) >> shift) >= kBuckets) ++shift;
   const Launch at(dim3(most < sm_count() ? (unsigned)most : sm_count()), kThreads, Cfg<D>::SMEM, s);
   return cudaLaunchKernelEx(&at.cfg, prompt_kernel<E, D>, P, shift, maps);
 }
@@ -629,8 +664,9 @@ cudaError_t launch_typed(const PromptParams& P, const PromptMaps& maps, cudaStre
 
 cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s) {
   PromptMaps maps;
-  cudaError_t e = encode(P.k, P.T, P.hkv, dtype, d, &maps.k);
-  if (e == cudaSuccess) e = encode(P.v, P.T, P.hkv, dtype, d, &maps.v);
+  cudaError_t e = encode(P.k, P.T, P.hkv, dtype, d, 1, kTile, &maps.k);
+  if (e == cudaSuccess) e = encode(P.v, P.T, P.hkv, dtype, d, 1, kTile, &maps.v);
+  if (e == cudaSuccess) e = encode(P.q, P.T, P.hq, dtype, d, P.G, tile_tokens(P), &maps.q);
   if (e != cudaSuccess) return e;
   if (dtype == PW_F16) return d == 128 ? launch_typed<__half, 128>(P, maps, s) : launch_typed<__half, 64>(P, maps, s);
   return d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, s) : launch_typed<__nv_bfloat16, 64>(P, maps, s);

@@ -110,7 +110,7 @@ struct EvictParams {
   int* new_lens;
   float* new_mass;
   int* kept;
-  int* ws_kept;         // [B][budget] tokens that stay
+  int2* ws_moves;       // [B][budget] slots of the tokens that stay, old and new (-1: none, or there already)
   float* ws_mass;       // their masses
   int* ws_left;         // [B]
 };

@@ -723,7 +723,7 @@ pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int
  *   offsets  device int32 [batch + 1], not descending, in [0, T]; others are
  *            clamped to that and flagged (descending ones that put a row into
  *            two sequences leave its results unspecified)
- *   k, v     strides of at least a row where there is more than one row along
+ *   q, k, v  strides of at least a row where there is more than one row along
  *            them (PW_ERR_INVALID_ARG otherwise)
  *   err      device int32 or NULL: the call's error word
  * Rows in front of the first sequence, behind the last and between two are left as they

@@ -39,7 +39,7 @@ def prompt(heads=(0, 8, 2, 128), **kw):
 @pytest.mark.parametrize("want,kw", [
     (UNSUPPORTED, {}), (UNSUPPORTED, dict(lse=None, err=None)), (UNSUPPORTED, dict(tokens=0, q=Rows(), offsets=None)),
     (UNSUPPORTED, dict(batch=0, offsets=None)), (UNSUPPORTED, dict(k=Rows(P, 128, 0), heads=(0, 8, 1, 128))),
-    (UNSUPPORTED, dict(tokens=1, k=Rows(P, 0, 128))), (UNSUPPORTED, dict(q=Rows(P, 0, 128))),
+    (UNSUPPORTED, dict(tokens=1, k=Rows(P, 0, 128))), (UNSUPPORTED, dict(out=Rows(P, 2048, -128))), (INVALID, dict(q=Rows(P, 0, 128))),
     (INVALID, dict(tokens=-1)), (INVALID, dict(tokens=(1 << 20) + 1)), (INVALID, dict(batch=-1)), (UNSUPPORTED, dict(batch=4097)),
     (INVALID, dict(heads=(2, 8, 2, 128))), (UNSUPPORTED, dict(heads=(0, 8, 2, 96))), (UNSUPPORTED, dict(heads=(0, 258, 2, 128))),
     (INVALID, dict(heads=(0, 8, 3, 128))), (INVALID, dict(scale=NAN)), (INVALID, dict(scale=INF)), (INVALID, dict(offsets=None)),
