@@ -15,7 +15,6 @@
 #include "pw_attend.cuh"
 #include "pw_heads.cuh"
 #include "pw_mma.cuh"
-#include "pw_tc.cuh"
 
 namespace pw {
 
@@ -221,67 +220,55 @@ cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
 // head's values) by 8 query rows, so that up to eight rows a key head, which is
 // what decode steps have, leave nothing idle and take 32 sums a lane; scores
 // become the second product's operand by transposing 8 x 8 blocks of weights.
-// Bound by the instructions that turn codes into operands, about 250 for 16
-// keys and values (2.5 KB), ahead of the loads: three CTAs an SM then hide what
-// is left of their latency.
+// A warp brings its own keys and values, 32 of a tile, by asynchronous copies
+// of 16 bytes a lane into a ring of its own, one block ahead (tensor copies of
+// small pages cost a producer warp more instructions than this costs all four).
+// Bound by the instructions that turn codes into operands, ahead of the loads.
 
-constexpr int kComputeWarps = 4;
-constexpr int kThreads = (kComputeWarps + 1) * 32;
-constexpr int kTile = 128;                                // keys a stage
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 128;                                // keys a tile
+constexpr int kBlock = 32;                                // of them a warp has at a time
+constexpr float kGrow = 8.f;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int CTAS = NT == 1 ? 3 : 2;            // an SM
-  // eight keys' steps take 128 bytes, where a copy lands, or 64 side by side (heads of 64 on pages of 16 tokens and more)
-  static constexpr int CODES = kTile * (D / 2), STEPS = kTile * 16;
+  static constexpr int CTAS = NT == 1 ? 4 : D == 64 ? 3 : 2;  // an SM
+  static constexpr int CODES = kBlock * (D / 2), STEPS = kBlock * (D / 8);
   static constexpr int K_AT = 0, V_AT = CODES, KS_AT = 2 * CODES, VS_AT = KS_AT + STEPS;
-  static constexpr int STAGE = 2 * (CODES + STEPS);
-  static constexpr int JOIN = 2 * NT * (D / 16) * 512;    // accumulators of two warps
-  static constexpr int REST = JOIN + 2 * NT * 64 + kPieces * (int)sizeof(Piece) + 16 * kPieces + 16 * 16 + 16;
-  static constexpr int FIT = (226 * 1024 / CTAS - 1024 - REST) / STAGE;
-  static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr int JOIN_AT = STAGES * STAGE;
+  static constexpr int STAGE = 2 * (CODES + STEPS);       // of a warp
+  static constexpr int STAGES = 2;
+  static constexpr int JOIN_AT = kWarps * STAGES * STAGE;
+  static constexpr int JOIN = NT * (D / 16) * 512;        // half the accumulators of two warps
   static constexpr int ML_AT = JOIN_AT + JOIN;
-  static constexpr int PIECE_AT = ML_AT + 2 * NT * 64;
-  static constexpr int BAR_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
-  static constexpr int SMEM = BAR_AT + 16 * STAGES + 16 * kPieces + 16;
-  static_assert(STAGES >= 2, "");
+  static constexpr int SMEM = ML_AT + 2 * NT * 64;
 };
 
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory"); }
-__device__ __forceinline__ bool compute_all(bool mine) {
-  uint32_t all;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(all)
-      : "r"((uint32_t)mine), "n"(kComputeWarps * 32)
-      : "memory");
-  return all != 0;
+__device__ __forceinline__ void compute_sync() { __syncthreads(); }
+
+// N bytes of a lane, or zeros.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const char* from, bool live) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(live ? N : 0) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
-  return v;
-}
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
+__device__ __forceinline__ void lds_words(const unsigned char* at, uint32_t (&w)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "");
   if constexpr (N == 4) {
-    const uint4 v = shared16(at);
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   } else if constexpr (N == 2) {
-    const uint2 v = lds64(at);
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
     w[0] = v.x, w[1] = v.y;
   } else {
-    w[0] = lds32(at);
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
   }
 }
+__device__ __forceinline__ uint32_t lds32(const unsigned char* at) { return *reinterpret_cast<const uint32_t*>(at); }
 
 // Rows and columns of an 8 x 8 block of 16-bit values exchanged (a row a group of four lanes).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -290,17 +277,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t more) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(more));
+  return d;
+}
+
 // The code pair at bits 4 n and 4 n + 16 of w as numbers, times step, plus least, rounded once.
 template <typename E>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, int n, uint32_t step2, uint32_t least2) {
   if constexpr (__is_same(E, __half)) {
-    const uint32_t bits = ((n & 2 ? w >> 8 : w) & (n & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;  // 1024 + c (or 16 c)
+    const uint32_t bits = and_or(n & 2 ? w >> 8 : w, n & 1 ? 0x00f000f0u : 0x000f000fu, 0x64006400u);  // 1024 + c (or 16 c)
     __half2 c = *reinterpret_cast<const __half2*>(&bits);
     c = n & 1 ? __hfma2(c, __float2half2_rn(0.0625f), __float2half2_rn(-64.f)) : __hadd2(c, __float2half2_rn(-1024.f));
     const __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&step2), *reinterpret_cast<const __half2*>(&least2));
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
-    const uint32_t bits = ((w >> 4 * n) & 0x000f000fu) | 0x43004300u;  // 128 + c
+    const uint32_t bits = and_or(w >> 4 * n, 0x000f000fu, 0x43004300u);  // 128 + c
     __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&bits);
     c = __hadd2(c, __float2bfloat162_rn(-128.f));
     const __nv_bfloat162 r =
@@ -309,94 +302,84 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, int n, uint32_t step2
   }
 }
 
-// Bytes of eight keys' steps in a stage.
-template <int D>
-__device__ __forceinline__ int step_group(int page_shift) {
-  return D == 128 || page_shift == 3 ? 128 : 64;
-}
-
 // NT row tiles of 8 a warp, MT such sets of rows; KS warps share the keys of a set.
 template <typename E, int D, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
-    attend4_kernel(const AttendParams P, const AttendWork W, const __grid_constant__ Kv4Maps maps) {
+    attend4_kernel(const AttendParams P, const Kv4View kv, const AttendWork W) {
   using C = Cfg<D, NT>;
-  constexpr int SET = 8 * NT, ROWS = SET * MT, KS = kComputeWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64, MV = D / 16;
-  using Walk = AttendWalk<ROWS, kTile, 1, 1, 1>;
+  constexpr int SET = 8 * NT, ROWS = SET * MT, KS = kWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64, MV = D / 16;
+  using Walk = AttendWalk<ROWS, kTile, 1, 1, 2>;  // with 1 / 2 / 3 / 5 tiles a CTA at least, one sequence of 19327 tokens 17.7 / 16.4 / 16.3 / 18.1 us
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-  const uint32_t full = base + C::BAR_AT, empty = full + 8 * C::STAGES;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_AT + 16 * C::STAGES + 16 * kPieces);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (base & 127) {
-    if (tid == 0) atomicExch(P.kv.err, kErrLayout);
-    return;
-  }
   behind_the_stream();
   const typename Walk::Mine mine = Walk::mine(P, W);
-  PieceRing ring;
-  ring.full = empty + 8 * C::STAGES;
-  ring.empty = ring.full + 8 * kPieces;
-  ring.at = reinterpret_cast<Piece*>(smem + C::PIECE_AT);
-  ring.abort_flag = abort_flag;
-  ring.err = P.kv.err;
-  if (tid < 2 * (C::STAGES + kPieces)) {
-    const bool one = tid < C::STAGES || (tid >= 2 * C::STAGES && tid < 2 * C::STAGES + kPieces);
-    mbar_init(full + 8 * tid, one ? 1 : kComputeWarps);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (tid == 0) *abort_flag = 0;
   Walk walk;
   walk.start(P, W, mine, reinterpret_cast<unsigned*>(smem + C::JOIN_AT));
-  Piece pc;
-  int stage = 0, phase = 0;
+  const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
 
-  if (warp == kComputeWarps) {
-    // ---- producer: one lane a box ----
-    const int shift = P.kv.page_shift, box = min(1 << shift, kBoxTokens), group = step_group<D>(shift);
-    const int* table;
-    bool ok = true;
-    uint64_t once;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    while (ok) {
-      const bool more = walk.next(P, pc, table);
-      ok = __all_sync(0xffffffffu, lane != 0 || ring.put(pc));
-      if (!more) break;
-      for (int t = pc.tile0; ok && t < pc.tile1; ++t) {
-        const int kt = key_tile<kTile>(pc, t), keys = min(kTile, pc.len - kt * kTile), boxes = (keys + box - 1) / box;
-        const int at = kt * kTile + lane * box;
-        int page = 0;
-        if (lane < boxes) {
-          page = table[at >> shift];
-          if (page < 0 || page >= P.kv.n_pages) atomicExch(P.kv.err, kErrPage);  // reads as zeros
+  // ---- the warp's blocks of 32 keys as one sequence, two ahead of the products: the pages of one, the copies of another.
+  // A page's rows of codes are page_bytes, a head's among them head_bytes from its start; steps take a quarter. ----
+  Walk ahead = walk;
+  Piece lp = {};
+  const int* table = nullptr;
+  const int shift = P.kv.page_shift, mask = (1 << shift) - 1;
+  const uint32_t page_bytes = (uint32_t)(P.kv.hkv << shift) * (D / 2);
+  uint32_t head_bytes = 0;
+  int lt = 0, lb = KPW, page = -1, first = 0;
+  bool more = true;
+  lp.tile1 = 0;
+  auto look = [&]() {  // finds the next block with keys and reads its pages, a key a lane
+    do {
+      lb += kBlock;
+      if (lb >= KPW) {
+        lb = 0;
+        if (++lt >= lp.tile1) {
+          more = ahead.next(P, lp, table);
+          if (!more) return;
+          lt = lp.tile0;
+          head_bytes = (uint32_t)(lp.head << shift) * (D / 2);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, abort_flag, P.kv.err));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(boxes * box * (D + D / 4)));
-        __syncwarp();
-        if (lane < boxes) {
-          const uint32_t to = base + stage * C::STAGE;
-          const int tok = at & ((1 << shift) - 1), off = lane * box;
-          tma_load_page(to + C::K_AT + off * (D / 2), &maps.k, 0, tok, pc.head, page, full + 8 * stage, once);
-          tma_load_3d(to + C::KS_AT + off / 8 * group, &maps.ks, tok * (D / 32), pc.head, page, full + 8 * stage, once);
-          tma_load_page(to + C::V_AT + off * (D / 2), &maps.v, 0, tok, pc.head, page, full + 8 * stage, once);
-          tma_load_3d(to + C::VS_AT + off / 8 * group, &maps.vs, tok * (D / 32), pc.head, page, full + 8 * stage, once);
-        }
-        __syncwarp();
-        if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      }
+      first = key_tile<kTile>(lp, lt) * kTile + k0 + lb;
+    } while (first >= lp.len);
+    page = -1;
+    if (first + lane < lp.len) {
+      page = table[(first + lane) >> shift];
+      if ((unsigned)page >= (unsigned)P.kv.n_pages) {
+        atomicExch(P.kv.err, kErrPage);  // reads as zeros
+        page = -1;
       }
     }
-    let_next_start();
-    // copies in flight land before the shared memory goes away (after a normal end all have)
-    for (int i = 0; i < C::STAGES; ++i)
-      for (int k = 0; k < (1 << 16) && !mbar_try_wait(full + 8 * i, phase ^ (i < stage ? 0 : 1)); ++k) {
+  };
+  const uint32_t ring = base + warp * C::STAGES * C::STAGE;
+  auto fetch = [&](int stage) {  // the copies of the block found last
+    if (more) {
+      const uint32_t to = ring + stage * C::STAGE;
+      constexpr int PARTS = D / 32;  // 16 bytes of a row's codes each
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        const int r = 32 / PARTS * j + lane / PARTS, pg = __shfl_sync(0xffffffffu, page, r);
+        const uint64_t at = (uint64_t)(uint32_t)max(pg, 0) * page_bytes +
+                            (head_bytes + ((first + r) & mask) * (D / 2) + 16 * (lane % PARTS));
+        copy_async<16>(to + C::K_AT + 512 * j + 16 * lane, kv.k + at, pg >= 0);
+        copy_async<16>(to + C::V_AT + 512 * j + 16 * lane, kv.v + at, pg >= 0);
       }
-    return;
-  }
+      const uint64_t at = (uint64_t)(uint32_t)max(page, 0) * (page_bytes / 4) + (head_bytes / 4 + ((first + lane) & mask) * (D / 8));
+      copy_async<D / 8>(to + C::KS_AT + lane * (D / 8), kv.ks + at, page >= 0);
+      copy_async<D / 8>(to + C::VS_AT + lane * (D / 8), kv.vs + at, page >= 0);
+      look();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  look();
+  fetch(0);
+  int stage = 0;
+  Piece pc;
+  const int* unused;
 
   // ---- compute warps ----
   const int g = lane >> 2, t4 = lane & 3;
-  const int group = step_group<D>(P.kv.page_shift);
-  const int mt = warp % MT, ks = warp / MT, k0 = ks * KPW;
   // Row m of eight keys is key order(m): the rows 2 t (and 2 t + 1) of values, which lanes t read at once, then lie in
   // different banks, and so do the keys that lanes g and g + 1 read.
   auto order = [](int m) { return m ^ (m >> 1 & 1); };
@@ -448,9 +431,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
       qs[j][1] = pack2<E>(c, 0.f);
     }
   };
-  bool have = ring.take(pc);
+  bool have = walk.next(P, pc, unused);
   if (have) load_q();
-  if constexpr (KS > 1) have = compute_all(have);
   while (have) {
     const Piece cur = pc;
     const int ra = cur.row0 + mt * SET + 2 * t4;  // this lane's first row of a tile
@@ -469,38 +451,41 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
     }
 
     for (int t = cur.tile0; t < cur.tile1; ++t) {
-      const bool landed = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, abort_flag, P.kv.err));
       const int tile_first = key_tile<kTile>(cur, t) * kTile + k0;
-      const uint32_t at = base + stage * C::STAGE;
 #pragma unroll 1
-      for (int blk = 0; blk < KPW; blk += 32) {
+      for (int blk = 0; blk < KPW; blk += kBlock) {
         const int first = tile_first + blk;  // this warp's next 32 keys
-        if (!landed || first >= cur.len) break;
-        const int row0 = k0 + blk;           // their rows in the stage
+        if (first >= cur.len) break;
+        fetch(stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const unsigned char* at = smem + warp * C::STAGES * C::STAGE + stage * C::STAGE;
+        stage ^= 1;
         float s[NT][2][4];                   // [row tile][16 keys]: keys order(g), + 8; rows 2 t4, + 1
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int krow = row0 + 16 * h;
+          const int krow = 16 * h;
           uint32_t ka[NG], kb[NG], sa[NG], sb[NG];
           lds_words<NG>(at + C::K_AT + (krow + key_g) * (D / 2) + t4 * (NG * 4), ka);
           lds_words<NG>(at + C::K_AT + (krow + 8 + key_g) * (D / 2) + t4 * (NG * 4), kb);
-          lds_words<NG>(at + C::KS_AT + krow / 8 * group + key_g * (D / 8), sa);
-          lds_words<NG>(at + C::KS_AT + (krow / 8 + 1) * group + key_g * (D / 8), sb);
+          lds_words<NG>(at + C::KS_AT + (krow + key_g) * (D / 8), sa);
+          lds_words<NG>(at + C::KS_AT + (krow + 8 + key_g) * (D / 8), sb);
           float p[NT][4];
 #pragma unroll
           for (int j = 0; j < NT; ++j) p[j][0] = p[j][1] = p[j][2] = p[j][3] = 0.f;
-          uint32_t la = 0, lb = 0;           // least values of the group t4
+          // least values of the group t4
+          const uint32_t la = t4 < NG ? lds32(at + C::KS_AT + (krow + key_g) * (D / 8) + 4 * t4) : 0u;
+          const uint32_t lb = t4 < NG ? lds32(at + C::KS_AT + (krow + 8 + key_g) * (D / 8) + 4 * t4) : 0u;
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
             const uint32_t wa = ka[i], wb = kb[i], wa8 = wa >> 8, wb8 = wb >> 8;
             const uint32_t even[4] = {wa & 0x000f000fu, wb & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu};
             const uint32_t odd[4] = {wa & 0x00f000f0u, wb & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u};
             const float fa = to_f32<E>(sa[i] >> 16), fb = to_f32<E>(sb[i] >> 16);
-            if (i == t4) la = sa[i], lb = sb[i];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              float acc[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<__half>(acc, even, qf[j][2 * i][0], qf[j][2 * i][1]);
+              float acc[4];
+              mma16816_first<__half>(acc, even, qf[j][2 * i][0], qf[j][2 * i][1]);
               mma16816<__half>(acc, odd, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
               p[j][0] = fmaf(fa, acc[0], p[j][0]);
               p[j][1] = fmaf(fa, acc[1], p[j][1]);
@@ -511,8 +496,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
           const uint32_t least[4] = {__byte_perm(la, la, 0x1010), __byte_perm(lb, lb, 0x1010), la & 0xffffu, lb & 0xffffu};
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            s[j][h][0] = s[j][h][1] = s[j][h][2] = s[j][h][3] = 0.f;
-            mma16816<E>(s[j][h], least, qs[j][0], qs[j][1]);
+            mma16816_first<E>(s[j][h], least, qs[j][0], qs[j][1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][h][i] = fmaf(p[j][i], 16777216.f, s[j][h][i]);
           }
@@ -530,20 +514,23 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
               if (edge && first + 16 * h + 8 * (i >> 1) + key_g >= vis[j][i & 1]) s[j][h][i] = -CUDART_INF_F;
               top[i & 1] = fmaxf(top[i & 1], s[j][h][i]);
             }
+          // the sums' reference moves when a lane's maximum has passed it by 2^kGrow (weights stay below 2^(kShift + kGrow),
+          // which fp16 holds, and nothing is lost: it cancels in o / l), and then to the row's maximum
           float ref[2];
           bool grew = false;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], x));
-            top[k] = fmaxf(top[k] - kShift, m[j][k]);
-            ref[k] = top[k] == -CUDART_INF_F ? 0.f : top[k];
-            grew |= top[k] > m[j][k];
+            grew |= top[k] - kShift > m[j][k] + kGrow;
+            ref[k] = m[j][k] == -CUDART_INF_F ? 0.f : m[j][k];
           }
           if (__any_sync(0xffffffffu, grew)) {
             float f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], x));
+              top[k] = fmaxf(top[k] - kShift, m[j][k]);
+              ref[k] = top[k] == -CUDART_INF_F ? 0.f : top[k];
               f[k] = ex2(m[j][k] - ref[k]);
               l[j][k] *= f[k];
               m[j][k] = top[k];
@@ -570,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
           uint32_t vw[4][VW], vs[4];  // keys order(2 t4), order(2 t4 + 1), and those + 8
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int in8 = k & 1 ? val_b : val_a, row = row0 + 16 * h + 8 * (k >> 1) + in8;
+            const int in8 = k & 1 ? val_b : val_a, row = 16 * h + 8 * (k >> 1) + in8;
             lds_words<VW>(at + C::V_AT + row * (D / 2) + value_word<D>(g * VW, in8) * 4, vw[k]);
-            vs[k] = lds32(at + C::VS_AT + (row0 / 8 + 2 * h + (k >> 1)) * group + in8 * (D / 8) + (g * NG / 8) * 4);
+            vs[k] = lds32(at + C::VS_AT + row * (D / 8) + (g * NG / 8) * 4);
             // nothing past the length counts, nor (of what only some rows see) what is no number: those rows get it below
             if (edge) {
               const int key = first + 16 * h + 8 * (k >> 1) + in8;
@@ -600,8 +587,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
 #pragma unroll 1
           for (int key = max(sure, first); key < min(cur.len, first + 32); ++key) {
             // this lane's values of a row lie in one group
-            if (finite_bits<E>(lds32(at + C::VS_AT + (row0 + key - first) / 8 * group + ((key - first) & 7) * (D / 8) +
-                                     (g * NG / 8) * 4)) == 0xffffffffu)
+            if (finite_bits<E>(lds32(at + C::VS_AT + (key - first) * (D / 8) + (g * NG / 8) * 4)) == 0xffffffffu)
               continue;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -613,13 +599,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
                 }
           }
         }
+        __syncwarp();  // the block's place is free
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * stage);
-      if (++stage == C::STAGES) stage = 0, phase ^= 1;
     }
 
-    have = ring.take(pc);
+    have = walk.next(P, pc, unused);
     if (have) load_q();  // on their way while this piece's sums are stored
 
     // ---- join the warps that share keys, in halving steps ----
@@ -631,45 +615,49 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
         for (int x = 4; x < 32; x <<= 1) l[j][k] += __shfl_xor_sync(0xffffffffu, l[j][k], x);
 #pragma unroll
     for (int step = KS / 2; step > 0; step >>= 1) {
-      if (step == KS / 2)
-        have = compute_all(have);
-      else
-        compute_sync();
-      // the buffer is free
-      if (ks >= step && ks < 2 * step) {
+      float fa[NT][2], fb[NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int slot = ((ks - step) * MT + mt) * NT + j;
+      for (int half = 0; half < 2; ++half) {
+        compute_sync();  // the buffer is free
+        if (ks >= step && ks < 2 * step) {
 #pragma unroll
-          for (int i = 0; i < MV; ++i)
-            *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * MV + i) * 512 + lane * 16) =
-                make_float4(o[j][i][0], o[j][i][1], o[j][i][2], o[j][i][3]);
-          if (g == 0) *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 64 + t4 * 16) = make_float4(m[j][0], l[j][0], m[j][1], l[j][1]);
-        }
-      }
-      compute_sync();
-      if (ks < step) {
+          for (int j = 0; j < NT; ++j) {
+            const int slot = ((ks - step) * MT + mt) * NT + j;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int slot = (ks * MT + mt) * NT + j;
-          const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 64 + t4 * 16);
-          const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
-          float fa[2], fb[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float mm = fmaxf(m[j][k], ym[k]), rr = mm == -CUDART_INF_F ? 0.f : mm;
-            fa[k] = ex2(m[j][k] - rr);
-            fb[k] = ex2(ym[k] - rr);
-            l[j][k] = l[j][k] * fa[k] + yl[k] * fb[k];
-            m[j][k] = mm;
+            for (int i = 0; i < MV / 2; ++i) {
+              const float(&v)[4] = o[j][half * (MV / 2) + i];
+              *reinterpret_cast<float4*>(smem + C::JOIN_AT + (slot * (MV / 2) + i) * 512 + lane * 16) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (half == 0 && g == 0)
+              *reinterpret_cast<float4*>(smem + C::ML_AT + slot * 64 + t4 * 16) = make_float4(m[j][0], l[j][0], m[j][1], l[j][1]);
           }
+        }
+        compute_sync();
+        if (ks < step) {
 #pragma unroll
-          for (int i = 0; i < MV; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * MV + i) * 512 + lane * 16);
-            o[j][i][0] = o[j][i][0] * fa[0] + v.x * fb[0];
-            o[j][i][1] = o[j][i][1] * fa[1] + v.y * fb[1];
-            o[j][i][2] = o[j][i][2] * fa[0] + v.z * fb[0];
-            o[j][i][3] = o[j][i][3] * fa[1] + v.w * fb[1];
+          for (int j = 0; j < NT; ++j) {
+            const int slot = (ks * MT + mt) * NT + j;
+            if (half == 0) {
+              const float4 y = *reinterpret_cast<const float4*>(smem + C::ML_AT + slot * 64 + t4 * 16);
+              const float ym[2] = {y.x, y.z}, yl[2] = {y.y, y.w};
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float mm = fmaxf(m[j][k], ym[k]), rr = mm == -CUDART_INF_F ? 0.f : mm;
+                fa[j][k] = ex2(m[j][k] - rr);
+                fb[j][k] = ex2(ym[k] - rr);
+                l[j][k] = l[j][k] * fa[j][k] + yl[k] * fb[j][k];
+                m[j][k] = mm;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < MV / 2; ++i) {
+              const float4 v = *reinterpret_cast<const float4*>(smem + C::JOIN_AT + (slot * (MV / 2) + i) * 512 + lane * 16);
+              float(&x)[4] = o[j][half * (MV / 2) + i];
+              x[0] = x[0] * fa[j][0] + v.x * fb[j][0];
+              x[1] = x[1] * fa[j][1] + v.y * fb[j][1];
+              x[2] = x[2] * fa[j][0] + v.z * fb[j][0];
+              x[3] = x[3] * fa[j][1] + v.w * fb[j][1];
+            }
           }
         }
       }
@@ -701,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
         }
     }
   }
+  let_next_start();
 }
 
 // Rows of a tile: 8 or 16 where a key head has no more, else 32 or 64.
@@ -708,13 +697,15 @@ int attend4_rows(int G, int ql) {
   const long long rows = (long long)G * ql;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
-int attend4_ctas(int rows) { return (rows == 8 ? 3 : 2) * sm_count(); }
+int attend4_ctas(int rows, int d) {
+  return sm_count() * (d == 64 ? rows == 8 ? Cfg<64, 1>::CTAS : Cfg<64, 2>::CTAS : rows == 8 ? Cfg<128, 1>::CTAS : Cfg<128, 2>::CTAS);
+}
 
 struct Layout4 {
   size_t row_o, row_ml, cta_o, cta_ml, total;
   Layout4(const KvView& kv, int B, int ql) {
     const int tile = attend4_rows(kv.hq / kv.hkv, ql);
-    const size_t rows = (size_t)B * ql * kv.hq, slots = (size_t)attend4_ctas(tile) * tile;
+    const size_t rows = (size_t)B * ql * kv.hq, slots = (size_t)attend4_ctas(tile, kv.d) * tile;
     size_t at = 0;
     auto take = [&](size_t n) {
       const size_t was = at;
@@ -730,17 +721,17 @@ struct Layout4 {
 };
 
 template <typename E, int D, int NT, int MT>
-cudaError_t launch_stream(const AttendParams& P, const AttendWork& W, const Kv4Maps& maps, cudaStream_t s) {
+cudaError_t launch_stream(const AttendParams& P, const Kv4View& kv, const AttendWork& W, cudaStream_t s) {
   using C = Cfg<D, NT>;
   const void* fn = reinterpret_cast<const void*>(attend4_kernel<E, D, NT, MT>);
   const cudaError_t e = ensure_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
-  const Launch at(dim3(attend4_ctas(8 * NT * MT)), kThreads, C::SMEM, s);
-  return cudaLaunchKernelEx(&at.cfg, attend4_kernel<E, D, NT, MT>, P, W, maps);
+  const Launch at(dim3(attend4_ctas(8 * NT * MT, D)), kThreads, C::SMEM, s);
+  return cudaLaunchKernelEx(&at.cfg, attend4_kernel<E, D, NT, MT>, P, kv, W);
 }
 
 template <typename E, int D>
-cudaError_t launch_typed(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s) {
+cudaError_t launch_typed(const AttendParams& P, const Kv4View& kv, void* ws, cudaStream_t s) {
   const Layout4 L(P.kv, P.B, P.ql);
   char* w = static_cast<char*>(ws);
   AttendWork W = {};
@@ -752,15 +743,15 @@ cudaError_t launch_typed(const AttendParams& P, const Kv4Maps& maps, void* ws, c
   W.suffix.cta_o = reinterpret_cast<float*>(w + L.cta_o);
   W.suffix.cta_ml = reinterpret_cast<float2*>(w + L.cta_ml);
   const int rows = attend4_rows(P.G, P.ql);
-  const cudaError_t e = rows == 8    ? launch_stream<E, D, 1, 1>(P, W, maps, s)
-                        : rows == 16 ? launch_stream<E, D, 2, 1>(P, W, maps, s)
-                        : rows == 32 ? launch_stream<E, D, 2, 2>(P, W, maps, s)
-                                     : launch_stream<E, D, 2, 4>(P, W, maps, s);
+  const cudaError_t e = rows == 8    ? launch_stream<E, D, 1, 1>(P, kv, W, s)
+                        : rows == 16 ? launch_stream<E, D, 2, 1>(P, kv, W, s)
+                        : rows == 32 ? launch_stream<E, D, 2, 2>(P, kv, W, s)
+                                     : launch_stream<E, D, 2, 4>(P, kv, W, s);
   if (e != cudaSuccess) return e;
   JoinShape shape = {};
   shape.rows[0] = shape.rows[1] = rows;
   shape.heads[0] = shape.heads[1] = 1;
-  shape.ctas[0] = shape.ctas[1] = attend4_ctas(rows);
+  shape.ctas[0] = shape.ctas[1] = attend4_ctas(rows, D);
   return launch_join(P, W, shape, s);
 }
 
@@ -773,36 +764,9 @@ cudaError_t launch_rows4(const Row4Params& P, bool load, cudaStream_t s) {
 
 size_t attend4_ws_bytes(const KvView& kv, int B, int ql) { return B == 0 ? 0 : Layout4(kv, B, ql).total; }
 
-cudaError_t launch_attend4(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s) {
-  if (P.kv.dtype == PW_F16) return P.kv.d == 128 ? launch_typed<__half, 128>(P, maps, ws, s) : launch_typed<__half, 64>(P, maps, ws, s);
-  return P.kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(P, maps, ws, s) : launch_typed<__nv_bfloat16, 64>(P, maps, ws, s);
-}
-
-cudaError_t encode_kv4_maps(const Kv4View& kv, Kv4Maps* maps) {
-  using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  const auto enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t pt = 1ull << kv.page_shift, row = kv.d / 2, words = kv.d / 32;
-  const cuuint32_t box = pt < (cuuint64_t)kBoxTokens ? (cuuint32_t)pt : kBoxTokens, one[4] = {1, 1, 1, 1};
-  // codes: (byte, token of a page, head, page); steps: (word of a page's tokens, head, page)
-  const cuuint64_t cdim[4] = {row, pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
-  const cuuint64_t cstride[3] = {row, row * pt, row * pt * kv.hkv};
-  const cuuint32_t cbox[4] = {(cuuint32_t)row, box, 1, 1};
-  const cuuint64_t sdim[3] = {words * pt, (cuuint64_t)kv.hkv, (cuuint64_t)kv.n_pages};
-  const cuuint64_t sstride[2] = {4 * words * pt, 4 * words * pt * kv.hkv};
-  const cuuint32_t sbox[3] = {(cuuint32_t)(words * box), 1, 1};
-  for (int i = 0; i < 2; ++i) {
-    if (enc(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? kv.v : kv.k, cdim, cstride, cbox, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-        enc(i ? &maps->vs : &maps->ks, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, i ? kv.vs : kv.ks, sdim, sstride, sbox, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  return cudaSuccess;
+cudaError_t launch_attend4(const AttendParams& P, const Kv4View& kv, void* ws, cudaStream_t s) {
+  if (P.kv.dtype == PW_F16) return P.kv.d == 128 ? launch_typed<__half, 128>(P, kv, ws, s) : launch_typed<__half, 64>(P, kv, ws, s);
+  return P.kv.d == 128 ? launch_typed<__nv_bfloat16, 128>(P, kv, ws, s) : launch_typed<__nv_bfloat16, 64>(P, kv, ws, s);
 }
 
 }  // namespace pw

@@ -8,7 +8,6 @@ using namespace pw;
 struct pw_kv4_s {
   Kv4View view;
   KvView plain;   // what the attention kernels' shared parts read of it: shape and error word
-  Kv4Maps maps;
 };
 
 namespace {
@@ -116,12 +115,7 @@ extern "C" pw_status pw_kv4_create(const pw_kv4_desc* desc, void* k, void* v, vo
   p.d = w.d;
   p.page_shift = w.page_shift;
   p.n_pages = w.n_pages;
-  Kv4Maps maps = {};
-  if (!host_sim()) {
-    const cudaError_t e = encode_kv4_maps(w, &maps);
-    if (e != cudaSuccess) return record_cuda_error(e);
-  }
-  auto* kv = new (std::nothrow) pw_kv4_s{w, p, maps};
+  auto* kv = new (std::nothrow) pw_kv4_s{w, p};
   if (!kv) return PW_ERR_OOM;
   *out = kv;
   return PW_OK;
@@ -198,7 +192,7 @@ extern "C" pw_status pw_kv4_attend(pw_kv4_t kv, const pw_attend_desc* a, void* w
   P.table = a->table;
   P.table_stride = a->table_stride;
   P.lens = a->lens;
-  return launched(launch_attend4(P, kv->maps, ws, as_stream(stream)));
+  return launched(launch_attend4(P, kv->view, ws, as_stream(stream)));
 }
 
 // ---- eviction --------------------------------------------------------------------
@@ -239,7 +233,7 @@ extern "C" pw_status pw_kv_weigh(pw_kv_t kv, const pw_weigh_desc* a, void* strea
 extern "C" pw_status pw_kv_evict_workspace_size(pw_kv_t kv, int batch, int budget, size_t* bytes) {
   if (!kv || !bytes || batch < 0 || budget < 1 || budget > (1 << 24)) return PW_ERR_INVALID_ARG;
   if (batch > kMaxBatch) return PW_ERR_UNSUPPORTED;
-  *bytes = up256((size_t)batch * budget * 8) + up256((size_t)batch * budget * 4) + up256((size_t)batch * 4);
+  *bytes = up256((size_t)batch * budget * 8) + up256((size_t)batch * 4);
   return PW_OK;
 }
 
@@ -284,9 +278,7 @@ extern "C" pw_status pw_kv_evict(pw_kv_t kv, const pw_evict_desc* a, void* ws, s
   P.new_mass = a->new_mass;
   P.kept = a->kept;
   char* at = static_cast<char*>(ws);
-  const size_t tokens = (size_t)a->batch * a->budget;
   P.ws_moves = reinterpret_cast<int2*>(at);
-  P.ws_mass = reinterpret_cast<float*>(at + up256(tokens * 8));
-  P.ws_left = reinterpret_cast<int*>(at + up256(tokens * 8) + up256(tokens * 4));
+  P.ws_left = reinterpret_cast<int*>(at + up256((size_t)a->batch * a->budget * 8));
   return launched(launch_evict(P, as_stream(stream)));
 }

@@ -6,7 +6,6 @@
 #include "pw_heads.cuh"
 #include "pw_mma.cuh"
 #include "pw_serve.h"
-#include "pw_tc.cuh"
 
 namespace pw {
 
@@ -23,11 +22,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // at a time, straight into the fragments of the product: the order of the
 // products inside a head does not matter as long as queries and keys share it.
 
-constexpr int kWeighWarps = 8;
-constexpr int kKeys = 64;            // keys a CTA
-
-template <typename E, int D>
-__global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const WeighParams P) {
+// CTAs of kWeighWarps warps take kKeys keys: 64 by 8 where there are few, so that more SMs share them, 128 by 4 where
+// there are many, so that a CTA's start weighs less (5 sequences to 1500 8.5 and 15 us, 64 to 4095 54.1 and 49.7).
+template <typename E, int D, int kKeys, int kWeighWarps>
+__global__ void __launch_bounds__(kWeighWarps * 32, 16 / kWeighWarps) weigh_kernel(const WeighParams P) {
   __shared__ float part[kWeighWarps][kKeys];
   behind_the_stream();
   let_next_start();
@@ -163,8 +161,10 @@ __device__ __forceinline__ int slot_of(const KvView& kv, const int* table, int i
   return page < 0 || page >= kv.n_pages ? -1 : (page << kv.page_shift) + (i & ((1 << kv.page_shift) - 1));
 }
 
+constexpr int kBins = 2048;                      // of a digit of the search: 11, 11 and 10 bits
+
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams P) {
-  __shared__ unsigned hist[256];
+  __shared__ unsigned hist[kBins];
   __shared__ unsigned s_prefix, s_left;
   __shared__ unsigned count[kOwn * 32];            // of 1024 tokens by warp: heavier ones, and equal ones << 16; then their sums
   __shared__ unsigned s_all;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   const int *from = P.table + (long long)b * P.table_stride, *to = P.new_table + (long long)b * P.new_stride;
   const long long row = (long long)b * P.budget;
   int2* moves = P.ws_moves + row;
-  float* held = P.ws_mass + row;
+  float* out = P.new_mass + (long long)b * P.mass_stride;
   float own[kOwn];
   auto load = [&](int first) {
 #pragma unroll
@@ -189,25 +189,27 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       own[k] = i < older ? mass[i] : 0.f;
     }
   };
+  // Token i stays, as number `at`.  Masses may go to their own place: `at` is never above i, and what a span's tokens
+  // write was read before (the span's own masses ahead of the barriers in it).
   auto keep = [&](int at, int i, float x) {
     const int src = slot_of(P.kv, from, i), dst = slot_of(P.kv, to, at);
     if (src < 0 || dst < 0) atomicExch(P.kv.err, kErrPage);
     moves[at] = make_int2(src, src == dst ? -1 : dst);
-    held[at] = x;
+    out[at] = x;
     if (P.kept) P.kept[row + at] = i;
   };
   load(0);
-  for (int i = tid; i < recent; i += kSelectThreads) keep(need + i, older + i, mass[older + i]);
   const bool all = need >= older;
   // the smallest key that stays (`bar`), and how many tokens of it
   unsigned bar = 0, equal = 0;
   if (!all) {
     if (tid == 0) s_prefix = 0, s_left = need;
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
-      const unsigned prefix = s_prefix;
+      const unsigned prefix = s_prefix, want = s_left;
 #pragma unroll 1
       for (int first = 0; first < older; first += kSpan) {
         if (older > kSpan) load(first);
@@ -215,30 +217,29 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
         for (int k = 0; k < kOwn; ++k) {
           if (first + k * kSelectThreads + tid >= older) break;
           const unsigned key = mass_key(own[k]);
-          if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[key >> shift & 255], 1u);
+          if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
         }
       }
       __syncthreads();
-      if (warp == 0) {  // the digit that holds the s_left-th largest
-        unsigned mine[8], sum = 0;  // lane 0 holds the largest digits
+      // the digit that holds the want-th largest; thread 0 has the two largest
+      const unsigned high = hist[kBins - 1 - 2 * tid], low = hist[kBins - 2 - 2 * tid];
+      unsigned scan = high + low;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += mine[k] = hist[255 - 8 * lane - k];
-        unsigned scan = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned y = __shfl_up_sync(0xffffffffu, scan, o);
-          if (lane >= o) scan += y;
-        }
-        unsigned before = scan - sum;
-        const unsigned want = s_left;
-        __syncwarp();
-        // want = 0 (only the recent stay) ends on the largest digit, with none of it
-        if ((before < want || (want == 0 && lane == 0)) && (scan >= want)) {
-          int k = 0;
-          while (k < 7 && before + mine[k] < want) before += mine[k++];
-          s_prefix = prefix << 8 | (255 - 8 * lane - k);
-          s_left = want - before;
-        }
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += y;
+      }
+      if (lane == 31) count[warp] = scan;
+      __syncthreads();
+      unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? count[lane] : 0u);  // in the warps in front
+      before += scan - high - low;
+      // want = 0 (only the recent stay) ends on the largest digit, with none of it
+      if ((before < want && want <= before + high) || (want == 0 && tid == 0)) {
+        s_prefix = prefix << bits | (kBins - 1 - 2 * tid & ((1u << bits) - 1));
+        s_left = want - before;
+      } else if (before + high < want && want <= before + high + low) {
+        s_prefix = prefix << bits | (kBins - 2 - 2 * tid & ((1u << bits) - 1));
+        s_left = want - before - high;
       }
       __syncthreads();
     }
@@ -290,9 +291,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
     more_before += s_all & 0xffff, same_before += s_all >> 16;
     __syncthreads();
   }
-  __syncthreads();  // the new masses may lie in the old ones' place
-  float* out = P.new_mass + (long long)b * P.mass_stride;
-  for (int i = tid; i < P.mass_stride; i += kSelectThreads) out[i] = i < left ? held[i] : 0.f;
+  // the recent ones, a step's masses read before any of it is written, then zeros behind them
+#pragma unroll 1
+  for (int i = tid; i - tid < recent; i += kSelectThreads) {
+    const float x = i < recent ? mass[older + i] : 0.f;
+    __syncthreads();
+    if (i < recent) keep(need + i, older + i, x);
+  }
+  __syncthreads();
+  for (int i = left + tid; i < P.mass_stride; i += kSelectThreads) out[i] = 0.f;
   if (P.kept)
     for (int i = left + tid; i < P.budget; i += kSelectThreads) P.kept[row + i] = -1;
   if (tid == 0) P.new_lens[b] = left, P.ws_left[b] = left;
@@ -302,104 +309,58 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
 //
 // Kept token j goes to slot j.  j is never above the token's old place, so a
 // CTA that goes through a row of places in order, and has each step's rows in
-// shared memory before any of the step is written, may move them inside the
-// same pages.  A CTA is one warp with the keys or the values of one head (or a
-// 64-byte column of them, where the rows alone would leave SMs idle); bulk
-// copies bring a step's 8 KB while the steps before go out, so that few
-// registers and no instructions in the data's way let seven CTAs an SM keep
-// HBM busy.
+// registers before any of the step is written, may move them inside the same
+// pages; the next step's rows and the slots of the one after are on their way
+// meanwhile.  A CTA takes the keys or the values of one head (or a 64-byte
+// column of them, where whole rows would leave SMs idle).  Bound by HBM; bulk
+// copies of a row each, tried instead, go out one in 12 cycles an SM, which is
+// less.
 
-constexpr int kStep = 8192;          // bytes of a step
-constexpr int kSteps = 3;            // in shared memory
-constexpr int kMoveSmem = kSteps * kStep + 8 * kSteps;
+constexpr int kMoveThreads = 128;
 
-template <int R>  // rows a lane and step, of 256 / R bytes
-__global__ void __launch_bounds__(32) move_kernel(const EvictParams P, int columns) {
-  constexpr int BYTES = kStep / 32 / R, ROWS = 32 * R;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem), bars = base + kSteps * kStep;
-  const int lane = threadIdx.x;
-  if (lane < kSteps) {
-    mbar_init(bars + 8 * lane, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncwarp();
+template <int LPR>  // lanes a row: 16 bytes each
+__global__ void __launch_bounds__(kMoveThreads, 8) move_kernel(const EvictParams P, int columns) {
+  constexpr int U = 4, RPS = kMoveThreads / LPR, STEP = U * RPS;
   behind_the_stream();
   let_next_start();
-  const int b = blockIdx.y, c = blockIdx.x / columns, col = blockIdx.x % columns;
-  char* cache = ((c & 1) ? P.kv.v : P.kv.k) + 2 * (c >> 1) * P.kv.head_stride + col * BYTES;
+  const int b = blockIdx.y, tid = threadIdx.x, sub = tid / LPR, c = blockIdx.x / columns, col = blockIdx.x % columns;
+  char* cache = ((c & 1) ? P.kv.v : P.kv.k) + 2 * (c >> 1) * P.kv.head_stride + (col * LPR + tid % LPR) * 16;
   const int left = P.ws_left[b], shift = P.kv.page_shift, mask = (1 << shift) - 1;
   const int2* moves = P.ws_moves + (long long)b * P.budget;
-  auto place = [&](int slot) { return cache + 2 * ((slot >> shift) * P.kv.page_stride + (slot & mask) * P.kv.token_stride); };
-  int dst[kSteps][R];
-  // rows of step s into shared memory; those of a page outside the cache are zeros
-  auto load = [&](int s, int (&to)[R]) {
-    int2 m[R];
-    unsigned rows = 0;
+  auto place = [&](int slot) {
+    return reinterpret_cast<uint4*>(cache + 2 * ((slot >> shift) * P.kv.page_stride + (slot & mask) * P.kv.token_stride));
+  };
+  int2 slots[U];
+  uint4 row[U], next[U];
+  int dst[U], next_dst[U];
+  auto look = [&](int j0) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int j = s * ROWS + r * 32 + lane;
-      m[r] = j < left ? moves[j] : make_int2(-1, -1);
-      to[r] = m[r].y;
-      rows += __popc(__ballot_sync(0xffffffffu, m[r].x >= 0 && m[r].y >= 0));
-    }
-    const uint32_t bar = bars + 8 * (s % kSteps), at = base + (s % kSteps) * kStep + lane * BYTES;
-    if (lane == 0) mbar_arrive_expect_tx(bar, rows * BYTES);
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (m[r].y < 0) continue;
-      if (m[r].x >= 0) {
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         at + r * 32 * BYTES),
-                     "l"(place(m[r].x)), "n"(BYTES), "r"(bar)
-                     : "memory");
-      } else {
-        for (int k = 0; k < BYTES; k += 16) sts128(at + r * 32 * BYTES + k, make_uint4(0, 0, 0, 0));
-        fence_proxy_async_smem();
-      }
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * RPS + sub;
+      slots[u] = j < left ? moves[j] : make_int2(-1, -1);
     }
   };
-  const int steps = (left + ROWS - 1) / ROWS;
-  // a wait that gives up flags the error word and ends the moves; what is on its way lands first
-  auto wait = [&](int s) {
-    bool ok = false;
-    const long long t0 = clock64();
-    while (!(ok = mbar_try_wait(bars + 8 * (s % kSteps), (s / kSteps) & 1)) && clock64() - t0 < kWaitCycles) {
+  auto load = [&](uint4 (&r)[U], int (&d)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      r[u] = make_uint4(0, 0, 0, 0);  // a page outside the cache reads as zeros
+      d[u] = slots[u].y;
+      if (slots[u].x >= 0 && slots[u].y >= 0) r[u] = *place(slots[u].x);
     }
-    return __all_sync(0xffffffffu, ok);
   };
-  bool ok = true;
-  load(0, dst[0]);
-  load(1, dst[1]);
-  int s0 = 0;
+  look(0);
+  load(row, dst);
+  look(STEP);
 #pragma unroll 1
-  for (; ok && s0 < steps; s0 += kSteps) {
+  for (int j0 = 0; j0 < left; j0 += STEP) {
+    load(next, next_dst);
+    look(j0 + 2 * STEP);
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {  // the places in registers by their number
-      const int s = s0 + k;
-      if (!ok || s >= steps) break;
-      ok = wait(s);
-      if (!ok) break;
-      const uint32_t at = base + k * kStep + lane * BYTES;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (dst[k][r] >= 0)
-          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(place(dst[k][r])),
-                       "r"(at + r * 32 * BYTES), "n"(BYTES)
-                       : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      // the step two ahead goes where the last one's rows have left
-      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      __syncwarp();
-      load(s + 2, dst[(k + 2) % kSteps]);
-    }
-  }
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  if (!ok) {
-    if (lane == 0) atomicExch(P.kv.err, kErrTimeout);
-    const long long t0 = clock64();
-    while (clock64() - t0 < 1000000) {
+    for (int u = 0; u < U; ++u) {
+      if (dst[u] >= 0) *place(dst[u]) = row[u];
+      row[u] = next[u];
+      dst[u] = next_dst[u];
     }
   }
 }
@@ -408,13 +369,17 @@ __global__ void __launch_bounds__(32) move_kernel(const EvictParams P, int colum
 
 cudaError_t launch_weigh(const WeighParams& P, cudaStream_t s) {
   const long long cap = min((long long)P.table_stride << P.kv.page_shift, (long long)P.mass_stride);
-  const unsigned tiles = (unsigned)((cap + kKeys - 1) / kKeys);
+  const bool many = P.B * (cap / 64) > 16 * sm_count();
+  const int keys = many ? 128 : 64;
+  const unsigned tiles = (unsigned)((cap + keys - 1) / keys);
   // without keys a CTA a sequence still looks at its length
-  const Launch at(dim3(tiles ? tiles : 1, P.B), kWeighWarps * 32, 0, s);
+  const Launch at(dim3(tiles ? tiles : 1, P.B), many ? 128 : 256, 0, s);
+  auto go = [&](auto few, auto lots) { return many ? cudaLaunchKernelEx(&at.cfg, lots, P) : cudaLaunchKernelEx(&at.cfg, few, P); };
   if (P.kv.dtype == PW_F16)
-    return P.kv.d == 128 ? cudaLaunchKernelEx(&at.cfg, weigh_kernel<__half, 128>, P) : cudaLaunchKernelEx(&at.cfg, weigh_kernel<__half, 64>, P);
-  return P.kv.d == 128 ? cudaLaunchKernelEx(&at.cfg, weigh_kernel<__nv_bfloat16, 128>, P)
-                       : cudaLaunchKernelEx(&at.cfg, weigh_kernel<__nv_bfloat16, 64>, P);
+    return P.kv.d == 128 ? go(weigh_kernel<__half, 128, 64, 8>, weigh_kernel<__half, 128, 128, 4>)
+                         : go(weigh_kernel<__half, 64, 64, 8>, weigh_kernel<__half, 64, 128, 4>);
+  return P.kv.d == 128 ? go(weigh_kernel<__nv_bfloat16, 128, 64, 8>, weigh_kernel<__nv_bfloat16, 128, 128, 4>)
+                       : go(weigh_kernel<__nv_bfloat16, 64, 64, 8>, weigh_kernel<__nv_bfloat16, 64, 128, 4>);
 }
 
 cudaError_t launch_evict(const EvictParams& P, cudaStream_t s) {
@@ -424,11 +389,11 @@ cudaError_t launch_evict(const EvictParams& P, cudaStream_t s) {
   // 64-byte columns where whole rows leave SMs idle (see move_kernel)
   const bool split = (long long)P.B * P.kv.hkv * 2 < 2 * sm_count();
   const int row = 2 * P.kv.d, columns = split ? row / 64 : 1;
-  const Launch at(dim3(P.kv.hkv * 2 * columns, P.B), 32, kMoveSmem, s);
+  const Launch at(dim3(P.kv.hkv * 2 * columns, P.B), kMoveThreads, 0, s);
   switch (row / columns) {
     case 64: return cudaLaunchKernelEx(&at.cfg, move_kernel<4>, P, columns);
-    case 128: return cudaLaunchKernelEx(&at.cfg, move_kernel<2>, P, columns);
-    default: return cudaLaunchKernelEx(&at.cfg, move_kernel<1>, P, columns);
+    case 128: return cudaLaunchKernelEx(&at.cfg, move_kernel<8>, P, columns);
+    default: return cudaLaunchKernelEx(&at.cfg, move_kernel<16>, P, columns);
   }
 }
 

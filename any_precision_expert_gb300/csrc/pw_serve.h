@@ -111,7 +111,6 @@ struct EvictParams {
   float* new_mass;
   int* kept;
   int2* ws_moves;       // [B][budget] slots of the tokens that stay, old and new (-1: none, or there already)
-  float* ws_mass;       // their masses
   int* ws_left;         // [B]
 };
 
@@ -183,13 +182,8 @@ cudaError_t launch_weigh(const WeighParams& P, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& P, cudaStream_t s);
 cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s);
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s);
-// Tensor maps of a 4-bit cache: codes (byte, token of a page, head, page), steps (word of a page's tokens, head, page).
-struct Kv4Maps {
-  CUtensorMap k, v, ks, vs;
-};
-cudaError_t encode_kv4_maps(const Kv4View& kv, Kv4Maps* maps);
 cudaError_t launch_rows4(const Row4Params& P, bool load, cudaStream_t s);
 size_t attend4_ws_bytes(const KvView& kv, int B, int ql);
-cudaError_t launch_attend4(const AttendParams& P, const Kv4Maps& maps, void* ws, cudaStream_t s);
+cudaError_t launch_attend4(const AttendParams& P, const Kv4View& kv, void* ws, cudaStream_t s);
 
 }  // namespace pw
