@@ -5,8 +5,10 @@
 // least + c step.  The order of a row's codes is that of the products, so that
 // a lane's share of a row is one aligned piece and a mask turns it into
 // operands:
-// * keys: word t D / 32 + i (i < D / 32, t < 4) holds values 32 i + 8 t .. + 7 in
-//   the nibbles of key_nibble: what lane t of four multiplies;
+// * keys: word t D / 32 + i (i < D / 32, t < 4) holds values 32 i + 8 t .. + 7,
+//   what lane t of four multiplies, in the order 0 4 2 6 1 5 3 7 from the lowest
+//   nibble on: values (0, 1) and (2, 3) are the operand pairs of an even product
+//   step, (4, 5) and (6, 7) of the odd one, and a pair lies 16 bits apart;
 // * values: in order, D / 8 for each of eight lanes; heads of 128 with the
 //   row's halves exchanged where bit 2 of the token is set, so that the rows
 //   a warp reads at once lie in different banks (value_word).
@@ -19,10 +21,6 @@
 namespace pw {
 
 namespace {
-
-// Nibble of a key word that holds value k of its eight: values (0, 1) and (2, 3) are the operand pairs of an even product
-// step, (4, 5) and (6, 7) of the odd one; a pair lies 16 bits apart.
-__device__ __forceinline__ constexpr int key_nibble(int k) { return (k & 1) * 4 + (k & 2) + (k >> 2); }
 
 template <int D>
 __device__ __forceinline__ int value_word(int l, int token) {
@@ -50,7 +48,7 @@ __device__ __forceinline__ uint16_t from_f32(float x) {
 // Eight values a lane: a row is D / 8 lanes, a group four of them, a lane's
 // codes one word.  Bound by HBM for long prompts, by one chain of loads else; a
 // warp has U steps of rows in flight (one while there are few).  Quotients are
-// products with the step's reciprocal, off by less than 2^-18, and exact
+// products with the step's reciprocal, off by less than 2^-17, and exact
 // divisions where one falls that near to a half.
 
 constexpr int kRowThreads = 128;
@@ -85,7 +83,7 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // of two va
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// The codes of eight values of a group as a word, and its least value and step, given the values of its other lanes.
+// The codes of eight values of a group as a word (all of its lanes call), and its least value and step, given the values of its other lanes.
 template <typename E>
 __device__ __forceinline__ uint2 quantise8(const uint4& raw, bool value) {
   // the group's least value and largest, the latter as the least of the negatives
@@ -95,42 +93,66 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, bool value) {
   uint32_t ends = min2<E>(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
   ends = min2<E>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
   ends = min2<E>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
-  const float lo = to_f32<E>(ends & 0xffff), hi = -to_f32<E>(ends >> 16);
-  const uint32_t step_bits = from_f32<E>((hi - lo) / 15.f);
+  const float lo = to_f32<E>(ends & 0xffff), hi = -to_f32<E>(ends >> 16), range = hi - lo;
+  // The step is the rounding of a quotient.  A product is within 2^-23 of it: where the numbers 2^-22 around round alike,
+  // so does the quotient.
+  const float about = range * (1.f / 15.f);
+  const uint32_t around = pack2<E>(about * (1.f - 2.384185791015625e-7f), about * (1.f + 2.384185791015625e-7f));
+  uint32_t step_bits = around & 0xffff;
+  if (around >> 16 != step_bits) step_bits = from_f32<E>(range / 15.f);
   const float step = to_f32<E>(step_bits);
-  if (!isfinite(lo) || !isfinite(hi) || !isfinite(step)) return make_uint2(0, 0x7fff7fff);  // the group holds what is no number
+  float x[8];
+  unpack8<E>(raw, x);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+  constexpr float kRound = 12582912.f;  // 1.5 2^23: a sum with it is rounded to a whole number, in its low bits
+  float far = 0.f;                      // the largest distance from a whole number
   uint32_t w = 0;
-  if (step > 0.f) {
-    float x[8];
-    unpack8<E>(raw, x);
-    const float inv = 1.f / step;
-    constexpr float kRound = 12582912.f;  // 1.5 2^23: a sum with it is rounded to a whole number, in its low bits
-    float far = 0.f;                      // the largest distance from a whole number
-    uint32_t c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float q = fminf((x[k] - lo) * inv, 15.f), r = q + kRound;
+    far = fmaxf(far, fabsf(q - (r - kRound)));
+    w += (__float_as_uint(r) - __float_as_uint(kRound)) << 4 * k;
+  }
+  constexpr float kNear = 0.5f - 7.62939453125e-6f;
+  if (far > kNear || !(inv < CUDART_INF_F)) {
+    // halves themselves are common where the type has few bits: a value less half-and-codes of steps is then 0, exactly
+    far = 0.f;
+    w = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float q = fminf((x[k] - lo) * inv, 15.f), r = q + kRound;
-      far = fmaxf(far, fabsf(q - (r - kRound)));
-      c[k] = __float_as_uint(r);
+      const float d = x[k] - lo, q = fminf(d * inv, 15.f), half = floorf(q) + 0.5f;
+      const bool tie = fmaf(-half, step, d) == 0.f;
+      const float r = (tie ? half : q) + kRound;
+      far = fmaxf(far, tie ? 0.f : fabsf(q - (r - kRound)));
+      w += (__float_as_uint(r) - __float_as_uint(kRound)) << 4 * k;
     }
-    if (far > 0.5f - 3.814697265625e-6f || !(inv < CUDART_INF_F)) {
+    if (far > kNear || !(inv < CUDART_INF_F)) {
+      w = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = __float_as_uint(fminf((x[k] - lo) / step, 15.f) + kRound);
+      for (int k = 0; k < 8; ++k) w |= (uint32_t)min(max(__float2int_rn((x[k] - lo) / step), 0), 15) << 4 * k;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w += (c[k] - __float_as_uint(kRound)) << 4 * (value ? k : key_nibble(k));
   }
+  if (!(step > 0.f)) w = 0;
+  if (!value) {  // keys: in the order 0 4 2 6 1 5 3 7
+    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+    w = __byte_perm(even | even >> 12, odd | odd >> 12, 0x5410);
+  }
+  if (!isfinite(lo) || !isfinite(hi) || !isfinite(step)) return make_uint2(0, 0x7fff7fff);  // the group holds what is no number
   return make_uint2(w, (ends & 0xffff) | step_bits << 16);
 }
 
 template <typename E>
 __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t st, bool value) {
   const float least = to_f32<E>(st & 0xffff), step = to_f32<E>(st >> 16);
+  if (!value) {  // back to the order of the values
+    const uint32_t even = w & 0xffffu, odd = w >> 16;
+    w = ((even | even << 12) & 0x0f0f0f0fu) | ((odd | odd << 12) & 0x0f0f0f0fu) << 4;
+  }
   float x[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    // 2^23 + c, less 2^23
-    const float c = __uint_as_float((w >> 4 * (value ? k : key_nibble(k)) & 15) | 0x4b000000u) - 8388608.f;
+    const float c = __uint_as_float((w >> 4 * k & 15) | 0x4b000000u) - 8388608.f;  // 2^23 + c, less 2^23
     x[k] = fmaf(c, step, least);
   }
   return pack8<E>(x);
@@ -502,7 +524,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
           }
         }
         const bool edge = first + 32 > sure;
-        uint32_t pf[NT][2][2];  // weights as the second operand: keys 2 t4, + 1 (and + 8) of 16, row g
+        // Weights as the second operand: keys 2 t4, + 1 (and + 8) of 16, row g.  In bf16, whose 8 bits would add to the values'
+        // own rounding, what a first number leaves of a weight goes into a second one and a second product.
+        constexpr int TERMS = __is_same(E, __half) ? 1 : 2;
+        uint32_t pf[NT][2][2][TERMS];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
@@ -548,8 +573,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
               s[j][h][i] = ex2(s[j][h][i] - ref[i & 1]);
               l[j][i & 1] += s[j][h][i];
             }
-            pf[j][h][0] = transpose8(pack2<E>(s[j][h][0], s[j][h][1]));
-            pf[j][h][1] = transpose8(pack2<E>(s[j][h][2], s[j][h][3]));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              float u = s[j][h][2 * b], v = s[j][h][2 * b + 1];
+#pragma unroll
+              for (int x = 0; x < TERMS; ++x) {
+                const uint32_t w = pack2<E>(u, v);
+                pf[j][h][b][x] = transpose8(w);
+                if (x + 1 < TERMS) {
+                  const float2 f = Pair<E>::up(*reinterpret_cast<const typename Pair<E>::V*>(&w));
+                  u -= f.x, v -= f.y;
+                }
+              }
+            }
           }
         }
 #pragma unroll
@@ -579,7 +615,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
                 const uint32_t a[4] = {value_pair<E>(x, n, step01, least01), value_pair<E>(x, n + 1, step01, least01),
                                        value_pair<E>(y, n, step23, least23), value_pair<E>(y, n + 1, step23, least23)};
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma16816<E>(o[j][4 * w + 2 * half + n / 2], a, pf[j][h][0], pf[j][h][1]);
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                  for (int x = 0; x < TERMS; ++x) mma16816<E>(o[j][4 * w + 2 * half + n / 2], a, pf[j][h][0][x], pf[j][h][1][x]);
               }
             }
         }
