@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 16 / kWeighWarps) weigh_kern
 #pragma unroll
     for (int k = 0; k < kWeighWarps; ++k) w += part[k][i];
     const long long at = (long long)b * P.mass_stride + key0 + i;
-    P.out[at] = fmaf(P.decay, P.mass[at], w);
+    P.out[at] = P.decay == 0.f ? w : fmaf(P.decay, P.mass[at], w);
   }
 }
 

@@ -6,6 +6,7 @@
 // took 8 to 11 us of host time a call, this takes 0.2 to 0.5 beside the launch.
 // Shape, type and device errors become ValueError; the pw_status is returned.
 #include <Python.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -61,6 +62,15 @@ int dtype_of(const at::Tensor& t, const char* what) {
 void on_gpu(const at::Tensor& t, const char* what) {
   if (!t.is_cuda() && !pw::host_sim()) fail(what, "must be on a GPU");
 }
+
+// The same, and the call runs on that GPU, whichever the current one is: the default streams of all of them look alike.
+struct OnGpu {
+  c10::cuda::OptionalCUDAGuard guard;
+  OnGpu(const at::Tensor& t, const char* what) {
+    on_gpu(t, what);
+    if (t.is_cuda()) guard.set_index(t.get_device());
+  }
+};
 
 // [T][H][D] head rows of the type and on the device of `like`.
 pw_rows rows(const at::Tensor& t, int64_t T, int64_t H, int64_t D, const at::Tensor& like, const char* what) {
@@ -137,7 +147,7 @@ pw_status rope(PyObject* const* a) {
   const at::Tensor *q = maybe(a[1], "q"), *k = maybe(a[2], "k");
   const at::Tensor* some = q ? q : k;
   if (!some || some->dim() != 3 || (k && k->dim() != 3)) fail("q", "q or k must be [T, heads, head_dim]");
-  on_gpu(*some, q ? "q" : "k");
+  const OnGpu here(*some, q ? "q" : "k");
   const int64_t T = some->size(0), D = some->size(2);
   const pw_heads heads = {dtype_of(*some, "q"), size32(some->size(1), "q"), size32((k ? k : q)->size(1), "k"), size32(D, "q")};
   const pw_rotary* r = rotary(a[0], heads.dtype, D, *some);
@@ -155,7 +165,7 @@ pw_status rope(PyObject* const* a) {
 pw_status append(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const int64_t hq = integer(a[2]), hk = cache.size(1), D = cache.size(3);
   const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
   const int64_t T = k.dim() == 3 ? k.size(0) : -1;
@@ -174,7 +184,7 @@ pw_status append(PyObject* const* a) {
 pw_status attend(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const int64_t hq = integer(a[2]), D = cache.size(3);
   const at::Tensor &q = tensor(a[3], "q"), &table = tensor(a[4], "table"), &out = tensor(a[6], "out");
   if (table.dim() != 2) fail("table", "must be [batch, pages]");
@@ -212,7 +222,7 @@ pw_status attend(PyObject* const* a) {
 pw_status verify(PyObject* const* a) {
   const at::Tensor& p = tensor(a[0], "target_p");
   if (p.dim() != 3) fail("target_p", "must be [B, K + 1, V]");
-  on_gpu(p, "target_p");
+  const OnGpu here(p, "target_p");
   const int64_t B = p.size(0), K = p.size(1) - 1, V = p.size(2);
   if (B > INT32_MAX || K > INT32_MAX || V > INT32_MAX) fail("target_p", "too large");
   return pw_verify_draft(vec<const float>(a[0], at::kFloat, p, "target_p", B, K + 1, V),
@@ -253,7 +263,7 @@ const at::Tensor& page_table(PyObject* o, const char* what) {
 pw_status prompt(PyObject* const* a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &offsets = tensor(a[3], "offsets");
   if (q.dim() != 3 || k.dim() != 3) fail("q", "q, k and v must be [T, heads, head_dim]");
-  on_gpu(q, "q");
+  const OnGpu here(q, "q");
   const int64_t T = q.size(0), hq = q.size(1), hk = k.size(1), D = q.size(2);
   const pw_heads heads = {dtype_of(q, "q"), size32(hq, "q"), size32(hk, "k"), size32(D, "q")};
   pw_prompt_desc d = {};
@@ -275,7 +285,7 @@ pw_status prompt(PyObject* const* a) {
 pw_status logprobs(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0], "logits");
   if (x.dim() != 2) fail("logits", "must be [T, V]");
-  on_gpu(x, "logits");
+  const OnGpu here(x, "logits");
   if (x.size(1) > 1 && x.stride(1) != 1) fail("logits", "a row's values must be contiguous");
   pw_logprob_desc d = {};
   d.dtype = x.scalar_type() == at::kFloat ? (int)PW_F32 : x.scalar_type() == at::kHalf ? (int)PW_F16 : (int)PW_BF16;
@@ -305,7 +315,7 @@ pw_status logprobs(PyObject* const* a) {
 pw_status rows4(PyObject* const* a) {
   auto* kv = static_cast<pw_kv4_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const int64_t hk = cache.size(1), D = cache.size(3) * 32;
   const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
   const int64_t T = k.dim() == 3 ? k.size(0) : -1;
@@ -319,7 +329,7 @@ pw_status rows4(PyObject* const* a) {
 pw_status attend4(PyObject* const* a) {
   auto* kv = static_cast<pw_kv4_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const int64_t hq = integer(a[2]), D = cache.size(3) * 32;
   const at::Tensor &q = tensor(a[3], "q"), &table = page_table(a[4], "table"), &out = tensor(a[6], "out");
   pw_attend_desc d = {};
@@ -341,7 +351,7 @@ pw_status attend4(PyObject* const* a) {
 pw_status weigh(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const int64_t hq = integer(a[2]), D = cache.size(3);
   const at::Tensor &q = tensor(a[3], "q"), &table = page_table(a[4], "table"), &mass = tensor(a[7], "mass");
   if (mass.dim() != 2) fail("mass", "must be [batch, positions]");
@@ -366,7 +376,7 @@ pw_status weigh(PyObject* const* a) {
 pw_status evict(PyObject* const* a) {
   auto* kv = static_cast<pw_kv_t>(PyLong_AsVoidPtr(a[0]));
   const at::Tensor& cache = tensor(a[1], "cache");
-  on_gpu(cache, "cache");
+  const OnGpu here(cache, "cache");
   const at::Tensor &table = page_table(a[2], "table"), &mass = tensor(a[4], "mass"), &to = page_table(a[8], "new_table");
   if (mass.dim() != 2) fail("mass", "must be [batch, positions]");
   pw_evict_desc d = {};

@@ -829,7 +829,8 @@ pw_status pw_kv4_attend(pw_kv4_t kv, const pw_attend_desc* desc, void* ws, size_
  *   out[b][i] = decay * mass[b][i] + sum over its q_len query tokens and all heads of e^(scale q . key_i - lse)
  * over the queries that see key i (query j sees 0 .. lens[b] - q_len + j); lse is
  * what pw_kv_attend gave (prefixes included); a query whose lse is -infinity
- * weighs nothing.  Positions at and past the length are left as they were.
+ * weighs nothing; where decay is 0 what mass holds does not count.  Positions
+ * at and past the length are left as they were.
  * Sums are fp32 and in a fixed order.
  *   q         [batch * q_len][n_heads] rows;  lse  device fp32 [batch * q_len][n_heads]
  *   mass,out  device fp32 [batch][mass_stride]; may be the same

@@ -377,6 +377,52 @@ def test_four_bit_append_and_load(T, hk, D, page, dt):
         assert torch.equal(x, y)
 
 
+def test_calls_of_the_4_bit_cache_and_eviction_in_a_graph():
+    """Append, attend, weigh and evict captured once and replayed on other contents of the same buffers."""
+    rng = np.random.default_rng(30)
+    B, hq, hk, D, page = 3, 8, 2, 64, 16
+    c = Case4(rng, [40, 20, 31], hq, hk, D, page, torch.float16)
+    f = Cached(rng, [40, 20, 31], hq, hk, D, page, torch.float16)
+    t4, t16, lens, lens0 = ints(c.table), ints(f.table), ints([40, 20, 31]), ints([40, 20, 31])
+    out, lse = torch.empty_like(c.q), torch.empty(B, hq, device="cuda")
+    o16, l16 = torch.empty_like(c.q), torch.empty(B, hq, device="cuda")
+    w4 = torch.empty(c.kv.attend_workspace_size(B), dtype=torch.uint8, device="cuda")
+    w16 = torch.empty(f.kv.attend_workspace_size(B), dtype=torch.uint8, device="cuda")
+    we = torch.empty(f.kv.evict_workspace_size(B, 16), dtype=torch.uint8, device="cuda")
+    mass, kept = torch.zeros(B, f.table.shape[1] * page, device="cuda"), ints(np.zeros((B, 16)))
+    slots = torch.arange(len(c.k), dtype=torch.int32, device="cuda")
+
+    def step():
+        c.kv.append(c.k, c.v, slots)
+        c.kv.attend(c.q, t4, lens0, out, w4, lse=lse)
+        lens.copy_(lens0)
+        f.kv.attend(c.q, t16, lens, o16, w16, lse=l16)
+        f.kv.weigh(c.q, t16, lens, l16, mass, decay=0.0)
+        f.kv.evict(t16, lens, mass, 16, we, recent=4, kept=kept)
+
+    step()  # sets up what a first call sets up
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2):
+        r = np.random.default_rng(seed)
+        for x in (c.k, c.v, c.q, f.k, f.v):
+            x.copy_(rand(r, *x.shape, dtype=torch.float16))
+        k0, v0 = host(f.k), host(f.v)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse)
+        _, rl, _, _, _ = S.attend(host(c.q), k0, v0, f.table, [40, 20, 31], 1, D ** -0.5)
+        w, _ = X.weigh(host(c.q), k0, f.table, [40, 20, 31], host(l16), np.zeros(mass.shape), 1, D ** -0.5, 1.0)
+        assert lens.tolist() == [16, 16, 16]
+        for b in range(B):
+            who = kept[b].tolist()
+            n = [40, 20, 31][b]
+            assert who == sorted(who) and who[-4:] == list(range(n - 4, n))
+            gone = [i for i in range(n) if i not in who]
+            assert w[b][who[:-4]].min() >= w[b][gone].max() * (1 - 1e-5)
+
+
 class Case4:
     def __init__(self, rng, lens, hq, hk, D, page, dtype, q_len=1, qscale=2.0, width=None):
         B = len(lens)
@@ -568,8 +614,29 @@ def test_weigh_ignores_what_is_behind_a_length_and_rows_that_saw_nothing():
     c.kv.weigh(q, ints(c.table), ints(c.lens), ls, b)
     assert torch.equal(a, b) and (a[0, :20] > 0).all() and (a[1, 9:] == 0).all()
     ls[1] = -INF
+    b.fill_(NAN)  # a decay of 0 starts anew
     c.kv.weigh(q, ints(c.table), ints(c.lens), ls, b, decay=0.0)
-    assert (b[1, :9] == 0).all() and torch.equal(b[0], a[0])
+    assert (b[1, :9] == 0).all() and torch.equal(b[0, :20], a[0, :20])
+
+
+def test_weigh_many_sequences():
+    # more tiles than the shape for few CTAs takes; every head's weights still sum to 1
+    rng = np.random.default_rng(9)
+    for D, page in ((64, 16), (128, 64)):
+        lens = rng.integers(1, 700, 300)
+        lens[:2] = 700, 129
+        c = Cached(rng, lens.tolist(), 8, 2, D, page, torch.float16)
+        q = rand(rng, 300, 8, D, dtype=torch.float16, scale=2.0)
+        out, lse = torch.empty_like(q), torch.empty(300, 8, device="cuda")
+        ws = torch.empty(c.kv.attend_workspace_size(300), dtype=torch.uint8, device="cuda")
+        c.kv.attend(q, ints(c.table), ints(lens), out, ws, lse=lse)
+        mass = torch.zeros(300, c.table.shape[1] * page, device="cuda")
+        c.kv.weigh(q, ints(c.table), ints(lens), lse, mass)
+        assert np.allclose(host(mass).sum(1), 8, rtol=1e-4)
+        for b in (0, 1, 299):
+            ref, size = X.weigh(host(q[b:b + 1]), host(c.k), c.table[b:b + 1], lens[b:b + 1], host(lse[b:b + 1]),
+                                np.zeros((1, mass.shape[1])), 1, D ** -0.5, 1.0)
+            close(mass[b:b + 1], ref, size * (2.0 ** -22 + (2 * D + 32) * E32 * 2 + 24 * E32))
 
 
 def run_evict(c, lens, mass, budget, recent, table=None, in_place=True):
@@ -617,6 +684,28 @@ def test_evict_matches_oracle(i, where):
                 ref[1][p, :, t % page] = bits(c.v)[p, :, t % page]
     assert np.array_equal(bits(c.k), ref[0]) and np.array_equal(bits(c.v), ref[1])
     assert c.kv.check_device() == 0
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_sequences_longer_than_a_span(in_place):
+    # 8192 masses are held at a time: lengths around that and past it, masses with many equal ones
+    rng = np.random.default_rng(12)
+    lens, page = [8192, 8193, 20000, 16500], 1024
+    for budget, recent in ((8192, 0), (9000, 300), (100, 99)):
+        c = Cached(rng, lens, 1, 1, 64, page, torch.float16, spare=-(-budget // page))
+        m = rng.choice([0.0, 0.25, 1.0, 3.5], (4, c.table.shape[1] * page)).astype(np.float32)
+        bits = lambda t: t.contiguous().view(torch.int16).cpu().numpy()  # noqa: E731
+        new = c.table if in_place else c.spare
+        k0 = bits(c.k)
+        nl, nm, kept = run_evict(c, lens, torch.from_numpy(m).cuda(), budget, recent, None if in_place else new, in_place=in_place)
+        k1 = bits(c.k)
+        for b, n in enumerate(lens):
+            who = X.stays(m[b], n, budget, recent)
+            assert nl[b] == len(who) and kept[b, :len(who)].tolist() == who and (kept[b, len(who):] == -1).all()
+            assert np.array_equal(nm[b, :len(who)].cpu().numpy(), m[b][who]) and (nm[b, len(who):] == 0).all()
+            who, at = np.array(who), np.arange(len(who))
+            assert np.array_equal(k1[new[b][at // page], 0, at % page], k0[c.table[b][who // page], 0, who % page])
+        assert c.kv.check_device() == 0
 
 
 def test_evict_odd_masses():
