@@ -10,6 +10,17 @@
 // split: a row's keys stay in one CTA, and its sums are divided and rounded on
 // their way out.
 //
+// Values at keys that only some rows see would bring an infinity or NaN into
+// the others' sums (0 times it): a warp looks the tiles on the diagonal through
+// before they go to the products, takes such values out and the rows that see
+// them get them back at the end.
+//
+// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 386 us (1425
+// TFLOP/s of what its rows see): 2750 cycles a tile pair, whose MMAs take 2048,
+// and some 6 k cycles a piece for its first scores, last sums and their way
+// out.  24 sequences of up to 1111 tokens, 44 heads of 64 on 4: 151 us; there a
+// piece has 3.4 key tiles on average, so those times are half of it.
+//
 // Work grows with a tile's place in its sequence, so the CTAs take the tiles by
 // falling place (a counting sort over the sequences' lengths, which every CTA
 // does for itself), to and fro: CTA c takes c, 2 P - 1 - c, 2 P + c, ...
@@ -48,13 +59,12 @@ struct Cfg {
   static constexpr int Q_AT = 0;                           // two row tiles
   static constexpr int RING_AT = 2 * SLOT;
   static constexpr int SORT = (3 * kBuckets + 4) * 4;
-  static constexpr int FIT = (226 * 1024 - RING_AT - SORT - 1024 - kSoftmaxWarps * 2048) / SLOT;
+  static constexpr int FIT = (226 * 1024 - RING_AT - SORT - 1024) / SLOT;
   static constexpr int SLOTS = FIT < 8 ? FIT / 2 * 2 : 8;  // even: keys, then values
   static constexpr int BAR_AT = RING_AT + SLOTS * SLOT;
   static constexpr int PIECE_AT = BAR_AT + 16 * SLOTS + 16 * kPieces + 192;
   static constexpr int SORT_AT = PIECE_AT + kPieces * (int)sizeof(Piece);
-  static constexpr int STAGE_AT = (SORT_AT + SORT + 127) / 128 * 128;  // 32 rows of 32 values a softmax warp, on their way out
-  static constexpr int SMEM = STAGE_AT + kSoftmaxWarps * 2048;
+  static constexpr int SMEM = SORT_AT + SORT;
   static constexpr int S_COL = 0, O_COL = 256;             // tensor-memory columns: S0 S1 O0 O1, 128 each
 };
 
@@ -373,15 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
     };
     // A row's token in the tile and head of its group; rows past the whole tokens are nobody's.
     const int row_tok = r / P.G, row_head = r - row_tok * P.G;
-    // The rows that this lane stores: 8 k + lane / 4 of the warp's 32.
-    int out_tok[4], out_head[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int x = 32 * w4 + 8 * k + lane / 4;
-      out_tok[k] = x / P.G;
-      out_head[k] = x - out_tok[k] * P.G;
-    }
-    const uint32_t stage = base + C::STAGE_AT + warp * 2048;
+    // whole sectors a lane where rows lie on them, halves else
+    const bool sectors = (((uintptr_t)P.out.ptr & 31) | (P.out.token_stride & 15) | (P.out.head_stride & 15)) == 0;
     unsigned n = 0;     // tiles of this row tile so far
     unsigned flat = 0;  // tiles of the CTA before the current piece
     unsigned turns = 0, done = 0;  // turns taken, pieces finished
@@ -491,13 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
       tc_fence_after();
       const bool in = row_tok < tokens && first + row_tok < cur.nrows;
       const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : __frcp_rn(sum);
-      // 32 values a row at a time through shared memory, so that four lanes store 64 bytes of a row
-      const int rest = min(tokens, cur.nrows - first);  // whole tokens of this sequence
-      E* out = static_cast<E*>(P.out.ptr) + (long long)(cur.tok0 + first) * P.out.token_stride + cur.head * P.G * P.out.head_stride +
-               8 * (lane & 3);
-      E* row[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) row[k] = out + out_tok[k] * P.out.token_stride + out_head[k] * P.out.head_stride;
+      E* row = static_cast<E*>(P.out.ptr) + (long long)(cur.tok0 + tok) * P.out.token_stride +
+               (long long)(cur.head * P.G + row_head) * P.out.head_stride;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 64) {
         uint32_t all[2][32];
@@ -506,20 +504,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         for (int b = 0; b < 2; ++b) {
           uint32_t (&o)[32] = all[b];
           if (odd && in) add_odd<E>(P, cur, sure0, vis, c0 + 32 * b, o);
-          __syncwarp();
+          if (in) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x[8];
+            for (int k = 0; k < 32; k += 16) {
+              uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(o[8 * k + j]) * inv;
-            sts128(stage + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4), pack8<E>(x));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int x = 8 * k + lane / 4;
-            const uint4 v = shared16(stage + x * 64 + (((lane & 3) ^ (x >> 1 & 3)) << 4));
-            if (out_tok[k] < rest) *reinterpret_cast<uint4*>(row[k] + c0 + 32 * b) = v;
+              for (int j = 0; j < 8; ++j) w[j] = pack2<E>(__uint_as_float(o[k + 2 * j]) * inv, __uint_as_float(o[k + 2 * j + 1]) * inv);
+              E* to = row + c0 + 32 * b + k;
+              if (sectors) {
+                store8(reinterpret_cast<float*>(to), w);
+              } else {
+                reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           }
         }
       }

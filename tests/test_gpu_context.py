@@ -163,6 +163,10 @@ def test_prompt_strides():
     pw.prompt_attend(q, k, v, ints(off), out)
     assert torch.equal(out, ref)
     check_prompt(q, k, v, off, out, rl)
+    # rows that begin inside a sector
+    wide = torch.full((131, 8, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+    pw.prompt_attend(q, k, v, ints(off), wide[..., 8:])
+    assert torch.equal(wide[..., 8:], ref) and (wide[..., :8] == 7).all()
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
