@@ -458,12 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         const float2 sc = make_float2(scale2, scale2), off = make_float2(-ref, -ref);
         if (t + 1 == tiles) {
-          // The last S is out of the queries' way: the next piece's are called in.  Whether values that are no numbers were
-          // taken out of this piece's is known once its last ones have been looked through.
+          // whether values that are no numbers were taken out of this piece's is known once its last ones have been looked
+          // through, and to be asked while they are still there
           const unsigned slot = 2 * (flat + t) + 1;
-          flat += cur.tile1;
-          have = advance();
-          if (have) call_q();
           ok = __all_sync(0xffffffffu, mbar_wait(clean + 8 * (slot % C::SLOTS), (slot / C::SLOTS) & 1, abort_flag, err));
           if (!ok) break;
           odd = *odd_seen;
@@ -489,6 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         }
       }
       if (!ok) break;
+      // The queries of the next piece with rows of this tile are called in before this one's sums come out.  Not before its
+      // last weights are handed over: that piece may be several ahead, and is announced only as the products go on.
+      flat += cur.tile1;
+      have = advance();
+      if (have) call_q();
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();

@@ -120,6 +120,25 @@ def test_prompt_many_tiles_a_cta():
         assert torch.equal(one, out[a:z]) and torch.equal(l1, lse[a:z])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_second_row_tiles_that_come_and_go(D):
+    # many pieces a CTA, most of whose second row tile is empty: the warpgroups go through the pieces at different paces
+    for seed, (B, hq, hk) in enumerate([(106, 16, 16), (160, 16, 16), (60, 64, 16)]):
+        rng = np.random.default_rng(40 + seed)
+        tokens = 128 // (hq // hk)
+        lens = np.where(rng.random(B) < (0.5, 0.15, 0.3)[seed], rng.integers(tokens + 1, 2 * tokens, B), rng.integers(1, tokens + 1, B))
+        off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+        q, k, v = prompt_case(rng, off[-1], hq, hk, D, torch.float16)
+        out, lse, err = run_prompt(q, k, v, off)
+        assert err == 0
+        for b in (0, B // 2, B - 1):
+            a, z = off[b], off[b + 1]
+            one, l1, _ = run_prompt(q[a:z], k[a:z], v[a:z], [0, z - a])
+            assert torch.equal(one, out[a:z]) and torch.equal(l1, lse[a:z])
+        a, z = off[1], off[2]
+        check_prompt(q[a:z, :1], k[a:z, :1], v[a:z, :1], [0, z - a], out[a:z, :1], lse[a:z, :1])
+
+
 def test_prompt_long_rows_against_32_bit_products():
     # 5000 tokens: rows sampled at tile borders, scores in 64 bits
     rng = np.random.default_rng(6)
