@@ -21,6 +21,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // order.  Bound by reading the keys once.  A lane reads 16 bytes of a key row
 // at a time, straight into the fragments of the product: the order of the
 // products inside a head does not matter as long as queries and keys share it.
+// Measured: 64 sequences to 4095, 8 heads of 128, 270 MB in 49.5 us (5.4 TB/s).
 
 // CTAs of kWeighWarps warps take kKeys keys: 64 by 8 where there are few, so that more SMs share them, 128 by 4 where
 // there are many, so that a CTA's start weighs less (5 sequences to 1500 8.5 and 15 us, 64 to 4095 54.1 and 49.7).
@@ -141,8 +142,8 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 16 / kWeighWarps) weigh_kern
 // A CTA a sequence.  Of the n - recent older tokens the budget - recent of the
 // largest masses stay: a radix search over the masses as ordered integers finds
 // the smallest that stays and how many of its equals do (the first ones), and a
-// scan in token order numbers them.  Latency bounds it; masses of up to
-// kSpan tokens stay in registers over its passes.
+// scan in token order numbers them.  Latency bounds it (64 sequences to 8190
+// 16 us); masses of up to kSpan tokens stay in registers over its passes.
 
 constexpr int kSelectThreads = 1024;
 constexpr int kOwn = 8;                          // masses a thread holds
@@ -312,9 +313,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
 // registers before any of the step is written, may move them inside the same
 // pages; the next step's rows and the slots of the one after are on their way
 // meanwhile.  A CTA takes the keys or the values of one head (or a 64-byte
-// column of them, where whole rows would leave SMs idle).  Bound by HBM; bulk
-// copies of a row each, tried instead, go out one in 12 cycles an SM, which is
-// less.
+// column of them, where whole rows would leave SMs idle).  Bound by HBM: 64
+// sequences to 2048 tokens of 8 heads of 128, 1.03 GB in 156 us (6.3 TB/s read
+// and written); bulk copies of a row each go out one in 12 cycles an SM, 176 us.
 
 constexpr int kMoveThreads = 128;
 

@@ -15,7 +15,7 @@
 // before they go to the products, takes such values out and the rows that see
 // them get them back at the end.
 //
-// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 386 us (1425
+// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 379 us (1450
 // TFLOP/s of what its rows see): 2750 cycles a tile pair, whose MMAs take 2048,
 // and some 6 k cycles a piece for its first scores, last sums and their way
 // out.  24 sequences of up to 1111 tokens, 44 heads of 64 on 4: 151 us; there a
