@@ -248,8 +248,9 @@ cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
 // of 16 bytes a lane into a ring of its own, one block ahead (tensor copies of
 // small pages cost a producer warp more instructions than this costs all four).
 // Bound by the instructions that turn codes into operands, ahead of the loads:
-// 64 sequences of up to 8190 tokens, 8 key heads of 128, 337 MB in 83 us (4.1
-// TB/s), 420 instructions for 16 keys and values.
+// 64 sequences of up to 8190 tokens, 8 key heads of 128, 337 MB in 95 us (3.5
+// TB/s), some 430 instructions for 16 keys and values (87 us with the weights
+// as one number, and errors of 1.5 times the output's own rounding, not 1.2).
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
@@ -528,9 +529,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
           }
         }
         const bool edge = first + 32 > sure;
-        // Weights as the second operand: keys 2 t4, + 1 (and + 8) of 16, row g.  In bf16, whose 8 bits would add to the values'
-        // own rounding, what a first number leaves of a weight goes into a second one and a second product.
-        constexpr int TERMS = __is_same(E, __half) ? 1 : 2;
+        // Weights as the second operand: keys 2 t4, + 1 (and + 8) of 16, row g.  Their rounding would add to the values' own,
+        // so what a first number leaves of a weight goes into a second one and a second product.
+        constexpr int TERMS = 2;
         uint32_t pf[NT][2][2][TERMS];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {

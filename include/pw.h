@@ -817,8 +817,8 @@ pw_status pw_kv4_load(pw_kv4_t kv, const int32_t* slots, int T, const pw_rows* k
  * Attention of a decode batch over the 4-bit cache: as pw_kv_attend without
  * prefixes (n_groups must be 0, PW_ERR_UNSUPPORTED otherwise; sequences may name
  * the same pages).  Keys enter the scores exactly as they are held, values
- * rounded to the heads' type; the weights e^s are rounded to fp16, or to the
- * sum of two bf16 numbers.
+ * rounded to the heads' type; the weights e^s enter as the sum of two numbers of
+ * it.
  */
 pw_status pw_kv4_attend_workspace_size(pw_kv4_t kv, int batch, int q_len, size_t* bytes);
 pw_status pw_kv4_attend(pw_kv4_t kv, const pw_attend_desc* desc, void* ws, size_t ws_bytes, void* stream);
