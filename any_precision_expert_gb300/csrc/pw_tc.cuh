@@ -284,16 +284,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(mbar)
       : "memory");
 }
-// The same with an L2 policy.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t mbar,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
-      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(mbar), "l"(policy)
-      : "memory");
-}
-
 // ---- of the attention kernels ----
 
 // fp16 or bf16 operands of 128 x n, B with its outer dimension contiguous or not.
