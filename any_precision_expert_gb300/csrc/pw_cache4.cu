@@ -118,12 +118,13 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, bool value) {
   }
   constexpr float kNear = 0.5f - 7.62939453125e-6f;
   if (far > kNear || !(inv < CUDART_INF_F)) {
-    // halves themselves are common where the type has few bits: a value less half-and-codes of steps is then 0, exactly
+    // halves themselves are common where the type has few bits: a value less half-and-codes of steps is then 0, exactly.
+    // Past 14.5 a half stays the 15 that it was cut to: 15.5 comes of a step that lost a thirty-first, and is even at 16.
     far = 0.f;
     w = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float d = x[k] - lo, q = fminf(d * inv, 15.f), half = floorf(q) + 0.5f;
+      const float d = x[k] - lo, q = fminf(d * inv, 15.f), half = fminf(floorf(q), 14.f) + 0.5f;
       const bool tie = fmaf(-half, step, d) == 0.f;
       const float r = (tie ? half : q) + kRound;
       far = fmaxf(far, tie ? 0.f : fabsf(q - (r - kRound)));

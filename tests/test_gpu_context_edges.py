@@ -1,0 +1,66 @@
+"""Ends of the types and sizes of the calls of test_gpu_context: the same oracle, bounds and equalities."""
+import numpy as np
+import pytest
+import torch
+
+import any_precision_expert_gb300 as pw
+from test_gpu_context import DEVICE_CHECK, TYPES, held, ints
+
+pytestmark = pytest.mark.gpu
+
+
+def append_and_load(x):
+    """What rows x [T, H, D] give back, as keys and as values of a 4-bit cache."""
+    T, H, D = x.shape
+    kv = pw.KvCache4.empty(-(-T // 16), H, H, 16, D, x.dtype)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    kv.append(x, x, slots)
+    k, v = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+    kv.load(slots, k, v)
+    assert kv.check_device() == 0
+    return k.cpu(), v.cpu()
+
+
+def same_as_definition(x):
+    """x: rows on the CPU."""
+    ref = held(x)[2]
+    for got in append_and_load(x.cuda()):
+        bad = torch.nan_to_num(got, nan=77.0) != torch.nan_to_num(ref, nan=77.0)
+        assert not bad.any(), f"{int(bad.sum())} values, first at {bad.nonzero()[0].tolist()}"
+    return ref
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt,unit,most", [("f16", 2.0 ** -24, 500), ("bf16", 2.0 ** -133, 120)])
+def test_four_bit_steps_of_few_bits(dt, unit, most, D):
+    # groups of whole multiples of a type's least number: their steps are rounded up or down by up to a half, quotients pass
+    # 15 (15.5 among them, where a step has lost a thirty-first) and many lie on halves; ranges below 8 have a step of 0
+    rng = np.random.default_rng(D)
+    rows = []
+    for n in range(241):
+        x = rng.integers(0, n + 1, (2, D // 32, 32))
+        x[..., rng.integers(32)] = 0
+        x[..., rng.integers(32)] = n  # may be the same place: a smaller range
+        rows.append(x + rng.integers(-most, most - n + 1, (2, D // 32, 1)))
+    x = np.concatenate(rows).reshape(-1, 1, D)
+    x[0, 0, :8], x[0, 0, 8:32] = [0, 31, 5, 3, 10, 12, 7, 1], 0
+    x = torch.from_numpy((x * unit).astype(np.float32)).to(TYPES[dt])
+    ref = same_as_definition(x)
+    assert torch.isfinite(ref).all() and (ref != 0).any()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_four_bit_quotients_on_halves(dt):
+    # least + (j + 1/2) step for every j, at steps of all sizes, and the numbers next to them
+    T = TYPES[dt]
+    rows = []
+    for e in (range(-24, 11) if dt == "f16" else range(-133, 120, 7)):
+        for least in (0.0, -8.0, -15.0):
+            g = np.concatenate([[least, least + 15], least + np.arange(15) + 0.5, np.arange(15) + least])
+            x = torch.from_numpy((g * 2.0 ** e).astype(np.float32)).to(T)
+            rows += [x, x.clone()]
+            near = x[2:17].view(torch.int16)
+            rows[-1][2:17] = (near + torch.from_numpy(np.random.default_rng(e + 200).integers(-1, 2, 15).astype(np.int16))).view(T)
+    x = torch.stack(rows)
+    x = torch.cat([x, x[torch.randperm(len(x), generator=torch.Generator().manual_seed(1))]], dim=1)[:, None]  # heads of 64
+    same_as_definition(torch.where(torch.isfinite(x), x, torch.zeros_like(x)))
