@@ -102,7 +102,11 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, bool value) {
   const uint32_t around = pack2<E>(about * (1.f - 2.384185791015625e-7f), about * (1.f + 2.384185791015625e-7f));
   uint32_t step_bits = around & 0xffff;
   if (around >> 16 != step_bits) step_bits = from_f32<E>(range / 15.f);
-  const float step = to_f32<E>(step_bits);
+  float step = to_f32<E>(step_bits);
+  // A top code that would stand for an infinity (of a value near the type's largest, and a step rounded up) takes the next
+  // lower step.  That is enough: rounding moved the step by half a last place, so 15 of the lower one stay below the largest.
+  constexpr float kOver = __is_same(E, __half) ? 65520.f : 3.39617752923046e38f;  // the least that rounds to infinity
+  if (fmaf(15.f, step, lo) >= kOver && step < CUDART_INF_F) step = to_f32<E>(--step_bits);
   float x[8];
   unpack8<E>(raw, x);
   float inv;

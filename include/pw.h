@@ -778,11 +778,13 @@ pw_status pw_token_logprobs(const pw_logprob_desc* desc, void* stream);
 /*
  * The paged cache held in 4 bits, in caller memory: 5 bits a value instead of
  * 16.  A head row is cut into groups of 32 values; a group keeps
- *   least = the least value,  step = (largest - least) / 15 rounded to the heads' type,
+ *   least = the least value,  step = (largest - least) / 15 rounded to the heads' type, or the
+ *       type's next lower number where least + 15 step would round to an infinity of the type,
  *   c = (value - least) / step rounded to a whole number (ties to even) in 0..15,
  *       0 where the step is 0 (differences and quotients are single fp32 operations)
  * and a value stands for least + c step.  A group with a value that is not a
- * finite number, or whose step would not be one, stands for NaN.
+ * finite number, or whose step would not be one, stands for NaN; finite groups
+ * stand for finite numbers of the type.
  *   k, v              device, 16-byte aligned, contiguous [n_pages][n_kv_heads]
  *                     [page_tokens][head_dim / 2] bytes of codes (their order inside
  *                     a row is the library's)

@@ -63,6 +63,12 @@ def quantise(x, to_type):
     with np.errstate(all="ignore"):
         least, most = g.min(-1), g.max(-1)
         step = to_type(((most - least).astype(f) / f(15)).astype(f)).astype(f)
+        # the next lower step where the top code would stand for no number of the type
+        over = np.isfinite(step) & np.isinf(to_type((least.astype(np.float64) + 15 * step.astype(np.float64)).astype(f)).astype(f))
+        lower = step
+        for j in range(24, 0, -1):  # the first that rounds below it is its neighbour
+            lower = np.where(lower < step, lower, to_type((step * f(1 - 2.0 ** -j)).astype(f)).astype(f))
+        step = np.where(over, lower, step)
         c = np.rint(((g - least[..., None]).astype(f) / step[..., None]).astype(f))
     c = np.where(step[..., None] > 0, np.clip(c, 0, 15), 0)
     bad = ~np.isfinite(g).all(-1) | ~np.isfinite(step)

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import any_precision_expert_gb300 as pw
-from test_gpu_context import DEVICE_CHECK, TYPES, held, ints
+from test_gpu_context import TYPES, Case4, held
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,60 @@ def test_four_bit_quotients_on_halves(dt):
     x = torch.stack(rows)
     x = torch.cat([x, x[torch.randperm(len(x), generator=torch.Generator().manual_seed(1))]], dim=1)[:, None]  # heads of 64
     same_as_definition(torch.where(torch.isfinite(x), x, torch.zeros_like(x)))
+
+
+def least_with_a_longer_step(dtype):
+    """The least value of a group up to the largest number whose step is rounded up so far that 15 of them pass it."""
+    return 0.0 if dtype == torch.float16 else 8 * 2.0 ** 120
+
+
+def ends_of_a_type(rng, dtype, n):
+    """n groups of 32 finite values that reach to a type's largest numbers or near them."""
+    most = torch.finfo(dtype).max
+    ends = [0.0, 1.0, -1.0, most, -most, most / 2, -most / 2, most * 0.999, -most * 0.99, most / 15]
+    rows = []
+    for i in range(n):
+        a, b = rng.choice(ends, 2)
+        g = np.clip(a + (b - a) * rng.random(32), -most, most)
+        g[rng.permutation(32)[:2]] = a, b
+        x = torch.from_numpy(g).to(dtype)
+        rows.append(torch.where(torch.isfinite(x), x, torch.full_like(x, most)))
+    rows[0][:], rows[0][3] = 0, most
+    rows[1][:], rows[1][4] = least_with_a_longer_step(dtype), most
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_four_bit_groups_at_the_ends_of_a_type_stay_numbers(dt):
+    # a top code would stand for an infinity where rounding has lengthened the step: the next lower step is taken
+    dtype = TYPES[dt]
+    x = ends_of_a_type(np.random.default_rng(7), dtype, 400).view(200, 1, 64)
+    ref = same_as_definition(x)
+    g, r = x.double().view(-1, 32), ref.double().view(-1, 32)
+    wide = g.max(-1).values - g.min(-1).values > torch.finfo(torch.float32).max  # bf16: no step in fp32, so no numbers
+    assert torch.isnan(r[wide]).all() and torch.isfinite(r[~wide]).all() and (dt == "bf16" or not wide.any())
+    step = (g.max(-1).values - g.min(-1).values)[~wide] / 15
+    u = torch.finfo(dtype).eps
+    # half a step, 15 times what the step has moved (2 half bits), and the rounding of what is loaded
+    bound = step * (0.5 + 15 * u) + u / 2 * torch.finfo(dtype).max
+    assert ((g - r).abs().amax(-1)[~wide] <= bound).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D,page", [(64, 8), (128, 16)])
+def test_four_bit_values_at_the_ends_of_a_type_reach_only_their_queries(D, page, dt):
+    rng = np.random.default_rng(D)
+    lens, ql = [3, 40, 130, 35], 3
+    c = Case4(rng, lens, 8, 2, D, page, TYPES[dt], ql, qscale=0.5)
+    clean, _ = c.run()
+    for b, n in enumerate(lens):
+        t = n - 1  # only a sequence's last query sees it
+        g = torch.full((2, D // 32, 32), least_with_a_longer_step(TYPES[dt]))
+        g[..., 5] = torch.finfo(TYPES[dt]).max
+        c.v[int(c.table[b][t // page]) * page + t % page] = g.view(2, D).to(TYPES[dt]).cuda()
+    c.kv.append(c.k, c.v, torch.arange(len(c.k), dtype=torch.int32, device="cuda"))
+    out, lse = c.run()
+    for b in range(len(lens)):
+        assert torch.equal(out[b * ql:b * ql + ql - 1], clean[b * ql:b * ql + ql - 1])
+    if dt == "f16":  # bf16's largest times weights of up to 2^14 leaves fp32
+        c.check(out, lse)
