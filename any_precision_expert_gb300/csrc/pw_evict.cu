@@ -183,11 +183,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   int2* moves = P.ws_moves + row;
   float* out = P.new_mass + (long long)b * P.mass_stride;
   float own[kOwn];
-  auto load = [&](int first) {
+  // positions are unsigned: a span's first may pass 2^31 where it ends the walk, and a span's last does before that
+  const unsigned candidates = older;
+  auto load = [&](unsigned first) {
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      const int i = first + k * kSelectThreads + tid;
-      own[k] = i < older ? mass[i] : 0.f;
+      const unsigned i = first + k * kSelectThreads + tid;
+      own[k] = i < candidates ? mass[i] : 0.f;
     }
   };
   // Token i stays, as number `at`.  Masses may go to their own place: `at` is never above i, and what a span's tokens
@@ -212,11 +214,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       __syncthreads();
       const unsigned prefix = s_prefix, want = s_left;
 #pragma unroll 1
-      for (int first = 0; first < older; first += kSpan) {
+      for (unsigned first = 0; first < candidates; first += kSpan) {
         if (older > kSpan) load(first);
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
-          if (first + k * kSelectThreads + tid >= older) break;
+          if (first + k * kSelectThreads + tid >= candidates) break;
           const unsigned key = mass_key(own[k]);
           if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
         }
@@ -249,15 +251,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   }
   unsigned more_before = 0, same_before = 0;  // in the spans before
 #pragma unroll 1
-  for (int first = 0; first < older; first += kSpan) {
+  for (unsigned first = 0; first < candidates; first += kSpan) {
     if (older > kSpan) load(first);
     unsigned at[kOwn];  // heavier and equal tokens of the warp's 32 in front of this thread's, with its own flags
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-      const int i = first + k * kSelectThreads + tid;
+      const bool in = first + k * kSelectThreads + tid < candidates;
       const unsigned key = mass_key(own[k]);
-      const unsigned more = __ballot_sync(0xffffffffu, i < older && (all || key > bar));
-      const unsigned same = __ballot_sync(0xffffffffu, i < older && !all && key == bar);
+      const unsigned more = __ballot_sync(0xffffffffu, in && (all || key > bar));
+      const unsigned same = __ballot_sync(0xffffffffu, in && !all && key == bar);
       const unsigned front = (1u << lane) - 1;
       at[k] = __popc(more & front) | __popc(same & front) << 8 | (more >> lane & 1) << 16 | (same >> lane & 1) << 17;
       if (lane == 0) count[k * 32 + warp] = __popc(more) | __popc(same) << 16;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import any_precision_expert_gb300 as pw
-from test_gpu_context import TYPES, Case4, held
+from test_gpu_context import TYPES, Case4, held, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,30 @@ def test_four_bit_values_at_the_ends_of_a_type_reach_only_their_queries(D, page,
         assert torch.equal(out[b * ql:b * ql + ql - 1], clean[b * ql:b * ql + ql - 1])
     if dt == "f16":  # bf16's largest times weights of up to 2^14 leaves fp32
         c.check(out, lse)
+
+
+def test_evict_the_most_tokens_that_a_table_may_have():
+    # 2^31 - 4096 masses, and a table that names four pages over and over; the heavy ones lie at the ends of the range
+    n, page, budget, recent = 0x7ffff000, 1024, 40, 3
+    rng = np.random.default_rng(3)
+    k, v = (torch.from_numpy(rng.standard_normal((5, 1, page, 64)).astype(np.float16)).cuda() for _ in range(2))
+    k0, v0 = k.clone(), v.clone()
+    kv = pw.KvCache(k, v, n_heads=1)
+    table = (torch.arange(n // page, dtype=torch.int32, device="cuda") % 4)[None].contiguous()
+    mass = torch.zeros(1, n, device="cuda")
+    heavy = np.unique(np.concatenate([rng.integers(0, n, 20), [0, n - 4, n - 5, n - 8192, n - 8193, n - 12289, 2 ** 30]]))
+    heavy = heavy[heavy < n - recent]
+    mass[0, torch.from_numpy(heavy).cuda()] = torch.from_numpy(rng.permutation(len(heavy)).astype(np.float32) + 1).cuda()
+    ends = mass[0, -recent:] = torch.tensor([0.25, 0.0, 0.5], device="cuda")
+    few = [int(x) for x in range(1, budget) if x not in heavy][:budget - recent - len(heavy)]  # of equal masses the first
+    who = sorted(heavy.tolist() + few) + list(range(n - recent, n))
+    was = mass[0, torch.tensor(who, device="cuda")].clone()
+    lens, new, kept = ints([n]), ints([[4]]), ints(np.zeros((1, budget)))
+    ws = torch.empty(kv.evict_workspace_size(1, budget), dtype=torch.uint8, device="cuda")
+    kv.evict(table, lens, mass, budget, ws, recent=recent, new_table=new, kept=kept)
+    assert kv.check_device() == 0 and lens.tolist() == [budget]
+    assert kept[0].tolist() == who and torch.equal(mass[0, :budget], was) and torch.equal(was[-recent:], ends)
+    assert not mass[0, budget:].any()
+    at = torch.tensor(who, device="cuda")
+    for now, then in ((k, k0), (v, v0)):
+        assert torch.equal(now[4, 0, :budget], then[at // page % 4, 0, at % page]) and torch.equal(now[:4], then[:4])
