@@ -136,6 +136,7 @@ _SIGS = {
     "pw_kv_attend": (i32, [vp, vp, vp, sz, vp]),
     "pw_verify_draft": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
     "pw_prompt_attend": (i32, [vp, vp, vp]),
+    "pw_prompt_check_device": (i32, [vp]),
     "pw_token_logprobs": (i32, [vp, vp]),
     "pw_kv4_create": (i32, [vp, vp, vp, vp, vp, vp, C.POINTER(vp)]),
     "pw_kv4_destroy": (i32, [vp]),

@@ -62,6 +62,13 @@ extern "C" pw_status pw_prompt_attend(const pw_heads* heads, const pw_prompt_des
   return launched(launch_prompt(P, heads->dtype, heads->head_dim, as_stream(stream)));
 }
 
+extern "C" pw_status pw_prompt_check_device(void* stream) {
+  if (host_sim()) return PW_ERR_UNSUPPORTED;
+  int* word = nullptr;
+  const cudaError_t e = prompt_error_word(&word);
+  return e == cudaSuccess ? read_error(word, as_stream(stream)) : record_cuda_error(e);
+}
+
 extern "C" pw_status pw_token_logprobs(const pw_logprob_desc* a, void* stream) {
   if (!a || bad_tokens(a->T) || a->V < 1 || a->V > (1 << 24)) return PW_ERR_INVALID_ARG;
   if (a->dtype != PW_F16 && a->dtype != PW_BF16 && a->dtype != PW_F32) return PW_ERR_INVALID_ARG;

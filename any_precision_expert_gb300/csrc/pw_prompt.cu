@@ -72,7 +72,7 @@ struct PromptMaps {
   CUtensorMap q, k, v;
 };
 
-__device__ int prompt_err;  // the error word of calls without one
+__device__ int prompt_err;  // the error word of calls without one, read by pw_prompt_check_device
 
 // Tokens of a sequence, inside the call's.
 struct Span {
@@ -661,6 +661,8 @@ cudaError_t launch_typed(const PromptParams& P, const PromptMaps& maps, cudaStre
 }
 
 }  // namespace
+
+cudaError_t prompt_error_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), prompt_err); }
 
 cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s) {
   PromptMaps maps;

@@ -181,6 +181,7 @@ cudaError_t launch_verify(const VerifyParams& P, cudaStream_t s);
 cudaError_t launch_weigh(const WeighParams& P, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& P, cudaStream_t s);
 cudaError_t launch_prompt(const PromptParams& P, int dtype, int d, cudaStream_t s);
+cudaError_t prompt_error_word(int** word);  // the current device's, of calls that bring none
 cudaError_t launch_logprobs(const LogprobParams& P, int dtype, cudaStream_t s);
 cudaError_t launch_rows4(const Row4Params& P, bool load, cudaStream_t s);
 size_t attend4_ws_bytes(const KvView& kv, int B, int ql);

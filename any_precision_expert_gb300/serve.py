@@ -215,10 +215,21 @@ class KvCache4:
 def prompt_attend(q, k, v, offsets, out, scale: float = None, lse=None, err=None, stream=None):
     """Causal attention of packed prompts over their own keys (pw_prompt_attend): q, out [T, Hq, D], k, v [T, Hkv, D] of
     one type (float16 or bfloat16) with contiguous heads of 64 or 128, offsets int32 [B + 1]: sequence b is rows offsets[b]
-    .. offsets[b + 1] - 1.  lse: optional fp32 [T, Hq]; err: optional int32 [1] error word."""
+    .. offsets[b + 1] - 1.  lse: optional fp32 [T, Hq]; err: optional int32 [1] error word (prompt_check_device reads the one
+    of calls without)."""
     st = _pw_torch.prompt(q, k, v, offsets, out, float("nan") if scale is None else scale, scale is None, lse, err, stream)
     if st:
         check(st, "pw_prompt_attend")
+
+
+def prompt_check_device(device=None, stream=None) -> int:
+    """Read and clear the error word that a device's prompt_attend calls without err share (pw_prompt_check_device;
+    synchronises the stream): 0, PW_ERR_TIMEOUT (6, rows may be unwritten) or PW_ERR_DEVICE_CHECK (7).  device: the current
+    one when None."""
+    if not torch.cuda.is_available():
+        return lib.pw_prompt_check_device(_s(stream))
+    with torch.cuda.device(device):
+        return lib.pw_prompt_check_device(_s(stream))
 
 
 def token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, err=None, stream=None):

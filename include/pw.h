@@ -725,7 +725,8 @@ pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int
  *            two sequences leave its results unspecified)
  *   q, k, v  strides of at least a row where there is more than one row along
  *            them (PW_ERR_INVALID_ARG otherwise)
- *   err      device int32 or NULL: the call's error word
+ *   err      device int32 or NULL: the call's error word.  Calls without one share a word of
+ *            their device, which pw_prompt_check_device reads
  * Rows in front of the first sequence, behind the last and between two are left as they
  * were.  out must not overlap q, k or v.  No workspace.
  */
@@ -739,6 +740,15 @@ typedef struct {
   int32_t* err;
 } pw_prompt_desc;
 pw_status pw_prompt_attend(const pw_heads* heads, const pw_prompt_desc* desc, void* stream);
+
+/*
+ * Read and clear the error word of the current device's prompt calls that
+ * brought none, behind what `stream` holds (synchronises it): PW_OK,
+ * PW_ERR_TIMEOUT (a wait ran out: rows of some call may be unwritten) or
+ * PW_ERR_DEVICE_CHECK (offsets were clamped).  Calls on streams that `stream` does not wait for
+ * may still run.
+ */
+pw_status pw_prompt_check_device(void* stream);
 
 /*
  * Log probabilities of given tokens under rows of logits x, ln p_i = x_i -

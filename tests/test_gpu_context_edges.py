@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import any_precision_expert_gb300 as pw
-from test_gpu_context import TYPES, Case4, held, ints
+from test_gpu_context import DEVICE_CHECK, TYPES, Case4, held, ints, prompt_case, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,22 @@ def test_evict_the_most_tokens_that_a_table_may_have():
     at = torch.tensor(who, device="cuda")
     for now, then in ((k, k0), (v, v0)):
         assert torch.equal(now[4, 0, :budget], then[at // page % 4, 0, at % page]) and torch.equal(now[:4], then[:4])
+
+
+# ---- prompts ------------------------------------------------------------------
+
+def test_prompt_calls_without_an_error_word_share_one():
+    q, k, v = prompt_case(np.random.default_rng(11), 50, 2, 1, 64, torch.float16)
+    ref, _, _ = run_prompt(q, k, v, [0, 20, 50])
+    out = torch.empty_like(ref)
+    pw.prompt_check_device()
+    pw.prompt_attend(q, k, v, ints([0, 20, 51]), out)
+    assert torch.equal(out, ref)
+    assert pw.prompt_check_device() == DEVICE_CHECK and pw.prompt_check_device(q.device) == 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    pw.prompt_attend(q, k, v, ints([-1, 20, 50]), out, stream=s)
+    assert pw.prompt_check_device(stream=s) == DEVICE_CHECK
+    pw.prompt_attend(q, k, v, ints([0, 20, 50]), out)
+    _, _, err = run_prompt(q, k, v, [0, 20, 51])  # a call's own word is its own
+    assert err != 0 and pw.prompt_check_device() == 0
