@@ -97,20 +97,33 @@ struct PromptWalk {
   int* start;   // [kBuckets] row tiles in the buckets above; [kBuckets]: all row tiles
   int shift, turn, bucket, b0, before;
 
+  __device__ __forceinline__ unsigned& held() { return reinterpret_cast<unsigned*>(start)[kBuckets + 1]; }  // tokens of all sequences
   __device__ __forceinline__ void clear(int tid) {
     for (int i = tid; i < kBuckets; i += kThreads) full[i] = rest[i] = 0;
+    if (tid == 0) held() = 0;
   }
   __device__ __forceinline__ void count(const PromptParams& P, int tid, int* err) {
+    int tokens = 0;  // of this thread's sequences, at most 11 of 2^20
     for (int b = tid; b < P.B; b += kThreads) {
-      const int tiles = row_tiles(P, span_of(P, b, blockIdx.x == 0 ? err : nullptr).n);
+      const Span s = span_of(P, b, blockIdx.x == 0 ? err : nullptr);
+      const int tiles = row_tiles(P, s.n);
+      tokens += s.n;
       if (tiles > 0) {
         atomicAdd(&full[tiles >> shift], 1);
         atomicAdd(&rest[tiles >> shift], tiles & ((1 << shift) - 1));
       }
     }
+    if (tokens > 0) atomicAdd(&held(), (unsigned)min(tokens, P.T + 1));  // kThreads of them stay below 2^32
   }
+  // Sequences that hold more than the call's tokens overlap: descending offsets could ask for 4096 times a call's work,
+  // more row tiles than the ranks count in 32 bits.  Nothing of such a call runs.
+  __device__ __forceinline__ bool overlap(const PromptParams& P) { return held() > (unsigned)P.T; }
   // One warp; lane 0 holds the highest buckets.
-  __device__ __forceinline__ void sort(int lane) {
+  __device__ __forceinline__ void sort(const PromptParams& P, int lane) {
+    if (overlap(P)) {
+      for (int i = lane; i <= kBuckets; i += 32) start[i] = 0;
+      return;
+    }
     constexpr int PER = kBuckets / 32;
     auto scan = [&](int sum) {  // what the lanes before this one hold
       int x = sum;
@@ -361,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  if (tid == 0 && blockIdx.x == 0 && walk.overlap(P)) atomicExch(err, kErrOffsets);
 
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -532,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftmaxWarps) {
       // ---- producer: keys and values of a tile take one ring slot each ----
-      walk.sort(lane);
+      walk.sort(P, lane);
       __syncwarp();
       walk.begin();
       unsigned x = 0;  // slots filled so far

@@ -722,7 +722,8 @@ pw_status pw_verify_draft(const float* target_p, const float* draft_p, const int
  * heads' type for the products with the values.
  *   offsets  device int32 [batch + 1], not descending, in [0, T]; others are
  *            clamped to that and flagged (descending ones that put a row into
- *            two sequences leave its results unspecified)
+ *            two sequences leave its results unspecified; where they make
+ *            sequences of more than T rows together, no row is written)
  *   q, k, v  strides of at least a row where there is more than one row along
  *            them (PW_ERR_INVALID_ARG otherwise)
  *   err      device int32 or NULL: the call's error word.  Calls without one share a word of

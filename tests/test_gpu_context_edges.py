@@ -167,3 +167,23 @@ def test_prompt_calls_without_an_error_word_share_one():
     pw.prompt_attend(q, k, v, ints([0, 20, 50]), out)
     _, _, err = run_prompt(q, k, v, [0, 20, 51])  # a call's own word is its own
     assert err != 0 and pw.prompt_check_device() == 0
+
+
+def test_prompt_offsets_that_ask_for_rows_over_and_over():
+    q, k, v = prompt_case(np.random.default_rng(12), 50, 2, 1, 64, torch.float16)
+    ref, _, _ = run_prompt(q, k, v, [0, 50])
+    for off in ([0, 50, 0, 50], [0, 30, 10, 50], [0, 50, 49, 50], [0, 50] * 2048):
+        out, lse, err = run_prompt(q, k, v, off)
+        assert err != 0 and (out == 7).all() and (lse == 7).all()
+    out, _, err = run_prompt(q, k, v, [0, 20, 5, 35])  # rows 5 .. 19 twice, but 50 in all: the others as they are asked for
+    own, _, _ = run_prompt(q[5:35], k[5:35], v[5:35], [0, 30])
+    assert err != 0 and torch.equal(out[:5], ref[:5]) and torch.equal(out[20:35], own[15:]) and (out[35:] == 7).all()
+    # 2^30 pairs of row tiles of up to 8192 key tiles each, of one buffer's overlapping rows
+    T, B, hq = 1 << 20, 4096, 128
+    buf = torch.zeros((T + hq) * 64, dtype=torch.float16, device="cuda")
+    rows = lambda h: buf.as_strided((T, h, 64), (64, 64, 1))  # noqa: E731
+    out = torch.full_like(buf, 7.0).as_strided((T, hq, 64), (64, 64, 1))
+    err = ints([0])
+    pw.prompt_attend(rows(hq), rows(1), rows(1), ints([0, T] * (B // 2) + [0]), out, err=err)
+    torch.cuda.synchronize()
+    assert err.item() != 0 and (out[:, 0] == 7).all()
