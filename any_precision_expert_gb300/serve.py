@@ -10,6 +10,7 @@ library refuses raises PwError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import torch
@@ -19,6 +20,11 @@ from ._lib import Heads, Kv4Desc, KvDesc, RotaryDesc, check, lib
 from .api import _p, _s
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _on(cache):
+    """The device of a cache's tensor as the current one: its stream orders the error word, its SMs set the scratch's size."""
+    return torch.cuda.device(cache.device) if cache.is_cuda else contextlib.nullcontext()
 
 
 class Rotary:
@@ -83,7 +89,8 @@ class KvCache:
 
     def check_device(self, stream=None) -> int:
         """Read and clear the error word (synchronises): 0 or PW_ERR_DEVICE_CHECK (7)."""
-        return lib.pw_kv_check_device(self.handle, _s(stream))
+        with _on(self.k):
+            return lib.pw_kv_check_device(self.handle, _s(stream))
 
     def append(self, k, v, slots, rotary: Rotary = None, positions=None, q=None, q_out=None, stream=None):
         """Append keys (normed and rotated when rotary is given) and values [T, Hkv, D] at int32 slots [T], and norm
@@ -95,8 +102,9 @@ class KvCache:
 
     def attend_workspace_size(self, batch: int, q_len: int = 1, n_groups: int = 0) -> int:
         n = C.c_size_t(0)
-        check(lib.pw_kv_attend_workspace_size(self.handle, batch, q_len, n_groups, C.byref(n)),
-              "pw_kv_attend_workspace_size")
+        with _on(self.k):
+            check(lib.pw_kv_attend_workspace_size(self.handle, batch, q_len, n_groups, C.byref(n)),
+                  "pw_kv_attend_workspace_size")
         return n.value
 
     def attend(self, q, table, lens, out, ws, q_len: int = 1, scale: float = None, prefix_table=None,
@@ -183,7 +191,8 @@ class KvCache4:
 
     def check_device(self, stream=None) -> int:
         """Read and clear the error word (synchronises): 0 or PW_ERR_DEVICE_CHECK (7)."""
-        return lib.pw_kv4_check_device(self.handle, _s(stream))
+        with _on(self.k):
+            return lib.pw_kv4_check_device(self.handle, _s(stream))
 
     def append(self, k, v, slots, stream=None):
         """Cut keys and values [T, Hkv, D] (normed and rotated already: qk_norm_rope) to 4 bits and put them at int32 slots
@@ -200,7 +209,8 @@ class KvCache4:
 
     def attend_workspace_size(self, batch: int, q_len: int = 1) -> int:
         n = C.c_size_t(0)
-        check(lib.pw_kv4_attend_workspace_size(self.handle, batch, q_len, C.byref(n)), "pw_kv4_attend_workspace_size")
+        with _on(self.k):
+            check(lib.pw_kv4_attend_workspace_size(self.handle, batch, q_len, C.byref(n)), "pw_kv4_attend_workspace_size")
         return n.value
 
     def attend(self, q, table, lens, out, ws, q_len: int = 1, scale: float = None, lse=None, stream=None):
