@@ -221,15 +221,26 @@ __global__ void __launch_bounds__(kRowThreads) row4_kernel(const Row4Params P) {
 template <typename E, int D, int U>
 cudaError_t launch_unrolled(const Row4Params& P, bool load, cudaStream_t s) {
   constexpr int kRows = kRowThreads / 32 * (32 / (D / 8)) * U;
-  const long long blocks = ((long long)P.T * 2 * P.kv.hkv + kRows - 1) / kRows;
-  if (blocks > 0x7fffffffll || blocks * kRows > 0xffffff00ll) return cudaErrorInvalidConfiguration;
-  const Launch at(dim3((unsigned)blocks), kRowThreads, 0, s);
+  const unsigned blocks = (unsigned)(((long long)P.T * 2 * P.kv.hkv + kRows - 1) / kRows);
+  const Launch at(dim3(blocks), kRowThreads, 0, s);
   return load ? cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, true, U>, P) : cudaLaunchKernelEx(&at.cfg, row4_kernel<E, D, false, U>, P);
 }
 template <typename E, int D>
 cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
   const bool few = (long long)P.T * 2 * P.kv.hkv * D < (1 << 20);
-  return few ? launch_unrolled<E, D, 1>(P, load, s) : launch_unrolled<E, D, 4>(P, load, s);
+  if (few) return launch_unrolled<E, D, 1>(P, load, s);
+  // rows are counted in 32 bits: as many tokens a launch as stay below that
+  const int most = (int)(0xfff00000u / (2u * P.kv.hkv));
+  cudaError_t e = cudaSuccess;
+  for (int t = 0; t < P.T && e == cudaSuccess; t += most) {
+    Row4Params Q = P;
+    Q.T = P.T - t < most ? P.T - t : most;
+    Q.slots += t;
+    Q.k.ptr = static_cast<E*>(P.k.ptr) + t * P.k.token_stride;
+    Q.v.ptr = static_cast<E*>(P.v.ptr) + t * P.v.token_stride;
+    e = launch_unrolled<E, D, 4>(Q, load, s);
+  }
+  return e;
 }
 
 // ---- attention ------------------------------------------------------------------

@@ -150,6 +150,30 @@ def test_evict_the_most_tokens_that_a_table_may_have():
         assert torch.equal(now[4, 0, :budget], then[at // page % 4, 0, at % page]) and torch.equal(now[:4], then[:4])
 
 
+def test_four_bit_append_and_load_of_more_rows_than_32_bits_count():
+    # 2^20 tokens of 2049 key heads: one token's row of each head, again and again, of which the slots take three
+    T, hk, D = 1 << 20, 2049, 64
+    rng = np.random.default_rng(1)
+    one = torch.from_numpy(rng.standard_normal((1, hk, D)).astype(np.float16)).cuda()
+    kv = pw.KvCache4.empty(1, hk, hk, 8, D)
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    for slot, t in enumerate((0, T // 2, T - 1)):
+        slots[t] = slot
+    k = one.expand(T, hk, D)
+    kv.append(k, -one.expand(T, hk, D), slots)
+    back, vback = torch.full((4, hk, D), 9.0, dtype=torch.float16, device="cuda"), torch.full((4, hk, D), 9.0, dtype=torch.float16, device="cuda")
+    kv.load(ints([0, 1, 2, 3]), back, vback)
+    for got, x in ((back, one), (vback, -one)):
+        assert torch.equal(got[:3].cpu(), held(x)[2].expand(3, hk, D)) and not got[3].any()
+    # a load of the same many tokens, all into one row of places, of which one is asked for
+    slots[:] = -1
+    slots[T - 2] = 1
+    ko, vo = torch.full_like(one, 9.0), torch.full_like(one, 9.0)
+    kv.load(slots, ko.expand(T, hk, D), vo.expand(T, hk, D))
+    assert torch.equal(ko[0], back[1]) and torch.equal(vo[0], vback[1])
+    assert kv.check_device() == 0
+
+
 # ---- prompts ------------------------------------------------------------------
 
 def test_prompt_calls_without_an_error_word_share_one():
