@@ -831,7 +831,8 @@ pw_status pw_kv4_load(pw_kv4_t kv, const int32_t* slots, int T, const pw_rows* k
  * prefixes (n_groups must be 0, PW_ERR_UNSUPPORTED otherwise; sequences may name
  * the same pages).  Keys enter the scores exactly as they are held, values
  * rounded to the heads' type; the weights e^s enter as the sum of two numbers of
- * it.
+ * it.  Products of queries up to 2^60 with keys and values up to 2^80 in
+ * magnitude stay inside fp32 (bf16 heads may hold larger ones).
  */
 pw_status pw_kv4_attend_workspace_size(pw_kv4_t kv, int batch, int q_len, size_t* bytes);
 pw_status pw_kv4_attend(pw_kv4_t kv, const pw_attend_desc* desc, void* ws, size_t ws_bytes, void* stream);

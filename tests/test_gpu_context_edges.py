@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import any_precision_expert_gb300 as pw
-from test_gpu_context import DEVICE_CHECK, TYPES, Case4, held, ints, prompt_case, run_prompt
+from test_gpu_context import DEVICE_CHECK, TYPES, Case4, check_prompt, held, ints, prompt_case, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -123,6 +123,19 @@ def test_four_bit_values_at_the_ends_of_a_type_reach_only_their_queries(D, page,
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("qe,ke,ve", [(-100, 80, 80), (60, -61, -100), (-100, 100, -20), (0, 0, 80)])
+@pytest.mark.parametrize("D,ql", [(64, 3), (128, 1)])
+def test_four_bit_attention_of_large_and_small_numbers(D, ql, qe, ke, ve):
+    # bf16 has the exponents of fp32: powers of two that cancel in the scores change nothing
+    c = Case4(np.random.default_rng(5), [200, 3, 33], 8, 2, D, 16, torch.bfloat16, ql)
+    c.scale *= 2.0 ** -(qe + ke)
+    c.k *= 2.0 ** ke
+    c.v *= 2.0 ** ve
+    c.q *= 2.0 ** qe
+    c.kv.append(c.k, c.v, torch.arange(len(c.k), dtype=torch.int32, device="cuda"))
+    c.check(*c.run())
+
+
 def test_evict_the_most_tokens_that_a_table_may_have():
     # 2^31 - 4096 masses, and a table that names four pages over and over; the heavy ones lie at the ends of the range
     n, page, budget, recent = 0x7ffff000, 1024, 40, 3
@@ -211,3 +224,23 @@ def test_prompt_offsets_that_ask_for_rows_over_and_over():
     pw.prompt_attend(rows(hq), rows(1), rows(1), ints([0, T] * (B // 2) + [0]), out, err=err)
     torch.cuda.synchronize()
     assert err.item() != 0 and (out[:, 0] == 7).all()
+
+
+@pytest.mark.parametrize("hq,hk,T,D", [(64, 1, 2300, 64), (128, 1, 2600, 128), (256, 2, 1500, 64)])
+def test_prompt_places_in_buckets_of_several_tiles(hq, hk, T, D):
+    # 2 tokens and 1 a row tile: more than 512 pairs of row tiles fit the call's tokens, so that its places are sorted 2 and
+    # 4 to a bucket; alone, a sequence is sorted by itself
+    rng = np.random.default_rng(T)
+    lens = [T // 2 + 3, 0, 1] + rng.integers(1, 60, 12).tolist() + [5, 2, T // 6]
+    off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    assert off[-1] <= T
+    q, k, v = prompt_case(rng, T, hq, hk, D, torch.float16)
+    out, lse, err = run_prompt(q, k, v, off)
+    assert err == 0 and (out[off[-1]:] == 7).all()
+    for a, z in zip(off[:-1], off[1:]):
+        if z > a:
+            one, l1, _ = run_prompt(q[a:z], k[a:z], v[a:z], [0, z - a])
+            assert torch.equal(one, out[a:z]) and torch.equal(l1, lse[a:z])
+    a, z = off[5], off[9]
+    some = [x - a for x in off[5:10]]
+    check_prompt(q[a:z, :2], k[a:z, :1], v[a:z, :1], some, out[a:z, :2], lse[a:z, :2])
