@@ -420,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// How the prefix and the suffix kernel cut rows: rows and heads of a segment, CTAs, and whether it is the tcgen05 one.
 // Warps that share four rows' pieces, by the number of rows (query tokens x heads), 16 up to four rows an SM: a lone
 // sequence on a long prefix has a piece from every CTA (measured: 20 rows of 300 pieces, the call 41 us with 4 warps, 31
 // with 16), many rows fill the GPU by themselves (8192 rows: the call 136 us with 1, 142 with 4).

@@ -50,8 +50,8 @@ __device__ __forceinline__ uint16_t from_f32(float x) {
 // warp has U steps of rows in flight (one while there are few).  Quotients are
 // products with the step's reciprocal, off by less than 2^-17, and exact
 // divisions where one falls that near to a half.  Measured: 8191 tokens of 16
-// heads of 128, append 38 us (128 instructions a lane and eight values), load
-// 20 (4.4 TB/s).
+// heads of 128, append 37 us in bf16 (some 265 instructions a lane and eight
+// values issued; 32 us in fp16, where halves are rarer), load 21 (4.2 TB/s; 147).
 
 constexpr int kRowThreads = 128;
 
@@ -227,6 +227,9 @@ cudaError_t launch_unrolled(const Row4Params& P, bool load, cudaStream_t s) {
 }
 template <typename E, int D>
 cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
+  // One step a warp below 2^20 values, four from there (append / load, us): of 2^18 values 1.6 / 1.5 and 2.9 / 2.0, of 2^20
+  // 3.25 / 2.4 and 3.3 / 2.3, of 2^22 6.0 / 4.5 and 6.5 / 5.6, of 2^24 20.1 / 16.8 and 22.7 / 11.2, of 2^25 39.7 / 33.2 and
+  // 37.1 / 21.0.
   const bool few = (long long)P.T * 2 * P.kv.hkv * D < (1 << 20);
   if (few) return launch_unrolled<E, D, 1>(P, load, s);
   // rows are counted in 32 bits: as many tokens a launch as stay below that
@@ -264,9 +267,10 @@ cudaError_t launch_rows(const Row4Params& P, bool load, cudaStream_t s) {
 // of 16 bytes a lane into a ring of its own, one block ahead (tensor copies of
 // small pages cost a producer warp more instructions than this costs all four).
 // Bound by the instructions that turn codes into operands, ahead of the loads:
-// 64 sequences of up to 8190 tokens, 8 key heads of 128, 337 MB in 95 us (3.5
-// TB/s), some 430 instructions for 16 keys and values (87 us with the weights
-// as one number, and errors of 1.5 times the output's own rounding, not 1.2).
+// 64 sequences of up to 8190 tokens, 8 key heads of 128, 337 MB in 95 to 99 us
+// (3.5 TB/s), some 430 instructions for 16 keys and values (8 % less with the
+// weights as one number, and errors of 1.5 times those of rounding the output
+// alone, not 1.2 to 1.4).
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
     attend4_kernel(const AttendParams P, const Kv4View kv, const AttendWork W) {
   using C = Cfg<D, NT>;
   constexpr int SET = 8 * NT, ROWS = SET * MT, KS = kWarps / MT, KPW = kTile / KS, NG = D / 32, VW = D / 64, MV = D / 16;
-  using Walk = AttendWalk<ROWS, kTile, 1, 1, 2>;  // with 1 / 2 / 3 / 5 tiles a CTA at least, one sequence of 19327 tokens 17.7 / 16.4 / 16.3 / 18.1 us
+  using Walk = AttendWalk<ROWS, kTile, 1, 1, 2>;  // with 1 / 3 / 5 tiles a CTA at least one sequence of 19327 tokens took 8 / 0 / 10 % longer
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -21,10 +21,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 // order.  Bound by reading the keys once.  A lane reads 16 bytes of a key row
 // at a time, straight into the fragments of the product: the order of the
 // products inside a head does not matter as long as queries and keys share it.
-// Measured: 64 sequences to 4095, 8 heads of 128, 270 MB in 49.5 us (5.4 TB/s).
+// Measured: 64 sequences to 4095, 8 heads of 128, 270 MB in 49.6 us (5.4 TB/s).
+// The grid goes by the tables' and masses' width, and a CTA past a sequence's
+// length reads that and leaves: behind rows of 32768 / 131072 / 2^20 positions
+// the same call takes 58 / 86 / 526 us, 64 sequences to 200 20 / 68 / 526
+// instead of 15.  More than 16 rows a key head read the keys once for every 16.
 
 // CTAs of kWeighWarps warps take kKeys keys: 64 by 8 where there are few, so that more SMs share them, 128 by 4 where
-// there are many, so that a CTA's start weighs less (5 sequences to 1500 8.5 and 15 us, 64 to 4095 54.1 and 49.7).
+// there are many, so that a CTA's start weighs less (5 sequences to 1500 took 1.8 times as long in the
+// second shape, 64 to 4095 9 % longer in the first).
 template <typename E, int D, int kKeys, int kWeighWarps>
 __global__ void __launch_bounds__(kWeighWarps * 32, 16 / kWeighWarps) weigh_kernel(const WeighParams P) {
   __shared__ float part[kWeighWarps][kKeys];

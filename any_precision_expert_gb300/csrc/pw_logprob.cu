@@ -7,18 +7,24 @@
 //
 // Bound: every logit is read once, HBM for long prompts, the chain of loads,
 // maxima and joins for a few rows.  Measured: 2047 rows of 131072 bf16 logits
-// with 8 alternatives, 537 MB, in 106 us (5.1 TB/s; 95 without alternatives),
-// where it issues 79 million instructions, 77 us of issue slots; 8 rows of 32000
-// in 7.5 us.  A thread holds kVecs 16-byte vectors of a round in registers, so
-// that their loads are in flight together (with 2 / 4 / 6 / 8: 138 / 109 / 111 /
-// 106 us); a cluster of CTAs shares a row only where rows are few.
+// with 8 alternatives, 537 MB, in 106 us (5.0 TB/s; a tenth less without
+// alternatives), where it issues 69 million instructions, 55 us of issue slots;
+// 8 rows of 32000 in 7.2 us.  A thread holds kVecs 16-byte vectors of a round in
+// registers, so that their loads are in flight together (with 2 / 4 / 6 in the
+// place of 8 it took 30 / 3 / 5 % longer); a cluster of CTAs shares a row only
+// where rows are few.
 //
 // Alternatives: a thread notes its vectors' maxima.  After kEpoch rounds the n-th
 // largest of 32 sets' maxima so far (the threads of a lane number) is a bound
 // that n logits reach, and hardly more than n do: the few vectors that reach it
 // are read again, from the L2, and their logits that do go to a list, whose
-// best n by (value, lowest index) are found by counting.  Where too many reach
-// it (rows of equal logits), the n are searched one after another instead.
+// best n by (value, lowest index) are found by counting.  Where more than kList
+// have reached it, the n are searched one after another instead, each with a
+// read of the row: rows of equal or rising logits, and with 32 alternatives, of
+// which about 130 places go in the first look and 130 / k in the k-th, ordinary
+// ones of large vocabularies (of normal fp32 logits by one CTA a row 1 % of the
+// rows at 131072, 10 to 15 % at 262144, nine in ten at a million; none of them
+// with 20 alternatives).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprob_kernel(const LogprobP
 template <typename E>
 cudaError_t launch_typed(const LogprobParams& P, cudaStream_t s) {
   // CTAs a row: more than one only while the rows leave places for CTAs idle and every thread keeps a vector.  A CTA's
-  // fixed times weigh more than uneven ends: 2047 rows of 131072 take 110 / 119 / 136 / 194 us with 1 / 2 / 4 / 8.
+  // fixed times weigh more than uneven ends: 2047 rows of 131072 took 8 / 24 / 76 % longer with 2 / 4 / 8 than with 1.
   int parts = 1;
   while (parts < kMaxCluster && (long long)P.T * parts < kCtas * sm_count() && P.V > parts * kThreads * Vec<E>::N) parts *= 2;
   const Launch at(dim3(P.T * parts), kThreads, 0, s, parts);

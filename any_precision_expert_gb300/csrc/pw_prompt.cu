@@ -15,11 +15,18 @@
 // before they go to the products, takes such values out and the rows that see
 // them get them back at the end.
 //
-// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 379 us (1450
-// TFLOP/s of what its rows see): 2750 cycles a tile pair, whose MMAs take 2048,
-// and some 6 k cycles a piece for its first scores, last sums and their way
-// out.  24 sequences of up to 1111 tokens, 44 heads of 64 on 4: 151 us; there a
-// piece has 3.4 key tiles on average, so those times are half of it.
+// Weights are one number of the heads' type each, which the product wants: two,
+// as the 4-bit kernel takes, would double that product, half of what bounds
+// heads of 128.  Their rounding makes the errors 1.2 to 1.35 times those of
+// rounding the output alone.
+//
+// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 379 to 413 us by
+// the box's clock (1450 to 1330 TFLOP/s of what its rows see): 2750 cycles a
+// tile pair, whose MMAs take 2048, and some 6 k cycles a piece for its first
+// scores, last sums and their way out.  24 sequences of up to 1111 tokens, 44
+// heads of 64 on 4: 150 us; there a piece has 3.4 key tiles on average, so those
+// times are half of it, and no pipe is full (tensor 25 %, exponentials 25 %, 1.5
+// instructions a cycle).
 //
 // Work grows with a tile's place in its sequence, so the CTAs take the tiles by
 // falling place (a counting sort over the sequences' lengths, which every CTA
@@ -39,15 +46,15 @@ constexpr int kTile = 128;           // keys a tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 // Registers: launched with 168 a thread; the softmax warps take what the other four give up (256 * 216 + 128 * 72 = 384 * 168;
-// with 208 and 88 a document of 8191 tokens takes 390 us instead of 385).
+// with 208 and 88 a document of 8191 tokens took 1 % longer).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-// Parts in which a tile's weights are handed over: with 1 / 2 / 4 the document takes 385 / 401 / 450 us, 24 prompts 157 / 167 / 187.
+// Parts in which a tile's weights are handed over: with 2 / 4 the document took 4 / 17 % longer, 24 prompts 6 / 19 %.
 constexpr int kParts = 1;
 constexpr float kGrow = 8.f;         // sums are rescaled when a row's maximum has grown by 2^kGrow
 constexpr int kBuckets = 512;
 // The softmax of heads of 128 meets the other row tile's products if the warpgroups take turns; with heads of 64, whose
-// products are half as long, the two do better side by side (24 prompts of up to 1111 tokens 180 -> 157 us; a document with
-// heads of 128 and no turns 479 us, with turns 401).
+// products are half as long, the two do better side by side (24 prompts of up to 1111 tokens took 15 % longer with turns, a
+// document with heads of 128 19 % longer without).
 template <int D>
 constexpr bool kTurns = D == 128;
 

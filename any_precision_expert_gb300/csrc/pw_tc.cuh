@@ -284,6 +284,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(mbar)
       : "memory");
 }
+
 // ---- of the attention kernels ----
 
 // fp16 or bf16 operands of 128 x n, B with its outer dimension contiguous or not.
