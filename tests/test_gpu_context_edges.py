@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import any_precision_expert_gb300 as pw
-from test_gpu_context import DEVICE_CHECK, TYPES, Case4, check_prompt, held, ints, prompt_case, run_prompt
+from test_gpu_context import DEVICE_CHECK, TYPES, Cached, Case4, check_logprobs, check_prompt, held, ints, prompt_case, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +244,92 @@ def test_prompt_places_in_buckets_of_several_tiles(hq, hk, T, D):
     a, z = off[5], off[9]
     some = [x - a for x in off[5:10]]
     check_prompt(q[a:z, :2], k[a:z, :1], v[a:z, :1], some, out[a:z, :2], lse[a:z, :2])
+
+
+# ---- layouts and streams ----------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["projection", "heads first"])
+@pytest.mark.parametrize("D,ql", [(64, 3), (128, 1)])
+def test_queries_and_outputs_of_other_layouts(D, ql, layout):
+    rng = np.random.default_rng(D)
+    lens, hq, hk, page = [70, 5, 200], 12, 3, 16
+    c = Case4(rng, lens, hq, hk, D, page, torch.bfloat16, ql)
+    f = Cached(rng, lens, hq, hk, D, page, torch.bfloat16)
+    B = len(lens)
+    T = B * ql
+
+    def other(x):  # [T, hq, D] with the same values
+        if layout == "heads first":
+            return x.transpose(0, 1).contiguous().transpose(0, 1)
+        wide = torch.full((T, (hq + 2 * hk) * D + 8), 7.0, dtype=x.dtype, device="cuda")
+        y = wide[:, 8:8 + hq * D].view(T, hq, D)
+        y.copy_(x)
+        return y
+
+    ref, lse = c.run()
+    q, out = other(c.q), other(torch.zeros_like(c.q))
+    ws = torch.full((c.kv.attend_workspace_size(B, ql),), 255, dtype=torch.uint8, device="cuda")
+    c.kv.attend(q, ints(c.table), ints(lens), out, ws, q_len=ql)
+    assert torch.equal(out, ref) and q.stride() == out.stride() != ref.stride()
+    m0, m1 = (torch.zeros(B, f.table.shape[1] * page, device="cuda") for _ in range(2))
+    f.kv.weigh(c.q, ints(f.table), ints(lens), lse, m0, q_len=ql)
+    f.kv.weigh(q, ints(f.table), ints(lens), lse, m1, q_len=ql)
+    assert torch.equal(m0, m1) and m0[2, :200].sum() > 0
+    if layout == "projection":
+        assert (out.as_strided((T, 8), (out.stride(0), 1), 0) == 7).all()  # in front of the heads
+
+
+def test_every_call_on_a_side_stream_and_in_a_graph_of_its_own():
+    rng = np.random.default_rng(2)
+    lens, hq, hk, D, page = [90, 33], 8, 2, 64, 16
+    c = Case4(rng, lens, hq, hk, D, page, torch.float16)
+    f = Cached(rng, lens, hq, hk, D, page, torch.float16)
+    x = torch.from_numpy(rng.standard_normal((3, 40000)).astype(np.float32)).cuda()
+    tokens = ints([5, 39999, -1])
+    table4, table, dl = ints(c.table), ints(f.table), ints(lens)
+    kept_k, kept_v = f.k.clone(), f.v.clone()
+
+    def buffers():
+        return dict(out=torch.full_like(c.q, 7.0), lse=torch.full((2, hq), 7.0, device="cuda"),
+                    mass=torch.zeros(2, f.table.shape[1] * page, device="cuda"), lens=ints([0, 0]), kept=ints(np.zeros((2, 20))),
+                    lp=torch.full((3,), 7.0, device="cuda"), ent=torch.full((3,), 7.0, device="cuda"),
+                    ids=ints(np.zeros((3, 9))), tops=torch.full((3, 9), 7.0, device="cuda"),
+                    ko=torch.full_like(c.k, 9.0), vo=torch.full_like(c.v, 9.0),
+                    ws4=torch.empty(c.kv.attend_workspace_size(2), dtype=torch.uint8, device="cuda"),
+                    wse=torch.empty(f.kv.evict_workspace_size(2, 20), dtype=torch.uint8, device="cuda"))
+
+    slots = torch.arange(len(c.k), dtype=torch.int32, device="cuda")
+
+    def step(b, stream=None):
+        c.kv.append(c.k, c.v, slots, stream=stream)
+        c.kv.load(slots, b["ko"], b["vo"], stream=stream)
+        c.kv.attend(c.q, table4, dl, b["out"], b["ws4"], lse=b["lse"], stream=stream)
+        f.kv.weigh(c.q, table, dl, b["lse"], b["mass"], decay=0.0, stream=stream)
+        f.kv.evict(table, dl, b["mass"], 20, b["wse"], recent=3, new_lens=b["lens"], kept=b["kept"], stream=stream)
+        pw.token_logprobs(x, tokens, b["lp"], entropy=b["ent"], top_ids=b["ids"], top_logprobs=b["tops"], stream=stream)
+
+    def restore():
+        f.k.copy_(kept_k), f.v.copy_(kept_v)
+        torch.cuda.synchronize()
+
+    ref = buffers()
+    step(ref)
+    torch.cuda.synchronize()
+    keys = f.k.clone()
+    names = [k for k in ref if not k.startswith("ws")]
+    b = buffers()
+    restore()
+    s = torch.cuda.Stream()
+    step(b, s)
+    s.synchronize()
+    assert all(torch.equal(b[k], ref[k]) for k in names) and torch.equal(f.k, keys)
+    b = buffers()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(b)
+    for _ in range(2):
+        restore()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(b[k], ref[k]) for k in names) and torch.equal(f.k, keys)
+    check_logprobs(x, [5, 39999, -1], 9)
