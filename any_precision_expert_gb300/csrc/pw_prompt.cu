@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
       const int sure0 = cur.row0 + 1;                 // keys that every row of the piece sees
       const int sure = first + 1;                     // ... of the row tile
       const int tiles = tiles_of(cur, i, tokens);
-      const bool two = active(cur, 1, tokens);
+      const bool two = active(cur, 1, tokens), in = row_tok < tokens && first + row_tok < cur.nrows;
       bool odd = false;
       float m = -CUDART_INF_F;
       float2 l = make_float2(0.f, 0.f);
@@ -460,11 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
         }
         top = fmaxf(max3(top, t1, t2), t3);
         top = top == -CUDART_INF_F ? top : top * scale2 - kShift;
+        // A row's reference moves with its own maximum alone: rows of the warp that see other keys, belong to the next
+        // sequence or to nobody (whose queries are what shared memory holds) leave its bits as they are.
+        const bool grew = in && top > m + kGrow;
         if (t == 0) {
           m = top;
-        } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
-          const float mm = fmaxf(m, top), f = mm == -CUDART_INF_F ? 1.f : ex2(m - mm);
-          m = mm;
+        } else if (__any_sync(0xffffffffu, grew)) {
+          const float f = grew ? ex2(m - top) : 1.f;
+          if (grew) m = top;
           l.x *= f, l.y *= f;
           // these scores were issued behind the last product into O: it is done
 #pragma unroll 1
@@ -515,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptParams 
       ok = __all_sync(0xffffffffu, mbar_wait(o_done + 8 * i, done++ & 1, abort_flag, err));
       if (!ok) break;
       tc_fence_after();
-      const bool in = row_tok < tokens && first + row_tok < cur.nrows;
       const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : __frcp_rn(sum);
       E* row = static_cast<E*>(P.out.ptr) + (long long)(cur.tok0 + tok) * P.out.token_stride +
                (long long)(cur.head * P.G + row_head) * P.out.head_stride;

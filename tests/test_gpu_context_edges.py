@@ -333,3 +333,44 @@ def test_every_call_on_a_side_stream_and_in_a_graph_of_its_own():
         torch.cuda.synchronize()
         assert all(torch.equal(b[k], ref[k]) for k in names) and torch.equal(f.k, keys)
     check_logprobs(x, [5, 39999, -1], 9)
+
+
+# ---- a row's bits are its own -----------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(11, 1), (44, 4), (3, 1), (100, 1)])
+def test_prompt_repeats_itself_whatever_ran_before(hq, hk, D):
+    # groups that leave rows of a tile to nobody: what shared memory holds there comes from earlier kernels
+    rng = np.random.default_rng(hq)
+    off = [0, 700, 701, 950]
+    q, k, v = prompt_case(rng, off[-1], hq, hk, D, torch.float16)
+    ref, rl, _ = run_prompt(q, k, v, off)
+    for scale in (1e-3, 30.0, 3000.0):
+        for d in (64, 128):
+            other = [torch.from_numpy(rng.standard_normal((600, h, d)) * scale).half().cuda() for h in (16, 2, 2)]
+            run_prompt(*other, [0, 600])
+        out, lse, _ = run_prompt(q, k, v, off)
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,D", [(4, 1, 64), (2, 2, 128), (11, 1, 128), (1, 1, 64)])
+def test_prompt_rows_do_not_change_with_what_they_do_not_see(hq, hk, D, dt):
+    # large queries and keys of later tokens, and of the next sequence, against the same rows with small ones
+    rng = np.random.default_rng(D + hq)
+    off = [0, 610, 850]
+    q, k, v = prompt_case(rng, off[-1], hq, hk, D, TYPES[dt])
+    ref, rl, _ = run_prompt(q, k, v, off)
+    for t in (1, 129, 300, 301, 520, 609):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        q2[t:] *= 20
+        k2[t:] *= 20
+        out, lse, _ = run_prompt(q2, k2, v2, off)
+        assert torch.equal(out[:t], ref[:t]) and torch.equal(lse[:t], rl[:t]), t
+        out, lse, _ = run_prompt(q2[:t], k2[:t], v2[:t], [0, t])
+        assert torch.equal(out, ref[:t]) and torch.equal(lse, rl[:t]), t
+    q2, k2 = q.clone(), k.clone()
+    q2[610:] *= 50
+    k2[610:] *= 50
+    out, lse, _ = run_prompt(q2, k2, v, off)
+    assert torch.equal(out[:610], ref[:610]) and torch.equal(lse[:610], rl[:610])
