@@ -565,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
               top[i & 1] = fmaxf(top[i & 1], s[j][h][i]);
             }
           // the sums' reference moves when a lane's maximum has passed it by 2^kGrow (weights stay below 2^(kShift + kGrow),
-          // which fp16 holds, and nothing is lost: it cancels in o / l), and then to the row's maximum
+          // which fp16 holds, and nothing is lost: it cancels in o / l), and then to the row's maximum; rows that have not
+          // grown stay, so that a query's bits do not go by keys that only the later ones beside it see
           float ref[2];
           bool grew = false;
 #pragma unroll
@@ -579,11 +580,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::CTAS))
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], x));
-              top[k] = fmaxf(top[k] - kShift, m[j][k]);
-              ref[k] = top[k] == -CUDART_INF_F ? 0.f : top[k];
-              f[k] = ex2(m[j][k] - ref[k]);
+              top[k] -= kShift;
+              f[k] = 1.f;
+              if (top[k] > m[j][k] + kGrow) {
+                f[k] = ex2(m[j][k] - top[k]);
+                m[j][k] = ref[k] = top[k];
+              }
               l[j][k] *= f[k];
-              m[j][k] = top[k];
             }
 #pragma unroll
             for (int i = 0; i < MV; ++i) {

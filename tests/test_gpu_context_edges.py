@@ -374,3 +374,39 @@ def test_prompt_rows_do_not_change_with_what_they_do_not_see(hq, hk, D, dt):
     k2[610:] *= 50
     out, lse, _ = run_prompt(q2, k2, v, off)
     assert torch.equal(out[:610], ref[:610]) and torch.equal(lse[:610], rl[:610])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,D,ql", [(4, 2, 64, 3), (8, 1, 128, 5), (2, 1, 128, 2), (16, 4, 64, 4)])
+def test_four_bit_queries_do_not_change_with_what_they_do_not_see(hq, hk, D, ql, dt):
+    # the last token's keys and queries large, against the earlier queries' bits with small ones
+    page = 16
+    lens = [ql + 3, 40, 130, 257, 700]
+    c = Case4(np.random.default_rng(hq), lens, hq, hk, D, page, TYPES[dt], ql, qscale=1.0)
+    ref, lse = c.run()
+    n4 = torch.arange(len(c.k), dtype=torch.int32, device="cuda")
+    for size in (20.0, 200.0):
+        k, q = c.k.clone(), c.q.clone()
+        for b, n in enumerate(lens):
+            k[int(c.table[b][(n - 1) // page]) * page + (n - 1) % page] *= size
+            c.q[(b + 1) * ql - 1] *= size
+        c.kv.append(k, c.v, n4)
+        out, l2 = c.run()
+        c.q.copy_(q)
+        for b in range(len(lens)):
+            a, z = b * ql, (b + 1) * ql - 1
+            assert torch.equal(out[a:z], ref[a:z]) and torch.equal(l2[a:z], lse[a:z]), b
+
+
+def test_four_bit_attention_repeats_itself_whatever_ran_before():
+    rng = np.random.default_rng(1)
+    for hq, hk, D, ql in ((11, 1, 64, 1), (44, 4, 64, 3), (5, 1, 128, 1), (32, 8, 128, 2), (16, 1, 128, 5)):
+        c = Case4(rng, [int(x) for x in rng.integers(0, 900, 20)], hq, hk, D, 16, torch.float16, ql)
+        ref, lse = c.run()
+        for scale in (1e-3, 3000.0):
+            x = [torch.from_numpy(rng.standard_normal((600, h, D)) * scale).half().cuda() for h in (16, 2, 2)]
+            run_prompt(*x, [0, 600])
+            o = Case4(rng, [300, 70], 8, 2, D, 32, torch.float16, 2, qscale=scale)
+            o.run()
+            out, l2 = c.run()
+            assert torch.equal(out, ref) and torch.equal(l2, lse)
