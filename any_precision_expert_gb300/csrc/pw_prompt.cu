@@ -24,7 +24,7 @@
 // the box's clock (1450 to 1330 TFLOP/s of what its rows see): 2750 cycles a
 // tile pair, whose MMAs take 2048, and some 6 k cycles a piece for its first
 // scores, last sums and their way out.  24 sequences of up to 1111 tokens, 44
-// heads of 64 on 4: 150 us; there a piece has 3.4 key tiles on average, so those
+// heads of 64 on 4: 147 us; there a piece has 3.4 key tiles on average, so those
 // times are half of it, and no pipe is full (tensor 25 %, exponentials 25 %, 1.5
 // instructions a cycle).
 //
