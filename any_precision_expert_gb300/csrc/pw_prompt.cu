@@ -20,8 +20,8 @@
 // heads of 128.  Their rounding makes the errors 1.2 to 1.35 times those of
 // rounding the output alone.
 //
-// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 379 to 413 us by
-// the box's clock (1450 to 1330 TFLOP/s of what its rows see): 2750 cycles a
+// Measured: one sequence of 8191 tokens, 32 heads of 128 on 8, 379 to 413 us as
+// the SM clock goes (1450 to 1330 TFLOP/s of what its rows see): 2750 cycles a
 // tile pair, whose MMAs take 2048, and some 6 k cycles a piece for its first
 // scores, last sums and their way out.  24 sequences of up to 1111 tokens, 44
 // heads of 64 on 4: 147 us; there a piece has 3.4 key tiles on average, so those
